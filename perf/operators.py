@@ -255,7 +255,7 @@ def _plan(s):
     unit_end = units.cumsum(0)
     mids = (units - 2).clamp(min=0)
     mid = mids.cumsum(0) - mids
-    used = torch.where(live, seal_end, 0).amax().reshape(1)
+    used = torch.where(live & (seals > 0), seal_end, 0).amax().reshape(1)
     u = torch.arange(max_units(T, R), device=dev)
     r = torch.searchsorted(unit_end, u, right=True)
     there = r < R
