@@ -11,9 +11,10 @@ first use; there is no fallback implementation.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
-from typing import Optional, Tuple
+from typing import Any, NamedTuple, Optional, Tuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "lib", "libjetfp8.so")
@@ -22,7 +23,10 @@ OK, ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_MODE, ERR_HIP, ERR_VALUE = 0, -1, -2, -3
 ROWS_1x128, COLS_128x1_T, BLOCKS_128x128, BLOCKS_128x128_FRAG = 0, 1, 2, 3
 EXPORTED = ("jetfp8_quantize", "jetfp8_quantize_dual", "jetfp8_requantize_cols_t", "jetfp8_rmsnorm_quantize",
             "jetfp8_swiglu_quantize", "jetfp8_gemm_fwd", "jetfp8_gemm_fwd_frag", "jetfp8_gemm_dgrad",
-            "jetfp8_gemm_wgrad", "jetfp8_status_string", "jetfp8_version")
+            "jetfp8_gemm_wgrad", "jetfp8_kv_max_units", "jetfp8_kv_plan", "jetfp8_kv_append", "jetfp8_attention",
+            "jetfp8_attention_workspace", "jetfp8_status_string", "jetfp8_version")
+KV_BLOCK, KV_UNIT_WORDS = 64, 8
+KV_OK, KV_BAD_LENGTH, KV_NO_ROWS, KV_NO_BLOCK = 0, 1, 2, 4
 
 _lib = None
 
@@ -56,6 +60,17 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         f = getattr(L, name)
         f.restype = c_int
         f.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, vp]
+    L.jetfp8_kv_max_units.restype = i64
+    L.jetfp8_kv_max_units.argtypes = [i64, i64]
+    L.jetfp8_kv_plan.restype = c_int
+    L.jetfp8_kv_plan.argtypes = [vp, vp, vp, i64, vp, vp, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp]
+    L.jetfp8_kv_append.restype = c_int
+    L.jetfp8_kv_append.argtypes = [vp, i64, vp, i64, i64, vp, i64, i64, i64, vp, vp, i64, vp, i64, vp]
+    L.jetfp8_attention.restype = c_int
+    L.jetfp8_attention.argtypes = [vp, i64, i64, vp, i64, vp, i64, i64, vp, vp, i64, vp, i64, i64, i64, i64, i64, i64,
+                                   ctypes.c_float, vp, vp, vp, vp, i64, vp]
+    L.jetfp8_attention_workspace.restype = i64
+    L.jetfp8_attention_workspace.argtypes = [i64] * 6
     L.jetfp8_status_string.restype = ctypes.c_char_p
     L.jetfp8_status_string.argtypes = [c_int]
     L.jetfp8_version.restype = c_int
@@ -268,6 +283,136 @@ def jetfp8_gemm_wgrad(dyqT, dysT, xqT, xsT, dw_bf16, M: int, N: int, K: int, str
                                                      int(M), int(N), int(K), _stream(stream)))
 
 
+class _on:
+    """The launch of a call: its tensors' device made current, and the stream to enqueue on (the current stream of that
+    device unless one is given)."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.guard = None
+        if device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(device)
+        self.stream = stream
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return _stream(self.stream)
+
+    def __exit__(self, *error):
+        if self.guard is not None:
+            self.guard.__exit__(*error)
+
+
+def _rows(t, shape, name, device=None):
+    """A bf16 tensor [tokens, heads, head_dim] whose rows lie any distance apart (columns of a fused projection, say),
+    each of them contiguous: its pointer and the distance in elements."""
+    torch = _torch_mod()
+    _need(t, shape, torch.bfloat16, name, device)
+    T, H, D = shape
+    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return t.data_ptr(), t.stride(0) if T > 1 else H * D
+
+
+def kv_max_units(tokens: int, requests: int) -> int:
+    n = load_library().jetfp8_kv_max_units(int(tokens), int(requests))
+    if n < 0:
+        _check("jetfp8_kv_max_units", n)
+    return n
+
+
+def jetfp8_kv_plan(state, new_lens, free_blocks, num_free: int, free_head, block_table, max_blocks: int, requests: int,
+                   tokens: int, max_new: int, next_state, next_free, status, units, slots=None, stream=None) -> None:
+    L = load_library()
+    torch = _torch_mod()
+    i32, R, T, F, W = torch.int32, int(requests), int(tokens), int(num_free), int(max_blocks)
+    n = L.jetfp8_kv_max_units(T, R)
+    if n >= 0 and F >= 0 and W >= 1:
+        _need(state, (R, 2), i32, "state")
+        dev = state.device
+        _need(new_lens, (R,), i32, "new_lens", dev)
+        _need(free_head, (1,), i32, "free_head", dev)
+        if F:
+            _need(free_blocks, (F,), i32, "free_blocks", dev)
+        _need(block_table, (R, W), i32, "block_table", dev)
+        _need(next_state, (R, 2), i32, "next_state", dev)
+        _need(next_free, (1,), i32, "next_free", dev)
+        _need(status, (R,), i32, "status", dev)
+        _need(units, (n, KV_UNIT_WORDS), i32, "units", dev)
+        if slots is not None:
+            _need(slots, (T,), torch.int64, "slots", dev)
+    with _on(state.device, stream) as st:
+        st = L.jetfp8_kv_plan(_ptr(state), _ptr(new_lens), _ptr(free_blocks) if F else None, F, _ptr(free_head),
+                              _ptr(block_table), W, R, T, int(max_new), _ptr(next_state), _ptr(next_free),
+                              _ptr(status), _ptr(units), _ptr(slots), st)
+    _check("jetfp8_kv_plan", st)
+
+
+def _kv_buffers(units, codes, scales, recent, kv_heads, head_dim):
+    """Checks a layer's cache and the units; their counts (units, physical blocks, recent blocks)."""
+    bf, u8, f32 = _bf16_u8_f32()
+    n = kv_heads, 2, KV_BLOCK * head_dim
+    counts = tuple(t.shape[0] if getattr(t, "ndim", 0) else 0 for t in (units, codes, recent))
+    _need(codes, (counts[1],) + n, u8, "codes")
+    dev = codes.device
+    _need(units, (counts[0], KV_UNIT_WORDS), _torch_mod().int32, "units", dev)
+    _need(scales, (counts[1],) + n[:2], f32, "scales", dev)
+    _need(recent, (counts[2],) + n, bf, "recent", dev)
+    return counts
+
+
+def jetfp8_kv_append(k_bf16, v_bf16, units, codes, scales, recent_bf16, tokens: int, kv_heads: int, head_dim: int,
+                     stream=None) -> None:
+    L = load_library()
+    T, H, D = int(tokens), int(kv_heads), int(head_dim)
+    num_units, blocks, recent_blocks = _kv_buffers(units, codes, scales, recent_bf16, H, D)
+    k, ldk = _rows(k_bf16, (T, H, D), "k", codes.device)
+    v, ldv = _rows(v_bf16, (T, H, D), "v", codes.device)
+    with _on(codes.device, stream) as st:
+        st = L.jetfp8_kv_append(k, ldk, v, ldv, T, _ptr(units), num_units, H, D, _ptr(codes), _ptr(scales), blocks,
+                                _ptr(recent_bf16), recent_blocks, st)
+    _check("jetfp8_kv_append", st)
+
+
+def attention_workspace(num_units: int, max_new: int, max_seq: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    """Bytes of workspace that jetfp8_attention needs for these sizes."""
+    n = load_library().jetfp8_attention_workspace(int(num_units), int(max_new), int(max_seq), int(q_heads),
+                                                  int(kv_heads), int(head_dim))
+    if n < 0:
+        _check("jetfp8_attention_workspace", n)
+    return n
+
+
+def jetfp8_attention(q_bf16, units, block_table, codes, scales, recent_bf16, tokens: int, max_new: int, max_seq: int,
+                     q_heads: int, kv_heads: int, head_dim: int, softmax_scale: float, dst_o_bf16=None, dst_codes=None,
+                     dst_scales=None, workspace=None, stream=None) -> None:
+    L = load_library()
+    bf, u8, f32 = _bf16_u8_f32()
+    T, Hq, H, D = int(tokens), int(q_heads), int(kv_heads), int(head_dim)
+    num_units, blocks, recent_blocks = _kv_buffers(units, codes, scales, recent_bf16, H, D)
+    dev = codes.device
+    q, ldq = _rows(q_bf16, (T, Hq, D), "q", dev)
+    requests, width = block_table.shape if getattr(block_table, "ndim", 0) == 2 else (0, 0)
+    _need(block_table, (requests, width), _torch_mod().int32, "block_table", dev)
+    if dst_o_bf16 is not None:
+        _need(dst_o_bf16, (T, Hq, D), bf, "dst_o_bf16", dev)
+    if dst_codes is not None:
+        _need(dst_codes, (T, Hq * D), u8, "dst_codes", dev)
+    if dst_scales is not None:
+        _need(dst_scales, (Hq * D // 128, T), f32, "dst_scales", dev)
+    size = 0
+    if workspace is not None:
+        _need(workspace, workspace.shape, None, "workspace", dev)
+        size = workspace.numel() * workspace.element_size()
+    with _on(dev, stream) as st:
+        st = L.jetfp8_attention(q, ldq, T, _ptr(units), num_units, _ptr(block_table), requests, width, _ptr(codes),
+                                _ptr(scales), blocks, _ptr(recent_bf16), recent_blocks, int(max_new), int(max_seq), Hq,
+                                H, D, float(softmax_scale), _ptr(dst_o_bf16), _ptr(dst_codes), _ptr(dst_scales),
+                                _ptr(workspace), size, st)
+    _check("jetfp8_attention", st)
+
+
 # ------------------------------------------------------------------------------------------------
 # Allocating helpers (torch tensors in, torch tensors out).
 # ------------------------------------------------------------------------------------------------
@@ -420,3 +565,79 @@ def linear_backward(dy, x, wqT, ws, stream=None):
     xqT, xsT = quantize_cols_t(x, stream)
     dw = gemm_wgrad(dyqT, dysT, xqT, xsT, stream)
     return dx, dw
+
+
+def _memory_of(stream, device):
+    """Where a helper allocates: the memory of the stream that the call runs on, so that what the helper frees when it
+    returns (a workspace) is handed out again only behind the call."""
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+class KVPlan(NamedTuple):
+    """A planned step: see jetfp8_kv_plan in include/jetfp8.h."""
+    next_state: Any     # int32 [R, 2], the next step's state
+    next_free: Any      # int32 [1], the next step's free_head
+    status: Any         # int32 [R]: KV_OK, KV_BAD_LENGTH, KV_NO_ROWS or KV_NO_BLOCK
+    units: Any          # int32 [kv_max_units(tokens, R), KV_UNIT_WORDS]
+    slots: Any          # int64 [tokens], or None
+
+
+def kv_cache(num_blocks: int, requests: int, tokens: int, kv_heads: int, head_dim: int, device="cuda"):
+    """One layer's key/value cache for up to `requests` requests and calls of up to `tokens` rows: codes uint8
+    [num_blocks, H, 2, 64 D], scales fp32 [num_blocks, H, 2], recent bf16 [2 requests + tokens / 64, H, 2, 64 D]."""
+    import torch
+    n = kv_heads, 2, KV_BLOCK * head_dim
+    return (torch.zeros((num_blocks,) + n, dtype=torch.uint8, device=device),
+            torch.zeros((num_blocks,) + n[:2], dtype=torch.float32, device=device),
+            torch.zeros((2 * requests + tokens // KV_BLOCK,) + n, dtype=torch.bfloat16, device=device))
+
+
+def kv_plan(state, new_lens, free_blocks, free_head, block_table, tokens: int, max_new: int, slot_map: bool = False,
+            stream=None) -> KVPlan:
+    """Plans a step of `tokens` rows: state int32 [R, 2], new_lens int32 [R] (none above max_new), free_blocks int32
+    [F] with free_head int32 [1] of them handed out, block_table int32 [R, max_blocks] (entries of the blocks that
+    the step completes are written)."""
+    import torch
+    R, W = block_table.shape
+    dev = block_table.device
+    new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=dev)
+    with _memory_of(stream, dev):
+        p = KVPlan(new(R, 2), new(1), new(R), new(kv_max_units(tokens, R), KV_UNIT_WORDS),
+                   torch.empty((tokens,), dtype=torch.int64, device=dev) if slot_map else None)
+    jetfp8_kv_plan(state, new_lens, free_blocks, free_blocks.shape[0], free_head, block_table, W, R, tokens, max_new,
+                   p.next_state, p.next_free, p.status, p.units, p.slots, stream)
+    return p
+
+
+def kv_append(k, v, units, codes, scales, recent, stream=None) -> None:
+    """New keys and values into a layer's cache: k, v bf16 [T, H, D] (rows may be columns of a wider matrix)."""
+    T, H, D = k.shape
+    jetfp8_kv_append(k, v, units, codes, scales, recent, T, H, D, stream)
+
+
+def attention(q, units, block_table, codes, scales, recent, max_new: int, max_seq: int, softmax_scale=None,
+              quantize: bool = False, return_o: bool = True, workspace=None, stream=None):
+    """Causal attention of a step's new tokens, after kv_append: q bf16 [T, Hq, D] -> bf16 [T, Hq, D]; with quantize
+    (D = 128) -> (codes [T, Hq * D], scales [Hq, T]) and, with return_o, the bf16 matrix as well.  softmax_scale:
+    1 / sqrt(D) unless given.  Rows that belong to no unit are left unwritten."""
+    import torch
+    T, Hq, D = q.shape
+    H = codes.shape[1]
+    dev = q.device
+    with _memory_of(stream, dev):
+        if workspace is None:
+            size = attention_workspace(units.shape[0], max_new, max_seq, Hq, H, D)
+            workspace = torch.empty((size,), dtype=torch.uint8, device=dev) if size else None
+        o = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev) if return_o or not quantize else None
+        c = torch.empty((T, Hq * D), dtype=torch.uint8, device=dev) if quantize else None
+        s = torch.empty((Hq * D // 128, T), dtype=torch.float32, device=dev) if quantize else None
+    jetfp8_attention(q, units, block_table, codes, scales, recent, T, max_new, max_seq, Hq, H, D,
+                     D ** -0.5 if softmax_scale is None else softmax_scale, o, c, s, workspace, stream)
+    if not quantize:
+        return o
+    return (c, s, o) if return_o else (c, s)

@@ -33,11 +33,29 @@ int check_gemm_extent(int64_t I, int64_t J, int64_t Kc) {
     return JETFP8_OK;
 }
 
+// Sizes of the key/value cache that append and attention share.
+bool kv_dims_ok(int64_t tokens, int64_t num_units, int64_t kv_heads, int64_t head_dim, int64_t num_blocks,
+                int64_t recent_blocks) {
+    return dim_ok(tokens) && dim_ok(num_units) && dim_ok(kv_heads) && (head_dim == 64 || head_dim == 128) &&
+           dim_ok(num_blocks) && dim_ok(recent_blocks) && dim_ok(2 * kv_heads * num_units);
+}
+
+bool row_pitch_ok(int64_t ld, int64_t heads, int64_t head_dim) {
+    return dim_ok(ld) && ld % 8 == 0 && heads <= ld / head_dim;
+}
+
+bool attention_dims_ok(int64_t num_units, int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads,
+                       int64_t head_dim) {
+    return dim_ok(num_units) && dim_ok(max_new) && dim_ok(max_seq) && dim_ok(q_heads) && dim_ok(kv_heads) &&
+           q_heads % kv_heads == 0 && q_heads <= 65536 && (head_dim == 64 || head_dim == 128) &&
+           jetfp8::attention_fits(num_units, max_new, max_seq, q_heads, kv_heads);
+}
+
 }  // namespace
 
 extern "C" {
 
-int jetfp8_version(void) { return 302; }
+int jetfp8_version(void) { return 400; }
 
 const char* jetfp8_status_string(int status) {
     switch (status) {
@@ -168,6 +186,83 @@ int jetfp8_gemm_wgrad(const uint8_t* dyqT, const float* dysT, const uint8_t* xqT
     if (rc != JETFP8_OK) return rc;
     return hip_status(jetfp8::launch_gemm_row_scaled_b(dyqT, dysT, xqT, xsT, static_cast<uint16_t*>(dw_bf16), N, K, M,
                                                        static_cast<hipStream_t>(stream)));
+}
+
+int64_t jetfp8_kv_max_units(int64_t tokens, int64_t requests) {
+    if (tokens < 1 || tokens > jetfp8::kKvMaxTokens || requests < 1 || requests > jetfp8::kKvMaxRequests)
+        return JETFP8_ERR_SHAPE;
+    return jetfp8::kv_max_units(tokens, requests);
+}
+
+int jetfp8_kv_plan(const int32_t* state, const int32_t* new_lens, const int32_t* free_blocks, int64_t num_free,
+                   const int32_t* free_head, int32_t* block_table, int64_t max_blocks, int64_t requests, int64_t tokens,
+                   int64_t max_new, int32_t* next_state, int32_t* next_free, int32_t* status, int32_t* units,
+                   int64_t* slots, void* stream) {
+    if (!state || !new_lens || !free_head || !block_table || !next_state || !next_free || !status || !units ||
+        (!free_blocks && num_free != 0))
+        return JETFP8_ERR_NULL;
+    if (requests < 1 || requests > jetfp8::kKvMaxRequests || tokens < 1 || tokens > jetfp8::kKvMaxTokens ||
+        !dim_ok(max_new) || !dim_ok(max_blocks) || !dim_ok(JETFP8_KV_BLOCK * max_blocks) || num_free < 0 ||
+        num_free >= kMaxDim)
+        return JETFP8_ERR_SHAPE;
+    if (!aligned16(state) || !aligned16(new_lens) || !aligned16(free_blocks) || !aligned16(free_head) ||
+        !aligned16(block_table) || !aligned16(next_state) || !aligned16(next_free) || !aligned16(status) ||
+        !aligned16(units) || !aligned16(slots))
+        return JETFP8_ERR_ALIGN;
+    return hip_status(jetfp8::launch_kv_plan(state, new_lens, free_blocks, num_free, free_head, block_table, max_blocks,
+                                             requests, tokens, max_new, next_state, next_free, status, units, slots,
+                                             static_cast<hipStream_t>(stream)));
+}
+
+int jetfp8_kv_append(const void* k_bf16, int64_t ldk, const void* v_bf16, int64_t ldv, int64_t tokens,
+                     const int32_t* units, int64_t num_units, int64_t kv_heads, int64_t head_dim, uint8_t* codes,
+                     float* scales, int64_t num_blocks, void* recent_bf16, int64_t recent_blocks, void* stream) {
+    if (!k_bf16 || !v_bf16 || !units || !codes || !scales || !recent_bf16) return JETFP8_ERR_NULL;
+    if (!kv_dims_ok(tokens, num_units, kv_heads, head_dim, num_blocks, recent_blocks) ||
+        !row_pitch_ok(ldk, kv_heads, head_dim) || !row_pitch_ok(ldv, kv_heads, head_dim))
+        return JETFP8_ERR_SHAPE;
+    if (!aligned16(k_bf16) || !aligned16(v_bf16) || !aligned16(units) || !aligned16(codes) || !aligned16(scales) ||
+        !aligned16(recent_bf16))
+        return JETFP8_ERR_ALIGN;
+    return hip_status(jetfp8::launch_kv_append(static_cast<const uint16_t*>(k_bf16), ldk,
+                                               static_cast<const uint16_t*>(v_bf16), ldv, tokens, units, num_units,
+                                               kv_heads, head_dim, codes, scales, num_blocks,
+                                               static_cast<uint16_t*>(recent_bf16), recent_blocks,
+                                               static_cast<hipStream_t>(stream)));
+}
+
+int64_t jetfp8_attention_workspace(int64_t num_units, int64_t max_new, int64_t max_seq, int64_t q_heads,
+                                   int64_t kv_heads, int64_t head_dim) {
+    if (!attention_dims_ok(num_units, max_new, max_seq, q_heads, kv_heads, head_dim)) return JETFP8_ERR_SHAPE;
+    return jetfp8::attention_workspace(num_units, max_new, max_seq, q_heads, kv_heads, head_dim);
+}
+
+int jetfp8_attention(const void* q_bf16, int64_t ldq, int64_t tokens, const int32_t* units, int64_t num_units,
+                     const int32_t* block_table, int64_t requests, int64_t max_blocks, const uint8_t* codes,
+                     const float* scales, int64_t num_blocks, const void* recent_bf16, int64_t recent_blocks,
+                     int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                     float softmax_scale, void* dst_o_bf16, uint8_t* dst_codes, float* dst_scales, void* workspace,
+                     int64_t workspace_bytes, void* stream) {
+    if (!q_bf16 || !units || !block_table || !codes || !scales || !recent_bf16 || (!dst_o_bf16 && !dst_codes) ||
+        !dst_codes != !dst_scales)
+        return JETFP8_ERR_NULL;
+    if (!attention_dims_ok(num_units, max_new, max_seq, q_heads, kv_heads, head_dim) ||
+        !kv_dims_ok(tokens, num_units, kv_heads, head_dim, num_blocks, recent_blocks) || !dim_ok(requests) ||
+        !dim_ok(max_blocks) || !row_pitch_ok(ldq, q_heads, head_dim) || (dst_codes && head_dim != 128))
+        return JETFP8_ERR_SHAPE;
+    if (!(softmax_scale > 0.0f && softmax_scale <= FLT_MAX)) return JETFP8_ERR_VALUE;
+    const int64_t need = jetfp8::attention_workspace(num_units, max_new, max_seq, q_heads, kv_heads, head_dim);
+    if (need > 0 && !workspace) return JETFP8_ERR_NULL;
+    if (need > workspace_bytes) return JETFP8_ERR_SHAPE;
+    if (!aligned16(q_bf16) || !aligned16(units) || !aligned16(block_table) || !aligned16(codes) || !aligned16(scales) ||
+        !aligned16(recent_bf16) || !aligned16(dst_o_bf16) || !aligned16(dst_codes) || !aligned16(dst_scales) ||
+        !aligned16(workspace))
+        return JETFP8_ERR_ALIGN;
+    return hip_status(jetfp8::launch_attention(
+        static_cast<const uint16_t*>(q_bf16), ldq, tokens, units, num_units, block_table, requests, max_blocks, codes,
+        scales, num_blocks, static_cast<const uint16_t*>(recent_bf16), recent_blocks, max_new, max_seq, q_heads,
+        kv_heads, head_dim, softmax_scale, static_cast<uint16_t*>(dst_o_bf16), dst_codes, dst_scales,
+        static_cast<float*>(workspace), static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

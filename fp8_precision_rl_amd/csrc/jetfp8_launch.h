@@ -50,6 +50,27 @@ hipError_t launch_decode_rows(const uint8_t* A, const float* As, const uint8_t* 
 bool gemm_fwd_frag_fits(int64_t M, int64_t K);
 hipError_t launch_gemm_fwd_frag(const uint8_t* xq, const float* xs, const uint8_t* wqf, const float* ws, uint16_t* y,
                                 int64_t M, int64_t N, int64_t K, hipStream_t st);
+// The FP8 key/value cache: a step's plan, the append of its keys and values, and the attention over the cache.
+constexpr int64_t kKvMaxRequests = 4096;            // three prefix sums of a request are kept in LDS
+constexpr int64_t kKvMaxTokens = (int64_t)1 << 19;  // sums over 4096 requests stay below 2^32
+int64_t kv_max_units(int64_t tokens, int64_t requests);
+hipError_t launch_kv_plan(const int32_t* state, const int32_t* new_lens, const int32_t* free_blocks, int64_t num_free,
+                          const int32_t* free_head, int32_t* table, int64_t width, int64_t requests, int64_t tokens,
+                          int64_t max_new, int32_t* next_state, int32_t* next_free, int32_t* status, int32_t* units,
+                          int64_t* slots, hipStream_t st);
+hipError_t launch_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv, int64_t tokens,
+                            const int32_t* units, int64_t num_units, int64_t heads, int64_t D, uint8_t* codes,
+                            float* scales, int64_t num_blocks, uint16_t* recent, int64_t recent_blocks, hipStream_t st);
+// Bytes of workspace, and whether the launch grids hold the call.
+int64_t attention_workspace(int64_t num_units, int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads,
+                            int64_t D);
+bool attention_fits(int64_t num_units, int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads);
+hipError_t launch_attention(const uint16_t* q, int64_t ldq, int64_t tokens, const int32_t* units, int64_t num_units,
+                            const int32_t* table, int64_t requests, int64_t width, const uint8_t* codes,
+                            const float* scales, int64_t num_blocks, const uint16_t* recent, int64_t recent_blocks,
+                            int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads, int64_t D,
+                            float softmax_scale, uint16_t* o, uint8_t* oq, float* os, float* workspace,
+                            hipStream_t st);
 hipError_t launch_gemm_row_scaled_b(const uint8_t* A, const float* As, const uint8_t* B, const float* Bs,
                                     uint16_t* C, int64_t I, int64_t J, int64_t Kc, hipStream_t st);
 

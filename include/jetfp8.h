@@ -177,6 +177,113 @@ int jetfp8_gemm_dgrad(const uint8_t* dyq, const float* dys, const uint8_t* wqT, 
 int jetfp8_gemm_wgrad(const uint8_t* dyqT, const float* dysT, const uint8_t* xqT, const float* xsT,
                       void* dw_bf16, int64_t M, int64_t N, int64_t K, void* stream);
 
+/* ---- Rollout's FP8 key/value cache ---------------------------------------------------------------------------
+ *
+ * Rollout takes most of RL training time, and more of it the longer the generations (Jet-RL explainers, "Enonce du
+ * Probleme"); next to the weights each decode step streams the keys and values of every token so far.  Here they are
+ * kept in the flow's own precision, E4M3 with scale amax / 448 formed when they are written, and by a definition that
+ * does not depend on how a sequence was cut into calls ("Architecture Centrale": rollout and the training forward
+ * share one graph and one quantization):
+ *   - a BLOCK is JETFP8_KV_BLOCK = 64 consecutive tokens of a request (positions 64 j .. 64 j + 63).  A complete block
+ *     is quantized once, from bf16: per kv head one scale for the 64 x D keys and one for the 64 x D values;
+ *   - until it is complete a block is kept in bf16 (a RECENT block);
+ *   - a query at position t reads blocks 0 .. t/64 - 1 as E4M3 and positions 64 (t/64) .. t as bf16.
+ * No token is quantized twice, and no query reads a scale that later tokens had a part in.
+ *
+ * Buffers (kv_heads H, head_dim D = 64 or 128):
+ *   codes  uint8 [num_blocks][H][2][64 D], scales float [num_blocks][H][2]: keys (0) and values (1) of the physical
+ *          blocks.  Complete blocks are never written again, so requests may share them (a prompt that several
+ *          rollouts start from: the same physical ids in several rows of the block table);
+ *   recent bf16 [recent_blocks][H][2][64 D], recent_blocks >= 2 requests + tokens / 64 for the largest call:
+ *          blocks 2 r and 2 r + 1 belong to request r and keep its unfinished block from call to call; those from
+ *          2 requests on hold the blocks that a call's prompts pass through;
+ *   block_table int32 [requests][max_blocks]: physical block of each complete block of each request.
+ * Inside a block the 64 D values are in the order in which the attention kernel's waves read them.  For key n and
+ * channel d:
+ *   codes, keys     ((n/16 * D/64 + d/64) * 64 + d%32/8 * 16 + n%16) * 16 + d%64/32 * 8 + d%8
+ *   codes, values   (d/16 * 64 + n%16/4 * 16 + d%16) * 16 + n/32 * 8 + n%32/16 * 4 + n%4
+ *   recent, keys    ((n/16 * D/32 + d/32) * 64 + d%32/8 * 16 + n%16) * 8 + d%8
+ *   recent, values  ((d/16 * 2 + n/32) * 64 + n%16/4 * 16 + d%16) * 8 + n%32/16 * 4 + n%4
+ *
+ * A step (decode, prefill, or both in one batch) is: plan once, then for every layer append and attention with that
+ * layer's codes, scales and recent.  Every call reads its lengths on the device, so a step can be captured in a graph
+ * and replayed; max_new and max_seq only bound them.
+ */
+#define JETFP8_KV_BLOCK 64
+#define JETFP8_KV_UNIT_WORDS 8
+
+typedef enum {                  /* per-request outcome of jetfp8_kv_plan */
+    JETFP8_KV_OK = 0,
+    JETFP8_KV_BAD_LENGTH = 1,   /* a negative length, more new tokens than max_new, more tokens than the table's row
+                                 * holds, or a recent block other than 0 or 1 */
+    JETFP8_KV_NO_ROWS = 2,      /* its new tokens end behind the call's rows */
+    JETFP8_KV_NO_BLOCK = 4      /* the free list is used up */
+} jetfp8_kv_status;
+
+/* Units that a plan of this many rows and requests may have: min(tokens, (tokens + 62 requests) / 64 + requests). */
+int64_t jetfp8_kv_max_units(int64_t tokens, int64_t requests);
+
+/* Block tables, slot map and work units of a step, on the device, from the requests' lengths.
+ *   state [requests][2] int32: tokens so far, and which of the request's two recent blocks (0 or 1) is being filled;
+ *                              (0, 0) for a new request;
+ *   new_lens [requests] int32: new tokens of each request, 0 .. max_new (0: it has no part in the step).  Their rows
+ *                              follow one another in the call's q, k, v ([tokens] rows; rows behind the last
+ *                              request's are padding and stay untouched);
+ *   free_blocks [num_free] int32 (may be NULL if num_free is 0), free_head [1] int32: ids of unused physical blocks, of
+ *                              which the first *free_head have been handed out.
+ * Writes
+ *   block_table [requests][max_blocks] int32: only the entries of blocks that the step completes, taken from the free
+ *                              list in request order;
+ *   next_state, next_free:     state and free_head after the step (other buffers than the inputs, so that a step can
+ *                              be planned again);
+ *   status [requests] int32:   jetfp8_kv_status.  A request that is refused has no units, its rows stay untouched in
+ *                              later calls, and its state does not change; the others go ahead;
+ *   units [jetfp8_kv_max_units(tokens, requests)][JETFP8_KV_UNIT_WORDS] int32, in request and block order: request,
+ *                              block index, recent block, first row, rows, place of the first row in the block,
+ *                              physical block (-1: not complete after this step), 0; unused records are all -1;
+ *   slots [tokens] int64 (NULL: not written): 64 * physical block + place of every new token whose block the step
+ *                              completes, -1 for the others.
+ * requests <= 4096, tokens <= 2^19, 64 * max_blocks < 2^31. */
+int jetfp8_kv_plan(const int32_t* state, const int32_t* new_lens, const int32_t* free_blocks, int64_t num_free,
+                   const int32_t* free_head, int32_t* block_table, int64_t max_blocks, int64_t requests,
+                   int64_t tokens, int64_t max_new, int32_t* next_state, int32_t* next_free, int32_t* status,
+                   int32_t* units, int64_t* slots, void* stream);
+
+/* New keys and values into a layer's cache: into the recent blocks, and for each block that the step completes its
+ * codes and scales.  k, v: bf16, row t at k + t * ldk elements, [kv_heads][head_dim] contiguous within a row (so they
+ * may be columns of a fused projection); ldk, ldv >= kv_heads * head_dim and multiples of 8.  Repeating the call
+ * writes the same values again.  Finite inputs (others give unspecified codes of their block and head). */
+int jetfp8_kv_append(const void* k_bf16, int64_t ldk, const void* v_bf16, int64_t ldv, int64_t tokens,
+                     const int32_t* units, int64_t num_units, int64_t kv_heads, int64_t head_dim, uint8_t* codes,
+                     float* scales, int64_t num_blocks, void* recent_bf16, int64_t recent_blocks, void* stream);
+
+/* Causal attention of the step's new tokens over the cache, after jetfp8_kv_append of the same step:
+ *   o[t][h] = sum_n p_n v_n,  p = softmax_n(softmax_scale * q[t][h] . k_n),  n over the positions up to t's,
+ * k_n and v_n being those of kv head h / (q_heads / kv_heads).  q: bf16, row t at q + t * ldq elements,
+ * [q_heads][head_dim] contiguous within a row.
+ *   dst_o_bf16 [tokens][q_heads][head_dim] (NULL: not written);
+ *   dst_codes, dst_scales (both or neither; head_dim 128 only): the JETFP8_ROWS_1x128 quantization of that bf16
+ *   matrix [tokens][q_heads * 128], bit for bit: the activation of the output projection, quantized by the operator
+ *   that produces it (Jet-RL explainers, "Schema de Quantification").
+ * fp32 scores, softmax and sums; the probabilities are rounded to bf16 for the second product.  A row's sums have one
+ * fixed order (spans of 4 blocks, joined in ascending order, then its own block), so a token's result is bitwise the
+ * same decoded alone, in a batch, or within a prompt.
+ * max_new: no request has more new tokens; max_seq: nor more tokens after the step.  A unit beyond either, or whose
+ * fields do not fit the buffers, is left out (its rows stay as they were); a block id outside 0 .. num_blocks - 1
+ * reads as a block without keys.  Infinities and NaN reach only the rows that may see them.
+ * workspace: jetfp8_attention_workspace() bytes (its content is not kept between calls; calls that may run at the same
+ * time need one each); JETFP8_ERR_SHAPE if workspace_bytes is less. */
+int jetfp8_attention(const void* q_bf16, int64_t ldq, int64_t tokens, const int32_t* units, int64_t num_units,
+                     const int32_t* block_table, int64_t requests, int64_t max_blocks, const uint8_t* codes,
+                     const float* scales, int64_t num_blocks, const void* recent_bf16, int64_t recent_blocks,
+                     int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
+                     float softmax_scale, void* dst_o_bf16, uint8_t* dst_codes, float* dst_scales, void* workspace,
+                     int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that jetfp8_attention needs for these sizes (0: none); JETFP8_ERR_SHAPE if it would refuse them. */
+int64_t jetfp8_attention_workspace(int64_t num_units, int64_t max_new, int64_t max_seq, int64_t q_heads,
+                                   int64_t kv_heads, int64_t head_dim);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char* jetfp8_status_string(int status);
 

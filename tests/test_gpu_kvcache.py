@@ -1,0 +1,115 @@
+"""The FP8 key/value cache on the GPU against the CPU oracle: plans and appended blocks bit for bit, attention within
+the error of fp32 arithmetic with bf16 probabilities (the bound is derived in oracle/kvcache.py)."""
+import numpy as np
+import pytest
+
+from kv_case import TwinCache
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True, scope="module")
+def library():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import fp8_precision_rl_amd as jf
+    jf.load_library()
+    return jf
+
+
+# ------------------------------------------------------------------------------------------------ plan
+@pytest.mark.parametrize("requests,ctx,new", [(1, 0, 1), (1, 63, 1), (1, 5, 300), (3, 200, 1), (70, 300, 130),
+                                              (257, 5000, 2), (1000, 700, 66), (4096, 90, 3)])
+def test_plan(requests, ctx, new):
+    rng = np.random.default_rng(requests + new)
+    c = TwinCache(requests, 1, 1, 64, 4 * requests + 16, (ctx + new) // 64 + 1, 64, 3)
+    c.state = np.stack([rng.integers(0, ctx + 1, requests), rng.integers(0, 2, requests)], 1).astype(np.int32)
+    c.dev["state"] = c.up(c.state)
+    lens = rng.integers(0 if requests > 1 else new, new + 1, requests)
+    for pad in (0, 37):
+        c.plan(lens, max(1, int(lens.sum())) + pad, new)
+
+
+def test_plan_refusals():
+    """Each way a request is refused; the others go ahead, and their rows stay where they are."""
+    c = TwinCache(12, 1, 1, 64, 6, 4, 64, 3)
+    c.state[:, 0] = [0, 60, -1, 200, 256, 10, 0, 64, 0, 0, 0, 3]
+    c.state[5, 1] = 2
+    c.dev["state"] = c.up(c.state)
+    lens = [64, 4, 1, 60, 1, 2, -7, 130, 64, 1, 200, 2]       # 200 is above max_new; blocks run out at the ninth
+    ref, _ = c.plan(lens, int(sum(max(n, 0) for n in lens)) - 1, 130)
+    assert list(ref["status"]) == [0, 0, 1, 1, 1, 1, 1, 0, 0, 0, 1, 2]
+    c = TwinCache(4, 1, 1, 64, 2, 8, 64, 3)
+    ref, _ = c.plan([64, 128, 64, 3], 259, 128)
+    assert list(ref["status"]) == [0, 4, 4, 0] and ref["next_free"][0] == 1
+
+
+@pytest.mark.parametrize("head", [-3, 0, 2, 5, 99])
+def test_plan_free_list_ends(head):
+    c = TwinCache(3, 1, 1, 64, 5, 8, 64, 3)
+    c.head[:] = head
+    c.dev["head"] = c.up(c.head)
+    c.plan([128, 64, 1], 193, 128)
+
+
+def test_plan_without_free_blocks_and_slots(library):
+    import torch
+    c = TwinCache(2, 1, 1, 64, 1, 8, 64, 3)
+    c.free = c.free[:0]
+    c.dev["free"] = c.dev["free"][:0]
+    ref, _ = c.plan([63, 64], 127, 64)
+    assert list(ref["status"]) == [0, 4]
+    p = library.kv_plan(c.dev["state"], torch.tensor([63, 64], dtype=torch.int32, device="cuda"), c.dev["free"],
+                        c.dev["head"], c.dev["table"], 127, 64)
+    assert p.slots is None and np.array_equal(p.units.cpu().numpy(), ref["units"])
+
+
+# ------------------------------------------------------------------------------------------------ steps
+@pytest.mark.parametrize("q_heads,kv_heads,head_dim", [(4, 1, 128), (2, 2, 64), (5, 1, 128), (16, 1, 64), (20, 1, 64),
+                                                       (6, 2, 128), (33, 3, 64)])
+def test_steps(q_heads, kv_heads, head_dim):
+    """Prompts, single tokens, chunks that cross blocks, idle requests and padding rows, one after the other."""
+    c = TwinCache(3, q_heads, kv_heads, head_dim, 24, 6, 400, 11)
+    for lens, pad in (([1, 64, 63], 0), ([1, 1, 1], 2), ([62, 1, 1], 0), ([1, 0, 130], 5), ([0, 1, 0], 0), ([1, 2, 1], 0)):
+        c.step(lens, pad)
+
+
+def test_long_context_is_split_and_joined():
+    """Ten summation units per row, a wave each; table bounds above what the requests need."""
+    c = TwinCache(2, 8, 2, 128, 80, 45, 2400, 5)
+    c.step([2300, 70], slack=300)
+    c.step([1, 1], slack=260)
+    c.step([1, 1])
+    c.step([5, 70])
+
+
+@pytest.mark.parametrize("chunk", [1, 3, 7, 64, 100, 200])
+def test_a_token_is_bitwise_the_same_in_every_cut(chunk):
+    """The same 200 tokens fed whole and in chunks, alone and beside other requests: same codes, scales and outputs."""
+    import torch
+    import fp8_precision_rl_amd as jf
+    c = TwinCache(1, 8, 2, 128, 8, 8, 200, 2)
+    host, (q, k, v) = c.qkv(200)
+
+    def run(cuts, beside):
+        R = 1 + beside
+        d = TwinCache(R, 8, 2, 128, 200, 8, 200 * R, 9)
+        out, at = [], 0
+        for n in cuts:
+            lens = [n] * R
+            tokens = n * R
+            p = jf.kv_plan(d.dev["state"], d.up(np.asarray(lens, np.int32)), d.dev["free"], d.dev["head"],
+                           d.dev["table"], tokens, n)
+            rep = lambda x: torch.cat([x[at:at + n]] + [x[at:at + n].flip(0)] * beside)
+            jf.kv_append(rep(k), rep(v), p.units, d.dev["codes"], d.dev["scales"], d.dev["recent"])
+            out.append(jf.attention(rep(q), p.units, d.dev["table"], d.dev["codes"], d.dev["scales"], d.dev["recent"],
+                                    max_new=n, max_seq=at + n)[:n])
+            d.dev["state"], d.dev["head"], at = p.next_state, p.next_free, at + n
+        blocks = d.dev["table"][0, :3].long()
+        return torch.cat(out), d.dev["codes"][blocks], d.dev["scales"][blocks]
+
+    whole = run([200], 0)
+    cuts = [chunk] * (200 // chunk) + ([200 % chunk] if 200 % chunk else [])
+    for beside in (0, 2):
+        for a, b in zip(whole, run(cuts, beside)):
+            assert torch.equal(a, b), (chunk, beside, (a != b).nonzero()[:4])
