@@ -12,10 +12,15 @@ namespace {
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 4;          // waves of a thread block; they share nothing but caches
 constexpr int kSpan = 4;           // cache blocks of a span, the unit of summation
+// The cache's probabilities enter the second product as fp16 (the values' codes are exact in it), scaled by 2^14: the
+// largest is 2^14, below the type's 65504, and all above 2^-28 of the largest keep 11 significant bits.
+constexpr float kLead = 14.0f;
 
 struct AttnArgs {
     const uint16_t* q;
@@ -47,8 +52,19 @@ __device__ __forceinline__ bf16x8 widen(uint32_t lo, uint32_t hi) {
     return bf16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
+__device__ __forceinline__ f16x8 widen_f16(uint32_t lo, uint32_t hi) {
+    const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false);
+    const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true);
+    const f16x2 c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false);
+    const f16x2 d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
+    return f16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
 __device__ __forceinline__ v4f mfma16(const bf16x8& a, const bf16x8& b, const v4f& c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ v4f mfma16(const f16x8& a, const f16x8& b, const v4f& c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
 // Maximum and sum over the four lanes that hold one query's column (lanes l, l + 16, l + 32, l + 48).
@@ -65,8 +81,9 @@ __device__ __forceinline__ float column_sum(float x) {
     return __uint_as_float(s.x) + __uint_as_float(s.y);
 }
 
-// Running softmax state of 16 RT query rows.  Lane l holds query l % 16 of each tile: the running maximum m (of the
-// scores times log2 e), its own share of the denominator, and the 4 channels 16 t + 4 (l / 16) .. + 3 of every t.
+// Running softmax state of 16 RT query rows.  Lane l holds query l % 16 of each tile: the reference m of its
+// exponentials (the running maximum of the scores times log2 e, less a lead), its own share of the denominator, and
+// the 4 channels 16 t + 4 (l / 16) .. + 3 of every t.
 template <int D, int RT>
 struct Softmax {
     float m[RT], l[RT];
@@ -84,11 +101,11 @@ struct Softmax {
 
 // Takes the next 64 scores of a query row (s, in units of c) into its state and leaves exp2(s c - m) in s.
 template <int D, int RT>
-__device__ __forceinline__ void take_scores(Softmax<D, RT>& st, int rt, v4f (&s)[4], float c) {
+__device__ __forceinline__ void take_scores(Softmax<D, RT>& st, int rt, v4f (&s)[4], float c, float lead) {
     float top = fmaxf(fmaxf(s[0].x, s[0].y), fmaxf(s[0].z, s[0].w));
 #pragma unroll
     for (int t = 1; t < 4; ++t) top = fmaxf(top, fmaxf(fmaxf(s[t].x, s[t].y), fmaxf(s[t].z, s[t].w)));
-    const float m = fmaxf(st.m[rt], column_max(top) * c);
+    const float m = fmaxf(st.m[rt], fmaf(column_max(top), c, -lead));
     if (__any(m > st.m[rt])) {          // otherwise every factor is exp2(0) = 1
         const float a = __builtin_amdgcn_exp2f(st.m[rt] - m);
         st.l[rt] *= a;
@@ -105,14 +122,6 @@ __device__ __forceinline__ void take_scores(Softmax<D, RT>& st, int rt, v4f (&s)
             sum += s[t][i];
         }
     st.l[rt] += sum;
-}
-
-// The probabilities of 64 keys, times the values' scale, as operands of the second product.
-__device__ __forceinline__ void to_operand(const v4f (&s)[4], float scale, bf16x8 (&p)[2]) {
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) p[k][j] = (__bf16)(s[2 * k + j / 4][j % 4] * scale);
 }
 
 // Joins the state of the next summation unit (its l already summed over the column) to that of those before it.
@@ -181,10 +190,10 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, int token, int head
 // a wave.  Scores are formed transposed, S^T = K Q^T, so that a lane holds 16 scores of one query per block: maximum
 // and sum need two exchanges between lanes, the factors of a row are plain lane values, and the probabilities
 // are the second product's operand as they are (O^T = V^T P^T; the cache keeps the values in that key order).  Codes
-// go from memory to registers in whole lines, are widened to bf16 (exact) and multiplied by
-// v_mfma_f32_16x16x32_bf16; the scales enter as one factor per block, the keys' in the exponent's argument, the
-// values' on the probabilities.  Rounded below fp32 are only the probabilities (times the values' scale), to bf16,
-// the operand type, an error of at most 2^-9 of each term, and the results.
+// go from memory to registers in whole lines, are widened to the queries' bf16 and the probabilities' fp16 (both exact)
+// and multiplied by v_mfma_f32_16x16x32; the scales enter in fp32, the keys' in the exponent's argument, the values' on
+// a block's product.  Rounded below fp32 are only the probabilities (at most 2^-12 of each, an eighth of what
+// bf16 would cost, whose error alone equals that of the results' own rounding), and the results.
 //
 // Blocks before the unit's own are complete and precede every query of the unit: no mask.  The own block is read as
 // bf16 with the causal mask.  A row's sums run over its blocks in ascending order in spans of 4 blocks, each span
@@ -291,19 +300,22 @@ __global__ __launch_bounds__(kWaves * 64, RT == 1 ? 2 : 1) void attention_kernel
                 }
             load_raw(kr, next, lane);
             if (here) {
-                bf16x8 p[RT][2];
+                f16x8 p[RT][2];
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
-                    take_scores(st, rt, s[rt], c);
-                    to_operand(s[rt], vscale, p[rt]);
+                    take_scores(st, rt, s[rt], c, kLead);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) p[rt][i / 8][i % 8] = (_Float16)s[rt][i / 4][i % 4];
                 }
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
-                    const bf16x8 v0 = widen(vr.w[t].x, vr.w[t].y), v1 = widen(vr.w[t].z, vr.w[t].w);
+                    const f16x8 v0 = widen_f16(vr.w[t].x, vr.w[t].y), v1 = widen_f16(vr.w[t].z, vr.w[t].w);
 #pragma unroll
                     for (int rt = 0; rt < RT; ++rt) {
-                        st.o[rt][t] = mfma16(v0, p[rt][0], st.o[rt][t]);
-                        st.o[rt][t] = mfma16(v1, p[rt][1], st.o[rt][t]);
+                        const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
+                        const v4f pv = mfma16(v1, p[rt][1], mfma16(v0, p[rt][0], z));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) st.o[rt][t][i] = fmaf(pv[i], vscale, st.o[rt][t][i]);
                     }
                 }
             }
@@ -339,7 +351,8 @@ __global__ __launch_bounds__(kWaves * 64, RT == 1 ? 2 : 1) void attention_kernel
                 for (int i = 0; i < 4; ++i) odd |= (w[i] & 0x7F807F80u) + 0x00800080u;
             }
         const bool poisoned = __any((odd & 0x80008000u) != 0);
-        bf16x8 p[RT][2], seen[RT][2];
+        // The values are bf16 here, and so are the probabilities, each as a sum of two (16 significant bits).
+        bf16x8 p[RT][2], rest[RT][2], seen[RT][2];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
             const int place = u.offset + (row0 + rt * 16 + col) / a.group;      // of the query in the block
@@ -351,8 +364,13 @@ __global__ __launch_bounds__(kWaves * 64, RT == 1 ? 2 : 1) void attention_kernel
                     if (!see) s[rt][t][i] = -INFINITY;
                     seen[rt][t / 2][t % 2 * 4 + i] = see ? (__bf16)1.0f : (__bf16)0.0f;
                 }
-            take_scores(st, rt, s[rt], a.scale_log2);
-            to_operand(s[rt], 1.0f, p[rt]);
+            take_scores(st, rt, s[rt], a.scale_log2, 0.0f);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float x = s[rt][i / 4][i % 4];
+                p[rt][i / 8][i % 8] = (__bf16)x;
+                rest[rt][i / 8][i % 8] = (__bf16)(x - (float)(__bf16)x);
+            }
         }
         // 0 * infinity and 0 * NaN would carry a masked key's values into the rows before it.  Where the block holds
         // any, they count as 0 in the product, and the channels of the rows that see one become NaN.
@@ -385,7 +403,7 @@ __global__ __launch_bounds__(kWaves * 64, RT == 1 ? 2 : 1) void attention_kernel
             for (int k = 0; k < 2; ++k) {
                 const bf16x8 x = __builtin_bit_cast(bf16x8, v[t][k]);
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) st.o[rt][t] = mfma16(x, p[rt][k], st.o[rt][t]);
+                for (int rt = 0; rt < RT; ++rt) st.o[rt][t] = mfma16(x, p[rt][k], mfma16(x, rest[rt][k], st.o[rt][t]));
             }
         if (poisoned) {
 #pragma unroll

@@ -265,7 +265,7 @@ int jetfp8_kv_append(const void* k_bf16, int64_t ldk, const void* v_bf16, int64_
  *   dst_codes, dst_scales (both or neither; head_dim 128 only): the JETFP8_ROWS_1x128 quantization of that bf16
  *   matrix [tokens][q_heads * 128], bit for bit: the activation of the output projection, quantized by the operator
  *   that produces it (Jet-RL explainers, "Schema de Quantification").
- * fp32 scores, softmax and sums; the probabilities are rounded to bf16 for the second product.  A row's sums have one
+ * fp32 scores, softmax and sums; the probabilities are rounded to 11 bits or more for the second product.  A row's sums have one
  * fixed order (spans of 4 blocks, joined in ascending order, then its own block), so a token's result is bitwise the
  * same decoded alone, in a batch, or within a prompt.
  * max_new: no request has more new tokens; max_seq: nor more tokens after the step.  A unit beyond either, or whose

@@ -1,5 +1,5 @@
 """The FP8 key/value cache on the GPU against the CPU oracle: plans and appended blocks bit for bit, attention within
-the error of fp32 arithmetic with bf16 probabilities (the bound is derived in oracle/kvcache.py)."""
+the error of fp32 arithmetic with 11-bit probabilities (the bound is derived in oracle/kvcache.py)."""
 import numpy as np
 import pytest
 
