@@ -18,9 +18,12 @@ typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 4;          // waves of a thread block; they share nothing but caches
 constexpr int kSpan = 4;           // cache blocks of a span, the unit of summation
-// The cache's probabilities enter the second product as fp16 (the values' codes are exact in it), scaled by 2^14: the
-// largest is 2^14, below the type's 65504, and all above 2^-28 of the largest keep 11 significant bits.
-constexpr float kLead = 14.0f;
+// The cache's probabilities enter the second product as fp16, in which the values' codes are exact.  A row's reference m
+// follows its running maximum only when that has grown by more than 2^8 (in 16 rows of fresh spans some maximum grows
+// with nearly every block, and following each would rescale the whole accumulator each time), so probabilities reach
+// 2^8 of the reference, and the values' share (below 2) comes on top: a lead of 2^6 keeps the largest at 2^15, below
+// the type's 65504, and all above 2^-20 of the largest at 11 significant bits.
+constexpr float kLead = 6.0f, kSlack = 8.0f;
 
 struct AttnArgs {
     const uint16_t* q;
@@ -67,12 +70,15 @@ __device__ __forceinline__ v4f mfma16(const f16x8& a, const f16x8& b, const v4f&
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
+// Maximum that keeps a NaN (one instruction for three operands, no quieting of its inputs).
+__device__ __forceinline__ float max_of(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 // Maximum and sum over the four lanes that hold one query's column (lanes l, l + 16, l + 32, l + 48).
 __device__ __forceinline__ float column_max(float x) {
     u32x2 s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    x = fmaxf(__uint_as_float(s.x), __uint_as_float(s.y));
+    x = max_of(__uint_as_float(s.x), __uint_as_float(s.y));
     s = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    return fmaxf(__uint_as_float(s.x), __uint_as_float(s.y));
+    return max_of(__uint_as_float(s.x), __uint_as_float(s.y));
 }
 __device__ __forceinline__ float column_sum(float x) {
     u32x2 s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -82,8 +88,7 @@ __device__ __forceinline__ float column_sum(float x) {
 }
 
 // Running softmax state of 16 RT query rows.  Lane l holds query l % 16 of each tile: the reference m of its
-// exponentials (the running maximum of the scores times log2 e, less a lead), its own share of the denominator, and
-// the 4 channels 16 t + 4 (l / 16) .. + 3 of every t.
+// exponentials (in log2), its own share of the denominator, and the 4 channels 16 t + 4 (l / 16) .. + 3 of every t.
 template <int D, int RT>
 struct Softmax {
     float m[RT], l[RT];
@@ -99,29 +104,13 @@ struct Softmax {
     }
 };
 
-// Takes the next 64 scores of a query row (s, in units of c) into its state and leaves exp2(s c - m) in s.
-template <int D, int RT>
-__device__ __forceinline__ void take_scores(Softmax<D, RT>& st, int rt, v4f (&s)[4], float c, float lead) {
-    float top = fmaxf(fmaxf(s[0].x, s[0].y), fmaxf(s[0].z, s[0].w));
+// Largest of the 64 scores that a query has in a block.
+__device__ __forceinline__ float top_score(const v4f (&s)[4]) {
+    float top = max_of(max_of(s[0].x, s[0].y), s[0].z);
+    top = max_of(max_of(top, s[0].w), s[1].x);
 #pragma unroll
-    for (int t = 1; t < 4; ++t) top = fmaxf(top, fmaxf(fmaxf(s[t].x, s[t].y), fmaxf(s[t].z, s[t].w)));
-    const float m = fmaxf(st.m[rt], fmaf(column_max(top), c, -lead));
-    if (__any(m > st.m[rt])) {          // otherwise every factor is exp2(0) = 1
-        const float a = __builtin_amdgcn_exp2f(st.m[rt] - m);
-        st.l[rt] *= a;
-#pragma unroll
-        for (int t = 0; t < D / 16; ++t) st.o[rt][t] *= a;
-        st.m[rt] = m;
-    }
-    float sum = 0.0f;
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            s[t][i] = __builtin_amdgcn_exp2f(fmaf(s[t][i], c, -m));
-            sum += s[t][i];
-        }
-    st.l[rt] += sum;
+    for (int i = 5; i < 15; i += 2) top = max_of(max_of(top, s[i / 4][i % 4]), s[(i + 1) / 4][(i + 1) % 4]);
+    return column_max(max_of(top, s[3].w));
 }
 
 // Joins the state of the next summation unit (its l already summed over the column) to that of those before it.
@@ -186,104 +175,254 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, int token, int head
     }
 }
 
-// Attention of the query rows of one unit's kv head: rows are (new token, query head of the group), 16 RT of them to
-// a wave.  Scores are formed transposed, S^T = K Q^T, so that a lane holds 16 scores of one query per block: maximum
-// and sum need two exchanges between lanes, the factors of a row are plain lane values, and the probabilities
-// are the second product's operand as they are (O^T = V^T P^T; the cache keeps the values in that key order).  Codes
-// go from memory to registers in whole lines, are widened to the queries' bf16 and the probabilities' fp16 (both exact)
-// and multiplied by v_mfma_f32_16x16x32; the scales enter in fp32, the keys' in the exponent's argument, the values' on
-// a block's product.  Rounded below fp32 are only the probabilities (at most 2^-12 of each, an eighth of what
-// bf16 would cost, whose error alone equals that of the results' own rounding), and the results.
-//
-// Blocks before the unit's own are complete and precede every query of the unit: no mask.  The own block is read as
-// bf16 with the causal mask.  A row's sums run over its blocks in ascending order in spans of 4 blocks, each span
-// from its own zero state, the spans joined in ascending order and the own block last.  The split form gives every
-// span a wave of its own and joins the partial results in a second kernel; the serial form walks them in one wave.
-// Both perform the same operations on a row, whatever rows share the call: a token's result is bitwise the same
-// decoded alone, in a batch, or within a prompt.
-template <int D, int RT, bool SPLIT>
-__global__ __launch_bounds__(kWaves * 64, RT == 1 ? 2 : 1) void attention_kernel(AttnArgs a) {
-    constexpr int NT = D / 16;      // output tiles, and loads of a block's keys or values
-    constexpr int NK = D / 32;      // contraction steps of the score product
-    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int g = lane / 16, col = lane % 16;
-    int job = blockIdx.x;
-    const int head = job % a.kv_heads;
-    job /= a.kv_heads;
-    int unit, rg, span = 0;
-    if (SPLIT) {
-        const int jobs = a.spans * a.row_groups, chunks = (jobs + kWaves - 1) / kWaves;
-        unit = job / chunks;
-        const int i = job % chunks * kWaves + wave;
-        if (i >= jobs) return;
-        span = i / a.row_groups;
-        rg = i % a.row_groups;
-    } else {
-        const int chunks = (a.row_groups + kWaves - 1) / kWaves;
-        unit = a.num_units - 1 - job / chunks;       // the longest rows of a request first
-        rg = job % chunks * kWaves + wave;
-    }
-    const KvUnit u = a.units[unit];
-    if (!unit_fits(u, a.requests, a.tokens, a.recent_blocks, a.num_blocks)) return;
-    const int rows = u.rows * a.group, row0 = rg * (16 * RT);
-    if (row0 >= rows || rows > a.max_rows || u.block > a.max_blocks) return;
-    const int total_spans = (u.block + kSpan - 1) / kSpan;
-    if (SPLIT && span > total_spans) return;
-    const int first = SPLIT ? span * kSpan : 0;
-    const int last = SPLIT ? min(first + kSpan, u.block) : u.block;      // first > last only for the own block's wave
+// The scalars of a span.  The values' scales are taken relative to ref, the power of two at or below the largest of
+// the span, so that a block's share r (below 2) can be a factor of its probabilities and the span's products stay in
+// one accumulator; ref returns when the span ends.  The share enters the exponential's argument as its log2, and the
+// denominator is divided by it again.  (A block whose values are 2^-20 of another's of its span, or less, loses bits: an
+// absolute error below 2^-31 of that other block's values.  Shares are held at 2^-60 or more, so that the denominator
+// keeps its terms.)  A block id out of range has no keys: its bit of use is 0.
+struct Span {
+    int at[kSpan];
+    float c[kSpan], r[kSpan];
+    int use;
+    float ref;
+};
 
-    bf16x8 q[RT][NK];
+// Blocks first .. of a request, of which those before `last` are read and those before `end` (no less) are loaded.
+__device__ __forceinline__ Span load_span(const AttnArgs& a, const int* entries, const float* scales, int first,
+                                          int last, int end) {
+    Span s;
+    float top = 0.0f;
+    s.use = 0;
+#pragma unroll
+    for (int i = 0; i < kSpan; ++i) {
+        const int id = entries[max(min(first + i, end - 1), 0)];
+        s.at[i] = min(max(id, 0), a.num_blocks - 1);
+        const float* p = scales + (int64_t)s.at[i] * a.kv_heads * 2;
+        const bool here = first + i < last && id == s.at[i];
+        s.c[i] = p[0] * a.scale_log2;
+        s.r[i] = here ? p[1] : 0.0f;
+        s.use |= here ? 1 << i : 0;
+        top = fmaxf(top, s.r[i]);
+    }
+    const uint32_t e = min(max(__float_as_uint(top) >> 23, 1u), 253u);
+    s.ref = __uint_as_float(e << 23);
+#pragma unroll
+    for (int i = 0; i < kSpan; ++i) s.r[i] = fmaxf(s.r[i] * __uint_as_float((254u - e) << 23), 0x1p-60f);
+    return s;
+}
+
+// The queries of a wave's row tiles, rows (token, query head of the group) from row0 on; rows behind the last are 0.
+template <int D, int RT>
+__device__ __forceinline__ void load_queries(bf16x8 (&q)[RT][D / 32], const AttnArgs& a, const KvUnit& u, int head,
+                                             int row0, int rows, int lane) {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-        const int row = row0 + rt * 16 + col, tok = row / a.group;
-        const uint16_t* p = a.q + (u.row + tok) * a.ldq + ((int64_t)head * a.group + row % a.group) * D + g * 8;
+        const int row = row0 + rt * 16 + lane % 16, tok = row / a.group;
+        const uint16_t* p = a.q + (u.row + tok) * a.ldq + ((int64_t)head * a.group + row % a.group) * D + lane / 16 * 8;
 #pragma unroll
-        for (int k = 0; k < NK; ++k) {
+        for (int k = 0; k < D / 32; ++k) {
             uint4 x = make_uint4(0, 0, 0, 0);
             if (row < rows) x = *reinterpret_cast<const uint4*>(p + k * 32);
             q[rt][k] = __builtin_bit_cast(bf16x8, x);
         }
     }
+}
 
-    Softmax<D, RT> st, all;
-    st.clear();
-    if (!SPLIT) all.clear();
-
-    auto join = [&]() {
+// Takes the scores of a cache block's 64 keys (s, in units of c) into the rows' states and gives their probabilities,
+// times the values' share r, as operands of the second product.  START: the first block of a span, whose states are
+// empty and take its maximum as it is.
+template <bool START, int D, int RT>
+__device__ __forceinline__ void take_block(Softmax<D, RT>& st, const v4f (&s)[RT][4], float c, float r, f16x8 (&p)[RT][2]) {
+    float m[RT];
+    bool grown = false;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        m[rt] = fmaf(top_score(s[rt]), c, -kLead);
+        if (START) st.m[rt] = m[rt];
+        else grown |= m[rt] > st.m[rt] + kSlack;
+    }
+    if (!START && __any(grown)) {
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-            float x, y;
-            join_factors(all.m[rt], st.m[rt], x, y);
-            all.l[rt] = fmaf(all.l[rt], x, column_sum(st.l[rt]) * y);
+            const float to = m[rt] > st.m[rt] + kSlack ? m[rt] : st.m[rt];
+            const float f = __builtin_amdgcn_exp2f(st.m[rt] - to);       // 1 for the rows that keep theirs
+            st.l[rt] *= f;
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) all.o[rt][t][i] = fmaf(all.o[rt][t][i], x, st.o[rt][t][i] * y);
+            for (int t = 0; t < D / 16; ++t) st.o[rt][t] *= f;
+            st.m[rt] = to;
         }
-        st.clear();
-    };
+    }
+    const float log_r = __builtin_amdgcn_logf(r), inv_r = __builtin_amdgcn_rcpf(r);
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const float base = log_r - st.m[rt];
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float e = __builtin_amdgcn_exp2f(fmaf(s[rt][i / 4][i % 4], c, base));
+            sum += e;
+            p[rt][i / 8][i % 8] = (_Float16)e;
+        }
+        st.l[rt] = fmaf(sum, inv_r, st.l[rt]);
+    }
+}
 
-    if (first < last) {
-        const int* entries = a.table + (int64_t)u.request * a.width;
+// The unit's own block, bf16 with the causal mask, into an empty state.  keys, values: the block's operands, 64 lanes
+// of 16 bytes each; AHEAD: the values are loaded before the scores are formed (from memory, not from LDS).
+template <bool AHEAD, int D, int RT>
+__device__ __forceinline__ void own_block(Softmax<D, RT>& st, const bf16x8 (&q)[RT][D / 32], float scale_log2,
+                                          int offset, int group, int row0, const bf16x8* keys, const uint4* values,
+                                          int lane) {
+    constexpr int NK = D / 32, NT = D / 16;
+    uint4 ahead[AHEAD ? NT : 1][2];
+    if (AHEAD) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) ahead[AHEAD ? t : 0][k] = values[(t * 2 + k) * 64 + lane];
+    }
+    v4f s[RT][4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int k = 0; k < NK; ++k) {
+            const bf16x8 x = keys[(t * NK + k) * 64 + lane];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
+                s[rt][t] = mfma16(x, q[rt][k], k ? s[rt][t] : z);
+            }
+        }
+    // The values are bf16 here, and so are the probabilities, each as a sum of two (16 significant bits).
+    bf16x8 p[RT][2], rest[RT][2];
+    int place[RT];                      // of the query in the block
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        place[rt] = offset + (row0 + rt * 16 + lane % 16) / group;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (i / 4 * 16 + lane / 16 * 4 + i % 4 > place[rt]) s[rt][i / 4][i % 4] = -INFINITY;
+        st.m[rt] = top_score(s[rt]) * scale_log2;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const float e = __builtin_amdgcn_exp2f(fmaf(s[rt][i / 4][i % 4], scale_log2, -st.m[rt]));
+            st.l[rt] += e;
+            p[rt][i / 8][i % 8] = (__bf16)e;
+            rest[rt][i / 8][i % 8] = (__bf16)(e - (float)(__bf16)e);
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        uint4 v[2];
+        uint32_t odd = 0;             // bit 15 of a half: some value's exponent is all ones (infinity or NaN)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            v[k] = AHEAD ? ahead[AHEAD ? t : 0][k] : values[(t * 2 + k) * 64 + lane];
+            const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) odd |= (w[i] & 0x7F807F80u) + 0x00800080u;
+        }
+        v4f bad[RT];                  // above 0: the row sees such a value in this channel
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) bad[rt] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+        if (__any((odd & 0x80008000u) != 0)) {
+            // 0 * infinity and 0 * NaN would carry a masked key's values into the rows before it: such values count
+            // as 0 in the product, and the channels of the rows that see one become NaN.
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w}, mark[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    mark[i] = ((w[i] & 0x7F80u) == 0x7F80u ? 0x3F80u : 0u) |
+                              ((w[i] & 0x7F800000u) == 0x7F800000u ? 0x3F800000u : 0u);
+                    w[i] &= ~((mark[i] & 0xFFFFu ? 0xFFFFu : 0u) | (mark[i] >> 16 ? 0xFFFF0000u : 0u));
+                }
+                v[k] = make_uint4(w[0], w[1], w[2], w[3]);
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    bf16x8 seen;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        seen[j] = (__bf16)(k * 32 + j / 4 * 16 + lane / 16 * 4 + j % 4 <= place[rt] ? 1.0f : 0.0f);
+                    bad[rt] = mfma16(__builtin_bit_cast(bf16x8, make_uint4(mark[0], mark[1], mark[2], mark[3])), seen, bad[rt]);
+                }
+            }
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const bf16x8 x = __builtin_bit_cast(bf16x8, v[k]);
+                st.o[rt][t] = mfma16(x, p[rt][k], mfma16(x, rest[rt][k], st.o[rt][t]));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) st.o[rt][t][i] = bad[rt][i] > 0.0f ? NAN : st.o[rt][t][i];
+        }
+    }
+}
+
+// The operands of a recent block: its keys, and behind them (64 D elements on) its values.
+template <int D>
+__device__ __forceinline__ const uint4* recent_block(const AttnArgs& a, int recent, int head) {
+    return reinterpret_cast<const uint4*>(a.recent + ((int64_t)recent * a.kv_heads + head) * 2 * (kKvBlock * D));
+}
+
+// Attention of the query rows of one unit's kv head.  Rows are (new token, query head of the group), 16 RT of them to
+// a wave.  Scores are formed transposed, S^T = K Q^T, so that a lane holds 16 scores of one query per block: maximum
+// and sum need two exchanges between lanes, the factors of a row are plain lane values, and the probabilities
+// are the second product's operand as they are (O^T = V^T P^T; the cache keeps the values in that key order).  Codes
+// are widened to the queries' bf16 and the probabilities' fp16 (both exact) and multiplied by
+// v_mfma_f32_16x16x32; the scales enter in fp32, the keys' in the exponent's argument, the values' on the
+// probabilities.  Rounded below fp32 are only the probabilities (at most 2^-12 of each, an eighth of what bf16
+// would cost, whose error alone equals that of the results' own rounding), and the results.
+//
+// Blocks before the unit's own are complete and precede every query of the unit: no mask.  A row's sums run over its
+// blocks in ascending order in spans of 4 blocks, each span from its own zero state; the spans are joined in ascending
+// order, and the own block last.  Two kernels do this, with the same operations on a row whatever rows share the call,
+// so that a token's result is bitwise the same decoded alone, in a batch, or within a prompt:
+//
+// attention_span_kernel gives every span of a row group a wave of its own and leaves the joining to
+// attention_join_kernel: for few rows, where the time is that of reading the cache and every wave must read.  Codes go
+// from memory to registers in whole lines (1 KB per load of a wave) and the next block's are loaded while this one's
+// are used; there is no LDS.
+template <int D, int RT>
+__global__ __launch_bounds__(kWaves * 64, RT == 1 ? 3 : 2) void attention_span_kernel(AttnArgs a) {
+    constexpr int NT = D / 16;      // output tiles, and loads of a block's keys or values
+    constexpr int NK = D / 32;      // contraction steps of the score product
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int head = blockIdx.x % a.kv_heads;
+    const int jobs = a.spans * a.row_groups, chunks = (jobs + kWaves - 1) / kWaves;
+    const int unit = blockIdx.x / a.kv_heads / chunks, job = blockIdx.x / a.kv_heads % chunks * kWaves + wave;
+    if (job >= jobs) return;
+    const int span = job / a.row_groups, row0 = job % a.row_groups * (16 * RT);
+    const KvUnit u = a.units[unit];
+    if (!unit_fits(u, a.requests, a.tokens, a.recent_blocks, a.num_blocks)) return;
+    const int rows = u.rows * a.group, own = (u.block + kSpan - 1) / kSpan;
+    if (row0 >= rows || rows > a.max_rows || u.block > a.max_blocks || span > own) return;
+
+    bf16x8 q[RT][NK];
+    load_queries<D, RT>(q, a, u, head, row0, rows, lane);
+    Softmax<D, RT> st;
+    st.clear();
+    float ref = 1.0f;
+    if (span == own) {
+        const uint4* mem = recent_block<D>(a, u.recent, head);
+        own_block<true, D, RT>(st, q, a.scale_log2, u.offset, a.group, row0, reinterpret_cast<const bf16x8*>(mem),
+                               mem + kKvBlock * D / 8, lane);
+    } else {
+        const int first = span * kSpan, last = min(first + kSpan, u.block);
         const int64_t block_bytes = (int64_t)a.kv_heads * 2 * kKvBlock * D;
         const uint8_t* codes = a.codes + (int64_t)head * 2 * kKvBlock * D;
-        const float* scales = a.scales + head * 2;
+        const Span sp = load_span(a, a.table + (int64_t)u.request * a.width, a.scales + head * 2, first, last, last);
+        ref = sp.ref;
         Raw<D> kr, vr;
-        int id = entries[first];
-        int at = min(max(id, 0), a.num_blocks - 1);
-        float ks = scales[(int64_t)at * a.kv_heads * 2], vs = scales[(int64_t)at * a.kv_heads * 2 + 1];
-        load_raw(kr, codes + at * block_bytes, lane);
-        load_raw(vr, codes + at * block_bytes + kKvBlock * D, lane);
-        int next_id = entries[min(first + 1, last - 1)];
-        for (int b = first; b < last; ++b) {
-            const bool here = id == at;
-            const float c = ks * a.scale_log2, vscale = vs;
-            id = next_id;
-            at = min(max(id, 0), a.num_blocks - 1);
-            const uint8_t* next = codes + at * block_bytes;
-            next_id = entries[min(b + 2, last - 1)];
-            ks = scales[(int64_t)at * a.kv_heads * 2];
-            vs = scales[(int64_t)at * a.kv_heads * 2 + 1];
+        load_raw(kr, codes + sp.at[0] * block_bytes, lane);
+        load_raw(vr, codes + sp.at[0] * block_bytes + kKvBlock * D, lane);
+#pragma unroll
+        for (int i = 0; i < kSpan; ++i) {
+            if (first + i >= last) break;
+            const uint8_t* next = codes + sp.at[i + 1 < kSpan ? i + 1 : i] * block_bytes;
             v4f s[RT][4];
 #pragma unroll
             for (int t = 0; t < 4; ++t)
@@ -294,146 +433,199 @@ __global__ __launch_bounds__(kWaves * 64, RT == 1 ? 2 : 1) void attention_kernel
 #pragma unroll
                     for (int rt = 0; rt < RT; ++rt) {
                         const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
-                        s[rt][t] = mfma16(k0, q[rt][k], k ? s[rt][t] : z);
-                        s[rt][t] = mfma16(k1, q[rt][k + 1], s[rt][t]);
+                        s[rt][t] = mfma16(k1, q[rt][k + 1], mfma16(k0, q[rt][k], k ? s[rt][t] : z));
                     }
                 }
-            load_raw(kr, next, lane);
-            if (here) {
+            const bool more = i + 1 < kSpan && first + i + 1 < last;
+            if (more) load_raw(kr, next, lane);
+            if (sp.use >> i & 1) {
                 f16x8 p[RT][2];
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    take_scores(st, rt, s[rt], c, kLead);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) p[rt][i / 8][i % 8] = (_Float16)s[rt][i / 4][i % 4];
-                }
+                if (i == 0) take_block<true>(st, s, sp.c[i], sp.r[i], p);
+                else take_block<false>(st, s, sp.c[i], sp.r[i], p);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     const f16x8 v0 = widen_f16(vr.w[t].x, vr.w[t].y), v1 = widen_f16(vr.w[t].z, vr.w[t].w);
 #pragma unroll
-                    for (int rt = 0; rt < RT; ++rt) {
-                        const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
-                        const v4f pv = mfma16(v1, p[rt][1], mfma16(v0, p[rt][0], z));
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) st.o[rt][t][i] = fmaf(pv[i], vscale, st.o[rt][t][i]);
-                    }
+                    for (int rt = 0; rt < RT; ++rt)
+                        st.o[rt][t] = mfma16(v1, p[rt][1], mfma16(v0, p[rt][0], st.o[rt][t]));
                 }
             }
-            load_raw(vr, next + kKvBlock * D, lane);
-            if (!SPLIT && (b % kSpan == kSpan - 1 || b + 1 == last)) join();
+            if (more) load_raw(vr, next + kKvBlock * D, lane);
         }
     }
-
-    if (!SPLIT || span == total_spans) {
-        // the own block: bf16, keys after the query masked
-        const uint16_t* mem = a.recent + ((int64_t)u.recent * a.kv_heads + head) * 2 * (kKvBlock * D);
-        v4f s[RT][4];
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int k = 0; k < NK; ++k) {
-                const bf16x8 x = *reinterpret_cast<const bf16x8*>(mem + ((t * NK + k) * 64 + lane) * 8);
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
-                    s[rt][t] = mfma16(x, q[rt][k], k ? s[rt][t] : z);
-                }
-            }
-        uint4 v[NT][2];
-        uint32_t odd = 0;             // bit 15 of a half: some value's exponent is all ones (infinity or NaN)
+    for (int rt = 0; rt < RT; ++rt) {
+        const int row = row0 + rt * 16 + lane % 16;
+        const float l = column_sum(st.l[rt]);
+        if (row >= rows) continue;
+        const int64_t at = (((int64_t)unit * a.kv_heads + head) * a.spans + span) * a.max_rows + row;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
+            *reinterpret_cast<v4f*>(a.part_o + at * D + t * 16 + lane / 16 * 4) = st.o[rt][t] * ref;
+        if (lane < 16) a.part_ml[at] = make_float2(st.m[rt], l);
+    }
+}
+
+// attention_tile_kernel walks all spans of 128 rows in one block of four waves: for prompts, where the time is that of
+// the arithmetic.  Each wave widens a quarter of a block's codes into LDS, as operands, and all four read them there,
+// so that a code is widened once per 128 rows instead of once per 32 (the conversions would otherwise take a third
+// of the vector unit's time).  Two buffers, one barrier per block; a block's codes are loaded from memory two blocks
+// ahead.  Units are taken in pairs: two of one request share thread blocks, the waves of the first leaving out the last
+// block or so, since a unit's rows (64 query heads per kv head) need not be a multiple of 128.
+template <int D>
+__global__ __launch_bounds__(kWaves * 64, 2) void attention_tile_kernel(AttnArgs a) {
+    constexpr int RT = 2, NT = D / 16, NK = D / 32;
+    constexpr int NL = NT / kWaves;        // loads of a block's keys, and of its values, per wave
+    constexpr int NO = kKvBlock * D / 8 / 64;   // operands of a block's keys, and of its values
+    __shared__ bf16x8 kt[2][NO][64];
+    __shared__ f16x8 vt[2][NO][64];
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int head = blockIdx.x % a.kv_heads, chunks = (a.row_groups + kWaves - 1) / kWaves;
+    const int pairs = (a.num_units + 1) / 2;
+    const int first_unit = 2 * (pairs - 1 - blockIdx.x / a.kv_heads / (2 * chunks));      // the longest rows first
+    const int chunk = blockIdx.x / a.kv_heads % (2 * chunks);
+    KvUnit us[2];
+    int tiles[2];                          // row tiles of 32 that the two units have
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                v[t][k] = *reinterpret_cast<const uint4*>(mem + kKvBlock * D + ((t * 2 + k) * 64 + lane) * 8);
-                const uint32_t w[4] = {v[t][k].x, v[t][k].y, v[t][k].z, v[t][k].w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) odd |= (w[i] & 0x7F807F80u) + 0x00800080u;
-            }
-        const bool poisoned = __any((odd & 0x80008000u) != 0);
-        // The values are bf16 here, and so are the probabilities, each as a sum of two (16 significant bits).
-        bf16x8 p[RT][2], rest[RT][2], seen[RT][2];
+    for (int i = 0; i < 2; ++i) {
+        us[i] = a.units[min(first_unit + i, a.num_units - 1)];
+        const int rows = us[i].rows * a.group;
+        const bool fits = first_unit + i < a.num_units &&
+                          unit_fits(us[i], a.requests, a.tokens, a.recent_blocks, a.num_blocks) &&
+                          rows <= a.max_rows && us[i].block <= a.max_blocks;
+        tiles[i] = fits ? (rows + 16 * RT - 1) / (16 * RT) : 0;
+    }
+    const bool shared = tiles[0] && tiles[1] && us[0].request == us[1].request;
+    const int own_chunks = (tiles[0] + kWaves - 1) / kWaves;      // of the first unit, where the two do not share
+    int tile = chunk * kWaves + wave, which = 0, end;             // end: blocks that the thread block walks
+    bool two = false;                                             // it has rows of both units
+    if (shared) {
+        if (chunk * kWaves >= tiles[0] + tiles[1]) return;
+        which = tile >= tiles[0];
+        two = chunk * kWaves < tiles[0] && chunk * kWaves + kWaves > tiles[0];
+        end = chunk * kWaves + kWaves > tiles[0] ? max(us[0].block, us[1].block) : us[0].block;
+        if (which) tile -= tiles[0];
+    } else {
+        which = chunk >= own_chunks;
+        if (which) tile -= own_chunks * kWaves;
+        if (chunk - (which ? own_chunks : 0) >= (tiles[which] + kWaves - 1) / kWaves) return;
+        end = us[which].block;
+    }
+    const KvUnit u = us[which];
+    const bool busy = tile < tiles[which];
+    const int row0 = tile * (16 * RT), rows = busy ? u.rows * a.group : 0, last = busy ? u.block : 0;
+
+    bf16x8 q[RT][NK];
+    load_queries<D, RT>(q, a, u, head, row0, rows, lane);
+    Softmax<D, RT> st, all;
+    st.clear();
+    all.clear();
+    auto join = [&](float ref) {
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-            const int place = u.offset + (row0 + rt * 16 + col) / a.group;      // of the query in the block
-#pragma unroll
-            for (int t = 0; t < 4; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool see = t * 16 + g * 4 + i <= place;
-                    if (!see) s[rt][t][i] = -INFINITY;
-                    seen[rt][t / 2][t % 2 * 4 + i] = see ? (__bf16)1.0f : (__bf16)0.0f;
-                }
-            take_scores(st, rt, s[rt], a.scale_log2, 0.0f);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float x = s[rt][i / 4][i % 4];
-                p[rt][i / 8][i % 8] = (__bf16)x;
-                rest[rt][i / 8][i % 8] = (__bf16)(x - (float)(__bf16)x);
-            }
-        }
-        // 0 * infinity and 0 * NaN would carry a masked key's values into the rows before it.  Where the block holds
-        // any, they count as 0 in the product, and the channels of the rows that see one become NaN.
-        v4f bad[RT][NT];
-        if (poisoned) {
+            float x, y;
+            join_factors(all.m[rt], st.m[rt], x, y);
+            all.l[rt] = fmaf(all.l[rt], x, column_sum(st.l[rt]) * y);
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    uint32_t w[4] = {v[t][k].x, v[t][k].y, v[t][k].z, v[t][k].w}, mark[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        mark[i] = ((w[i] & 0x7F80u) == 0x7F80u ? 0x3F80u : 0u) |
-                                  ((w[i] & 0x7F800000u) == 0x7F800000u ? 0x3F800000u : 0u);
-                        if (mark[i] & 0xFFFFu) w[i] &= 0xFFFF0000u;
-                        if (mark[i] >> 16) w[i] &= 0xFFFFu;
-                    }
-                    v[t][k] = make_uint4(w[0], w[1], w[2], w[3]);
-                    const bf16x8 x = __builtin_bit_cast(bf16x8, make_uint4(mark[0], mark[1], mark[2], mark[3]));
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt) {
-                        const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
-                        bad[rt][t] = mfma16(x, seen[rt][k], k ? bad[rt][t] : z);
-                    }
-                }
+                for (int i = 0; i < 4; ++i) all.o[rt][t][i] = fmaf(all.o[rt][t][i], x, st.o[rt][t][i] * ref * y);
         }
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const bf16x8 x = __builtin_bit_cast(bf16x8, v[t][k]);
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) st.o[rt][t] = mfma16(x, p[rt][k], mfma16(x, rest[rt][k], st.o[rt][t]));
-            }
-        if (poisoned) {
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (bad[rt][t][i] > 0.0f) st.o[rt][t][i] = NAN;
-        }
-        if (!SPLIT) join();
-    }
+        st.clear();
+    };
 
+    const int* entries = a.table + (int64_t)u.request * a.width;
+    const float* scales = a.scales + head * 2;
+    const int64_t block_bytes = (int64_t)a.kv_heads * 2 * kKvBlock * D;
+    const uint8_t* codes = a.codes + (int64_t)head * 2 * kKvBlock * D + lane * 16 + wave * (NL * 1024);
+    uint4 kr[NL], vr[NL];
+    auto load = [&](int at) {
+        const uint8_t* p = codes + at * block_bytes;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            kr[i] = *reinterpret_cast<const uint4*>(p + i * 1024);
+            vr[i] = *reinterpret_cast<const uint4*>(p + kKvBlock * D + i * 1024);
+        }
+    };
+    auto store = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            const int n = 2 * (wave * NL + i);
+            kt[buf][n][lane] = widen(kr[i].x, kr[i].y);
+            kt[buf][n + 1][lane] = widen(kr[i].z, kr[i].w);
+            vt[buf][n][lane] = widen_f16(vr[i].x, vr[i].y);
+            vt[buf][n + 1][lane] = widen_f16(vr[i].z, vr[i].w);
+        }
+    };
+    if (end > 0) {
+        Span next = load_span(a, entries, scales, 0, last, end);
+        load(next.at[0]);
+        store(0);
+        load(next.at[1]);
+        __syncthreads();
+        for (int first = 0; first < end; first += kSpan) {
+            const Span sp = next;
+            next = load_span(a, entries, scales, first + kSpan, last, end);
+#pragma unroll
+            for (int i = 0; i < kSpan; ++i) {
+                if (first + i >= end) break;
+                const int buf = i % 2;
+                const bool here = sp.use >> i & 1;
+                v4f s[RT][4];
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int k = 0; k < NK; ++k) {
+                        const bf16x8 x = kt[buf][t * NK + k][lane];
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt) {
+                            const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
+                            s[rt][t] = mfma16(x, q[rt][k], k ? s[rt][t] : z);
+                        }
+                    }
+                store(buf ^ 1);                                 // block i + 1; nobody reads that buffer before the barrier
+                load(i + 2 < kSpan ? sp.at[i + 2 < kSpan ? i + 2 : 0] : next.at[i + 2 < kSpan ? 0 : i + 2 - kSpan]);
+                if (here) {
+                    f16x8 p[RT][2];
+                    if (i == 0) take_block<true>(st, s, sp.c[i], sp.r[i], p);
+                    else take_block<false>(st, s, sp.c[i], sp.r[i], p);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const f16x8 x = vt[buf][t * 2 + k][lane];
+#pragma unroll
+                            for (int rt = 0; rt < RT; ++rt) st.o[rt][t] = mfma16(x, p[rt][k], st.o[rt][t]);
+                        }
+                }
+                __syncthreads();
+            }
+            if (first < last) join(sp.ref);
+        }
+    }
+    // The own blocks, as they are, through the same buffers: the first unit's (or the only one's) and the second's.
+    const int owns[2] = {two ? us[0].recent : u.recent, us[1].recent};
+#pragma unroll
+    for (int buf = 0; buf < 2; ++buf) {
+        if (buf && !two) break;
+        const uint4* mem = recent_block<D>(a, owns[buf], head) + wave * (NO / kWaves * 64) + lane;
+#pragma unroll
+        for (int i = 0; i < NO / kWaves; ++i) {
+            kt[buf][wave * (NO / kWaves) + i][lane] = __builtin_bit_cast(bf16x8, mem[i * 64]);
+            vt[buf][wave * (NO / kWaves) + i][lane] = __builtin_bit_cast(f16x8, mem[kKvBlock * D / 8 + i * 64]);
+        }
+    }
+    __syncthreads();
+    if (!busy) return;
+    const int buf = two ? which : 0;
+    own_block<false, D, RT>(st, q, a.scale_log2, u.offset, a.group, row0, &kt[buf][0][0],
+                            reinterpret_cast<const uint4*>(&vt[buf][0][0]), lane);
+    join(1.0f);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-        const int row = row0 + rt * 16 + col;
-        const bool live = row < rows;
-        if (SPLIT) {
-            const float l = column_sum(st.l[rt]);
-            if (live) {
-                const int64_t at = (((int64_t)unit * a.kv_heads + head) * a.spans + span) * a.max_rows + row;
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    *reinterpret_cast<v4f*>(a.part_o + at * D + t * 16 + g * 4) = st.o[rt][t];
-                if (g == 0) a.part_ml[at] = make_float2(st.m[rt], l);
-            }
-        } else {
-            store_row<D>(a, u.row + row / a.group, head * a.group + row % a.group, lane, all.o[rt], 1.0f / all.l[rt],
-                         live);
-        }
+        const int row = row0 + rt * 16 + lane % 16;
+        store_row<D>(a, u.row + row / a.group, head * a.group + row % a.group, lane, all.o[rt], 1.0f / all.l[rt],
+                     row < rows);
     }
 }
 
@@ -536,10 +728,10 @@ struct AttnShape {
 AttnShape attn_shape(int64_t num_units, int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads) {
     AttnShape s;
     s.max_rows = (max_new < kKvBlock ? max_new : kKvBlock) * (q_heads / kv_heads);
-    s.rt = s.max_rows <= 16 ? 1 : 2;
-    s.row_groups = (s.max_rows + 16 * s.rt - 1) / (16 * s.rt);
     s.max_blocks = (max_seq - 1) / kKvBlock;
     s.spans = (s.max_blocks + kSpan - 1) / kSpan + 1;
+    s.rt = s.max_rows <= 16 && s.spans > 1 ? 1 : 2;
+    s.row_groups = (s.max_rows + 16 * s.rt - 1) / (16 * s.rt);
     // Waves of the serial form; four per compute unit keep the memory and the matrix units busy.
     const int64_t waves = num_units * kv_heads * s.row_groups;
     s.split = s.spans > 1 && (s.max_rows <= 16 || waves < 1024);
@@ -551,19 +743,18 @@ int64_t partial_rows(const AttnShape& s, int64_t num_units, int64_t kv_heads) {
 }
 
 int64_t attn_blocks(const AttnShape& s, int64_t num_units, int64_t kv_heads) {
-    const int64_t jobs = s.split ? s.spans * s.row_groups : s.row_groups;
-    return num_units * kv_heads * ((jobs + kWaves - 1) / kWaves);
+    if (s.split) return num_units * kv_heads * ((s.spans * s.row_groups + kWaves - 1) / kWaves);
+    return (num_units + 1) / 2 * kv_heads * 2 * ((s.row_groups + kWaves - 1) / kWaves);
 }
 
 template <int D>
 hipError_t launch(const AttnArgs& a, const AttnShape& s, unsigned grid, hipStream_t st) {
     if (!s.split) {
-        if (s.rt == 1) attention_kernel<D, 1, false><<<grid, kWaves * 64, 0, st>>>(a);
-        else attention_kernel<D, 2, false><<<grid, kWaves * 64, 0, st>>>(a);
+        attention_tile_kernel<D><<<grid, kWaves * 64, 0, st>>>(a);
         return hipGetLastError();
     }
-    if (s.rt == 1) attention_kernel<D, 1, true><<<grid, kWaves * 64, 0, st>>>(a);
-    else attention_kernel<D, 2, true><<<grid, kWaves * 64, 0, st>>>(a);
+    if (s.rt == 1) attention_span_kernel<D, 1><<<grid, kWaves * 64, 0, st>>>(a);
+    else attention_span_kernel<D, 2><<<grid, kWaves * 64, 0, st>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t rows = (int64_t)a.num_units * a.kv_heads * a.max_rows;

@@ -129,10 +129,10 @@ def bf16(bits):
 def attention(q, units, table, codes, scales, recent, softmax_scale):
     """q float64 [T, Hq, D] -> o [T, Hq, D] (NaN where no unit has the row), and per output a bound on the error of a
     computation in fp32 whose probabilities are rounded to 11 bits (before the rounding of the result):
-        |v| weighted by the probabilities * (2^-11 + 2 e + N 2^-22) + N 2^-39 max |v|,
+        |v| weighted by the probabilities * (2^-11 + 2 e + N 2^-22) + N 2^-31 max |v|,
     2^-11 for the rounding of each probability; e for the relative error of an exponential, from the score's D products
-    and sums, its scaling and the exponential itself; N 2^-22 for the sums over N keys; 2^-39 for probabilities below
-    2^-28 of the largest, which are subnormal."""
+    and sums, its scaling and the exponential itself; N 2^-22 for the sums over N keys; 2^-31 for probabilities that are
+    subnormal in fp16 (below 2^-20 of the largest, or the less the smaller their block's values are)."""
     T, Hq, D = q.shape
     H = codes.shape[1]
     G = Hq // H
@@ -157,5 +157,5 @@ def attention(q, units, table, codes, scales, recent, softmax_scale):
                 size = (np.abs(qs) @ np.abs(k).T).max(axis=1, keepdims=True) * softmax_scale
                 e = (D + 8) * 2.0 ** -24 * size + 2.0 ** -21
                 bound[row + i, h * G:(h + 1) * G] = (p @ np.abs(v)) * (2.0 ** -11 + 2 * e + len(k) * 2.0 ** -22) + \
-                    len(k) * 2.0 ** -39 * np.abs(v).max()
+                    len(k) * 2.0 ** -31 * np.abs(v).max()
     return out, bound

@@ -113,3 +113,56 @@ def test_a_token_is_bitwise_the_same_in_every_cut(chunk):
     for beside in (0, 2):
         for a, b in zip(whole, run(cuts, beside)):
             assert torch.equal(a, b), (chunk, beside, (a != b).nonzero()[:4])
+
+
+@pytest.mark.parametrize("q_heads,kv_heads,head_dim", [(8, 8, 64), (8, 8, 128), (40, 8, 128), (24, 8, 64), (56, 8, 128)])
+def test_prompts_equal_the_same_prompts_alone(library, q_heads, kv_heads, head_dim):
+    """A batch of prompts and continuations (the serial kernel, units of one request in one thread block and of two)
+    against each request on its own (the split kernel): the same bits.  And the batch against the oracle on one
+    request of each kind."""
+    import torch
+    jf, R = library, 30
+    rng = np.random.default_rng(q_heads)
+    c = TwinCache(R, q_heads, kv_heads, head_dim, 400, 16, R * 700, 4)
+    past = rng.integers(0, 400, R)
+    past[:4] = 0, 64, 256, 63
+    lens = rng.integers(1, 400, R)
+    lens[3], lens[7] = 0, 1
+    rest = lambda n: (lens if n else past)
+    outs = []
+    for n in (0, 1):
+        new, T = rest(n).astype(np.int32), int(rest(n).sum())
+        p = jf.kv_plan(c.dev["state"], c.up(new), c.dev["free"], c.dev["head"], c.dev["table"], T, int(new.max()))
+        assert not p.status.any()
+        host, (q, k, v) = c.qkv(T)
+        jf.kv_append(k, v, p.units, c.dev["codes"], c.dev["scales"], c.dev["recent"])
+        if n:
+            break
+        c.dev["state"], c.dev["head"] = p.next_state, p.next_free
+    most = int((past + lens).max())
+    assert jf.attention_workspace(len(p.units), int(new.max()), most, q_heads, kv_heads, head_dim) == 0
+    o = jf.attention(q, p.units, c.dev["table"], c.dev["codes"], c.dev["scales"], c.dev["recent"],
+                     max_new=int(new.max()), max_seq=most)
+    units = p.units.cpu().numpy()
+    seen = set()
+    for r in range(R):
+        mine = p.units[torch.from_numpy(np.flatnonzero(units[:, 0] == r)).cuda()].contiguous()
+        if not len(mine):
+            continue
+        size = jf.attention_workspace(len(mine), int(new[r]), int(past[r] + new[r]), q_heads, kv_heads, head_dim)
+        assert (size > 0) == (past[r] + new[r] > 64)
+        alone = jf.attention(q, mine, c.dev["table"], c.dev["codes"], c.dev["scales"], c.dev["recent"],
+                             max_new=int(new[r]), max_seq=int(past[r] + new[r]))
+        rows = slice(int(new[:r].sum()), int(new[:r + 1].sum()))
+        assert torch.equal(o[rows].view(torch.int16), alone[rows].view(torch.int16)), r
+        kind = (min(int(new[r]), 65) // 64, int(past[r]) % 64 == 0)
+        if kind in seen or len(seen) > 2:
+            continue
+        seen.add(kind)
+        from kv_case import check_rows
+        down = lambda t: t.cpu().numpy()
+        local = mine.cpu().numpy().copy()
+        local[:, 3] -= rows.start
+        want, bound = c.orc.attention(c.orc.bf16(host[0][rows]), local, down(c.dev["table"]), down(c.dev["codes"]),
+                                      down(c.dev["scales"]), c.down_bits(c.dev["recent"]), head_dim ** -0.5)
+        check_rows(c.orc.bf16(c.down_bits(o[rows])), want, bound)
