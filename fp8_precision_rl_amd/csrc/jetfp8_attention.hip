@@ -18,6 +18,8 @@ typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 4;          // waves of a thread block; they share nothing but caches
 constexpr int kSpan = 4;           // cache blocks of a span, the unit of summation
+constexpr int kRun = 16;           // spans of a run, the unit of joining
+constexpr int kRunBlocks = kRun * kSpan;
 // The cache's probabilities enter the second product as fp16, in which the values' codes are exact.  A row's reference m
 // follows its running maximum only when that has grown by more than 2^8 (in 16 rows of fresh spans some maximum grows
 // with nearly every block, and following each would rescale the whole accumulator each time), so probabilities reach
@@ -35,7 +37,7 @@ struct AttnArgs {
     uint16_t* o;                   // may be null
     uint8_t* oq;                   // may be null
     float* os;
-    float* part_o;                 // split form: partial results of the spans
+    float* part_o;                 // partial results, [unit][kv head][part][row]
     float2* part_ml;
     int64_t ldq;
     float scale_log2;              // softmax scale * log2(e)
@@ -43,7 +45,8 @@ struct AttnArgs {
     int q_heads, kv_heads, group;  // group: query heads of a kv head
     int max_rows;                  // rows (token, query head) that a unit may have
     int row_groups;                // row groups of 16 RT rows that cover them
-    int spans;                     // split form: partial results per row, the own block's among them
+    int parts;                     // partial results that a row may have, its own block's among them
+    int runs;                      // tile kernel: runs, a thread block each
 };
 
 // Eight E4M3 codes -> bf16, exact.
@@ -231,7 +234,7 @@ __device__ __forceinline__ void load_queries(bf16x8 (&q)[RT][D / 32], const Attn
 
 // Takes the scores of a cache block's 64 keys (s, in units of c) into the rows' states and gives their probabilities,
 // times the values' share r, as operands of the second product.  START: the first block of a span, whose states are
-// empty and take its maximum as it is.
+// empty (whatever the registers hold) and take its maximum as it is.
 template <bool START, int D, int RT>
 __device__ __forceinline__ void take_block(Softmax<D, RT>& st, const v4f (&s)[RT][4], float c, float r, f16x8 (&p)[RT][2]) {
     float m[RT];
@@ -264,11 +267,21 @@ __device__ __forceinline__ void take_block(Softmax<D, RT>& st, const v4f (&s)[RT
             sum += e;
             p[rt][i / 8][i % 8] = (_Float16)e;
         }
-        st.l[rt] = fmaf(sum, inv_r, st.l[rt]);
+        st.l[rt] = START ? sum * inv_r : fmaf(sum, inv_r, st.l[rt]);
     }
 }
 
-// The unit's own block, bf16 with the causal mask, into an empty state.  keys, values: the block's operands, 64 lanes
+// Adds a block's product to the rows' accumulators (START: the accumulators begin with it).
+template <bool START, int D, int RT, typename T>
+__device__ __forceinline__ void add_values(Softmax<D, RT>& st, int t, const T& v, const T (&p)[RT][2], int k) {
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
+        st.o[rt][t] = mfma16(v, p[rt][k], START && k == 0 ? z : st.o[rt][t]);
+    }
+}
+
+// The unit's own block, bf16 with the causal mask, into an empty state (whatever the registers hold).  keys, values: the block's operands, 64 lanes
 // of 16 bytes each; AHEAD: the values are loaded before the scores are formed (from memory, not from LDS).
 template <bool AHEAD, int D, int RT>
 __device__ __forceinline__ void own_block(Softmax<D, RT>& st, const bf16x8 (&q)[RT][D / 32], float scale_log2,
@@ -304,6 +317,7 @@ __device__ __forceinline__ void own_block(Softmax<D, RT>& st, const bf16x8 (&q)[
         for (int i = 0; i < 16; ++i)
             if (i / 4 * 16 + lane / 16 * 4 + i % 4 > place[rt]) s[rt][i / 4][i % 4] = -INFINITY;
         st.m[rt] = top_score(s[rt]) * scale_log2;
+        st.l[rt] = 0.0f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const float e = __builtin_amdgcn_exp2f(fmaf(s[rt][i / 4][i % 4], scale_log2, -st.m[rt]));
@@ -354,11 +368,28 @@ __device__ __forceinline__ void own_block(Softmax<D, RT>& st, const bf16x8 (&q)[
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const bf16x8 x = __builtin_bit_cast(bf16x8, v[k]);
-                st.o[rt][t] = mfma16(x, p[rt][k], mfma16(x, rest[rt][k], st.o[rt][t]));
+                const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
+                st.o[rt][t] = mfma16(x, p[rt][k], mfma16(x, rest[rt][k], k ? st.o[rt][t] : z));
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) st.o[rt][t][i] = bad[rt][i] > 0.0f ? NAN : st.o[rt][t][i];
         }
+    }
+}
+
+// A state as one of the partial results of its rows (l summed over the column, o in units of ref).
+template <int D, int RT>
+__device__ __forceinline__ void store_part(const Softmax<D, RT>& st, float ref, const AttnArgs& a, int unit, int head,
+                                           int part, int row0, int rows, int lane) {
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const int row = row0 + rt * 16 + lane % 16;
+        if (row >= rows) continue;
+        const int64_t at = (((int64_t)unit * a.kv_heads + head) * a.parts + part) * a.max_rows + row;
+#pragma unroll
+        for (int t = 0; t < D / 16; ++t)
+            *reinterpret_cast<v4f*>(a.part_o + at * D + t * 16 + lane / 16 * 4) = st.o[rt][t] * ref;
+        if (lane < 16) a.part_ml[at] = make_float2(st.m[rt], st.l[rt]);
     }
 }
 
@@ -377,10 +408,11 @@ __device__ __forceinline__ const uint4* recent_block(const AttnArgs& a, int rece
 // probabilities.  Rounded below fp32 are only the probabilities (at most 2^-12 of each, an eighth of what bf16
 // would cost, whose error alone equals that of the results' own rounding), and the results.
 //
-// Blocks before the unit's own are complete and precede every query of the unit: no mask.  A row's sums run over its
-// blocks in ascending order in spans of 4 blocks, each span from its own zero state; the spans are joined in ascending
-// order, and the own block last.  Two kernels do this, with the same operations on a row whatever rows share the call,
-// so that a token's result is bitwise the same decoded alone, in a batch, or within a prompt:
+// Blocks before the unit's own are complete and precede every query of the unit: no mask.  A row's sums have one order.
+// Its blocks are taken in spans of 4, each from an empty state; the spans are joined in ascending order in runs of 16,
+// each run from an empty state; the runs are joined in ascending order, and the own block last.  Two kernels do this,
+// with the same operations on a row whatever rows share the call, so that a token's result is bitwise the same decoded
+// alone, in a batch, or within a prompt:
 //
 // attention_span_kernel gives every span of a row group a wave of its own and leaves the joining to
 // attention_join_kernel: for few rows, where the time is that of reading the cache and every wave must read.  Codes go
@@ -392,7 +424,7 @@ __global__ __launch_bounds__(kWaves * 64, RT == 1 ? 3 : 2) void attention_span_k
     constexpr int NK = D / 32;      // contraction steps of the score product
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int head = blockIdx.x % a.kv_heads;
-    const int jobs = a.spans * a.row_groups, chunks = (jobs + kWaves - 1) / kWaves;
+    const int jobs = a.parts * a.row_groups, chunks = (jobs + kWaves - 1) / kWaves;
     const int unit = blockIdx.x / a.kv_heads / chunks, job = blockIdx.x / a.kv_heads % chunks * kWaves + wave;
     if (job >= jobs) return;
     const int span = job / a.row_groups, row0 = job % a.row_groups * (16 * RT);
@@ -404,7 +436,6 @@ __global__ __launch_bounds__(kWaves * 64, RT == 1 ? 3 : 2) void attention_span_k
     bf16x8 q[RT][NK];
     load_queries<D, RT>(q, a, u, head, row0, rows, lane);
     Softmax<D, RT> st;
-    st.clear();
     float ref = 1.0f;
     if (span == own) {
         const uint4* mem = recent_block<D>(a, u.recent, head);
@@ -416,6 +447,7 @@ __global__ __launch_bounds__(kWaves * 64, RT == 1 ? 3 : 2) void attention_span_k
         const uint8_t* codes = a.codes + (int64_t)head * 2 * kKvBlock * D;
         const Span sp = load_span(a, a.table + (int64_t)u.request * a.width, a.scales + head * 2, first, last, last);
         ref = sp.ref;
+        if (!(sp.use & 1)) st.clear();
         Raw<D> kr, vr;
         load_raw(kr, codes + sp.at[0] * block_bytes, lane);
         load_raw(vr, codes + sp.at[0] * block_bytes + kKvBlock * D, lane);
@@ -445,28 +477,21 @@ __global__ __launch_bounds__(kWaves * 64, RT == 1 ? 3 : 2) void attention_span_k
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     const f16x8 v0 = widen_f16(vr.w[t].x, vr.w[t].y), v1 = widen_f16(vr.w[t].z, vr.w[t].w);
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt)
-                        st.o[rt][t] = mfma16(v1, p[rt][1], mfma16(v0, p[rt][0], st.o[rt][t]));
+                    if (i == 0) add_values<true>(st, t, v0, p, 0);
+                    else add_values<false>(st, t, v0, p, 0);
+                    add_values<false>(st, t, v1, p, 1);
                 }
             }
             if (more) load_raw(vr, next + kKvBlock * D, lane);
         }
     }
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const int row = row0 + rt * 16 + lane % 16;
-        const float l = column_sum(st.l[rt]);
-        if (row >= rows) continue;
-        const int64_t at = (((int64_t)unit * a.kv_heads + head) * a.spans + span) * a.max_rows + row;
-#pragma unroll
-        for (int t = 0; t < NT; ++t)
-            *reinterpret_cast<v4f*>(a.part_o + at * D + t * 16 + lane / 16 * 4) = st.o[rt][t] * ref;
-        if (lane < 16) a.part_ml[at] = make_float2(st.m[rt], l);
-    }
+    for (int rt = 0; rt < RT; ++rt) st.l[rt] = column_sum(st.l[rt]);
+    store_part(st, ref, a, unit, head, span, row0, rows, lane);
 }
 
-// attention_tile_kernel walks all spans of 128 rows in one block of four waves: for prompts, where the time is that of
+// attention_tile_kernel walks a run of 128 rows in one block of four waves, and where that is all (up to 4096 tokens
+// before the own block) finishes the rows, else leaves the joining of the runs to attention_join_kernel: for prompts, where the time is that of
 // the arithmetic.  Each wave widens a quarter of a block's codes into LDS, as operands, and all four read them there,
 // so that a code is widened once per 128 rows instead of once per 32 (the conversions would otherwise take a third
 // of the vector unit's time).  Two buffers, one barrier per block; a block's codes are loaded from memory two blocks
@@ -482,8 +507,8 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attention_tile_kernel(AttnArgs
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int head = blockIdx.x % a.kv_heads, chunks = (a.row_groups + kWaves - 1) / kWaves;
     const int pairs = (a.num_units + 1) / 2;
-    const int first_unit = 2 * (pairs - 1 - blockIdx.x / a.kv_heads / (2 * chunks));      // the longest rows first
-    const int chunk = blockIdx.x / a.kv_heads % (2 * chunks);
+    const int first_unit = 2 * (pairs - 1 - blockIdx.x / a.kv_heads / (2 * chunks * a.runs));   // the longest rows first
+    const int chunk = blockIdx.x / a.kv_heads % (2 * chunks), run = blockIdx.x / a.kv_heads / (2 * chunks) % a.runs;
     KvUnit us[2];
     int tiles[2];                          // row tiles of 32 that the two units have
 #pragma unroll
@@ -511,14 +536,19 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attention_tile_kernel(AttnArgs
         if (chunk - (which ? own_chunks : 0) >= (tiles[which] + kWaves - 1) / kWaves) return;
         end = us[which].block;
     }
+    const int begin = run * kRunBlocks;
+    if (run && begin >= end) return;
+    // Whether a unit's own block may be due here: with the run that ends before it.
+    const bool tail = max((two ? min(us[0].block, us[1].block) : end) - 1, 0) / kRunBlocks <= run;
+    end = min(end, begin + kRunBlocks);
     const KvUnit u = us[which];
-    const bool busy = tile < tiles[which];
-    const int row0 = tile * (16 * RT), rows = busy ? u.rows * a.group : 0, last = busy ? u.block : 0;
+    const int own_run = max(u.block - 1, 0) / kRunBlocks;         // the run whose thread block takes the own block too
+    const bool busy = tile < tiles[which] && run <= own_run;
+    const int row0 = tile * (16 * RT), rows = busy ? u.rows * a.group : 0, last = busy ? min(u.block, end) : 0;
 
     bf16x8 q[RT][NK];
     load_queries<D, RT>(q, a, u, head, row0, rows, lane);
     Softmax<D, RT> st, all;
-    st.clear();
     all.clear();
     auto join = [&](float ref) {
 #pragma unroll
@@ -526,12 +556,12 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attention_tile_kernel(AttnArgs
             float x, y;
             join_factors(all.m[rt], st.m[rt], x, y);
             all.l[rt] = fmaf(all.l[rt], x, column_sum(st.l[rt]) * y);
+            y *= ref;
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) all.o[rt][t][i] = fmaf(all.o[rt][t][i], x, st.o[rt][t][i] * ref * y);
+                for (int i = 0; i < 4; ++i) all.o[rt][t][i] = fmaf(all.o[rt][t][i], x, st.o[rt][t][i] * y);
         }
-        st.clear();
     };
 
     const int* entries = a.table + (int64_t)u.request * a.width;
@@ -557,14 +587,15 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attention_tile_kernel(AttnArgs
             vt[buf][n + 1][lane] = widen_f16(vr[i].z, vr[i].w);
         }
     };
-    if (end > 0) {
-        Span next = load_span(a, entries, scales, 0, last, end);
+    if (begin < end) {
+        Span next = load_span(a, entries, scales, begin, last, end);
         load(next.at[0]);
         store(0);
         load(next.at[1]);
         __syncthreads();
-        for (int first = 0; first < end; first += kSpan) {
+        for (int first = begin; first < end; first += kSpan) {
             const Span sp = next;
+            if (!(sp.use & 1)) st.clear();
             next = load_span(a, entries, scales, first + kSpan, last, end);
 #pragma unroll
             for (int i = 0; i < kSpan; ++i) {
@@ -594,8 +625,8 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attention_tile_kernel(AttnArgs
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             const f16x8 x = vt[buf][t * 2 + k][lane];
-#pragma unroll
-                            for (int rt = 0; rt < RT; ++rt) st.o[rt][t] = mfma16(x, p[rt][k], st.o[rt][t]);
+                            if (i == 0) add_values<true>(st, t, x, p, k);
+                            else add_values<false>(st, t, x, p, k);
                         }
                 }
                 __syncthreads();
@@ -607,7 +638,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attention_tile_kernel(AttnArgs
     const int owns[2] = {two ? us[0].recent : u.recent, us[1].recent};
 #pragma unroll
     for (int buf = 0; buf < 2; ++buf) {
-        if (buf && !two) break;
+        if (!tail || (buf && !two)) break;
         const uint4* mem = recent_block<D>(a, owns[buf], head) + wave * (NO / kWaves * 64) + lane;
 #pragma unroll
         for (int i = 0; i < NO / kWaves; ++i) {
@@ -617,9 +648,18 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attention_tile_kernel(AttnArgs
     }
     __syncthreads();
     if (!busy) return;
+    const int unit = first_unit + which, own_part = (u.block + kRunBlocks - 1) / kRunBlocks;
+    if (a.parts && run < own_part) store_part(all, 1.0f, a, unit, head, run, row0, rows, lane);
+    if (run < own_run) return;
     const int buf = two ? which : 0;
     own_block<false, D, RT>(st, q, a.scale_log2, u.offset, a.group, row0, &kt[buf][0][0],
                             reinterpret_cast<const uint4*>(&vt[buf][0][0]), lane);
+    if (a.parts) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) st.l[rt] = column_sum(st.l[rt]);
+        store_part(st, 1.0f, a, unit, head, own_part, row0, rows, lane);
+        return;
+    }
     join(1.0f);
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
@@ -629,14 +669,50 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attention_tile_kernel(AttnArgs
     }
 }
 
-// Joins the spans of one row (a wave each): 64 spans at a time, lane s forms the factors of span s from the running
-// maximum before it (a maximum has no rounding, so the prefix maxima may be formed in any order), then the spans'
-// results are added one after the other, as the serial form does.
-template <int D>
+// Joins n <= 16 consecutive partial results of a row to the state (M, L, o) of those before them.  Lane s forms the
+// factors of the s-th from the running maximum before it (a maximum has no rounding, so the prefix maxima may be formed
+// in any order); then they are added one after the other, as the tile kernel does.  ml: lane s's (m, l).
+template <int W>
+__device__ __forceinline__ void join_parts(const float2& ml, const float* from, int64_t step, int n, int lane, float& M,
+                                           float& L, float (&o)[W]) {
+    float v[kRun][W];
+#pragma unroll
+    for (int s = 0; s < kRun; ++s)
+#pragma unroll
+        for (int i = 0; i < W; ++i) v[s][i] = from[min(s, n - 1) * step + i];
+    float top = lane < n ? ml.x : -INFINITY;         // maximum of the parts up to this lane's
+#pragma unroll
+    for (int d = 1; d < kRun; d *= 2) {
+        const float y = __shfl_up(top, d);
+        if (lane >= d) top = fmaxf(top, y);
+    }
+    top = fmaxf(top, M);
+    float before = __shfl_up(top, 1), x, y;
+    if (lane == 0) before = M;
+    join_factors(before, ml.x, x, y);
+    const float ly = ml.y * y;
+    M = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(top), kRun - 1));
+#pragma unroll
+    for (int s = 0; s < kRun; ++s)
+        if (s < n) {
+            const float fx = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), s));
+            const float fy = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(y), s));
+            L = fmaf(L, fx, __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ly), s)));
+#pragma unroll
+            for (int i = 0; i < W; ++i) o[i] = fmaf(o[i], fx, v[s][i] * fy);
+        }
+}
+
+// Joins the partial results of a row: those of its spans (SPANS) to runs, the runs, and the own block's.  Bound by the
+// latency of a few dependent loads where there are few rows, so all of a run's parts are loaded at once and, where
+// rows may have several runs, WAVES waves form them at the same time.
+template <int D, bool SPANS, int WAVES>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
     constexpr int W = D / 64;       // channels of a lane
-    const int lane = threadIdx.x % 64;
-    int64_t job = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    __shared__ float run_o[WAVES > 1 ? kRun : 1][D];
+    __shared__ float2 run_ml[WAVES > 1 ? kRun : 1];
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    int64_t job = WAVES > 1 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 4 + wave;
     const int row = job % a.max_rows;
     job /= a.max_rows;
     const int head = job % a.kv_heads;
@@ -646,47 +722,52 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
     if (!unit_fits(u, a.requests, a.tokens, a.recent_blocks, a.num_blocks)) return;
     const int rows = u.rows * a.group;
     if (row >= rows || rows > a.max_rows || u.block > a.max_blocks) return;
-    const int n = (u.block + kSpan - 1) / kSpan + 1;
-    const int64_t base = ((int64_t)unit * a.kv_heads + head) * a.spans * a.max_rows + row;
-    const float* po = a.part_o + base * D + lane * W;
+    const int runs = (u.block + kRunBlocks - 1) / kRunBlocks, parts = SPANS ? (u.block + kSpan - 1) / kSpan : runs;
+    const int64_t base = ((int64_t)unit * a.kv_heads + head) * a.parts * a.max_rows + row;
     const int64_t step = (int64_t)a.max_rows * D;
+    const float* po = a.part_o + base * D + lane * W;
+    const float2* pml = a.part_ml + base;
+    auto load_ml = [&](int first, int n) {
+        return lane < n ? pml[(int64_t)(first + lane) * a.max_rows] : make_float2(-INFINITY, 0.0f);
+    };
+    const float2 own_ml = load_ml(parts, 1);
     float M = -INFINITY, L = 0.0f, o[W];
 #pragma unroll
     for (int i = 0; i < W; ++i) o[i] = 0.0f;
-    for (int s0 = 0; s0 < n; s0 += 64) {
-        const int m_n = min(64, n - s0);
-        float2 ml = make_float2(-INFINITY, 0.0f);
-        if (lane < m_n) ml = a.part_ml[base + (int64_t)(s0 + lane) * a.max_rows];
-        float top = ml.x;             // maximum of the spans up to this lane's
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const float y = __shfl_up(top, d);
-            if (lane >= d) top = fmaxf(top, y);
+    for (int r0 = 0; r0 < runs; r0 += kRun) {
+        const int n = min(kRun, runs - r0);
+        if (!SPANS) {
+            join_parts<W>(load_ml(r0, n), po + r0 * step, step, n, lane, M, L, o);
+            continue;
         }
-        top = fmaxf(top, M);
-        float before = __shfl_up(top, 1);
-        if (lane == 0) before = M;
-        float x, y;
-        join_factors(before, ml.x, x, y);
-        const float ly = ml.y * y;
-        M = __shfl(top, 63);
-        for (int s = 0; s < m_n; s += 8) {
-            float from[8][W];
+        for (int r = wave % WAVES; r < n; r += WAVES) {
+            const int s0 = (r0 + r) * kRun, m = min(kRun, parts - s0);
+            float rm = -INFINITY, rl = 0.0f, ro[W];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int i = 0; i < W; ++i) ro[i] = 0.0f;
+            join_parts<W>(load_ml(s0, m), po + s0 * step, step, m, lane, rm, rl, ro);
+            if (WAVES == 1) {
+                float x, y;
+                join_factors(M, rm, x, y);
+                L = fmaf(L, x, rl * y);
 #pragma unroll
-                for (int i = 0; i < W; ++i) from[j][i] = po[(s0 + min(s + j, m_n - 1)) * step + i];
+                for (int i = 0; i < W; ++i) o[i] = fmaf(o[i], x, ro[i] * y);
+            } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (s + j >= m_n) break;
-                const float fx = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), s + j));
-                const float fy = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(y), s + j));
-                L = fmaf(L, fx, __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ly), s + j)));
-#pragma unroll
-                for (int i = 0; i < W; ++i) o[i] = fmaf(o[i], fx, from[j][i] * fy);
+                for (int i = 0; i < W; ++i) run_o[WAVES > 1 ? r : 0][lane * W + i] = ro[i];
+                if (lane == 0) run_ml[WAVES > 1 ? r : 0] = make_float2(rm, rl);
             }
         }
+        if (WAVES > 1) {
+            __syncthreads();
+            if (wave == 0)
+                join_parts<W>(lane < n ? run_ml[WAVES > 1 ? lane : 0] : make_float2(-INFINITY, 0.0f), &run_o[0][lane * W],
+                              D, n, lane, M, L, o);
+            __syncthreads();
+        }
     }
+    if (WAVES > 1 && wave) return;
+    join_parts<W>(own_ml, po + parts * step, step, 1, lane, M, L, o);
     const float inv = 1.0f / L;
     const int token = u.row + row / a.group, qh = head * a.group + row % a.group;
     uint32_t y[W];
@@ -720,7 +801,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
 
 // The form of a call, from what the host knows of it.
 struct AttnShape {
-    int64_t max_rows, row_groups, spans, max_blocks;
+    int64_t max_rows, row_groups, runs, parts, max_blocks;
     int rt;
     bool split;
 };
@@ -729,36 +810,38 @@ AttnShape attn_shape(int64_t num_units, int64_t max_new, int64_t max_seq, int64_
     AttnShape s;
     s.max_rows = (max_new < kKvBlock ? max_new : kKvBlock) * (q_heads / kv_heads);
     s.max_blocks = (max_seq - 1) / kKvBlock;
-    s.spans = (s.max_blocks + kSpan - 1) / kSpan + 1;
-    s.rt = s.max_rows <= 16 && s.spans > 1 ? 1 : 2;
+    const int64_t spans = (s.max_blocks + kSpan - 1) / kSpan;
+    s.runs = (spans + kRun - 1) / kRun;
+    // Waves of the tile kernel; four per compute unit keep the memory and the matrix units busy.
+    const int64_t waves = num_units * kv_heads * ((s.max_rows + 31) / 32);
+    s.split = spans > 0 && (s.max_rows <= 16 || waves < 1024);
+    s.rt = s.split && s.max_rows <= 16 ? 1 : 2;
     s.row_groups = (s.max_rows + 16 * s.rt - 1) / (16 * s.rt);
-    // Waves of the serial form; four per compute unit keep the memory and the matrix units busy.
-    const int64_t waves = num_units * kv_heads * s.row_groups;
-    s.split = s.spans > 1 && (s.max_rows <= 16 || waves < 1024);
+    s.parts = s.split ? spans + 1 : s.runs > 1 ? s.runs + 1 : 0;
+    if (s.runs < 1) s.runs = 1;
     return s;
 }
 
 int64_t partial_rows(const AttnShape& s, int64_t num_units, int64_t kv_heads) {
-    return s.split ? num_units * kv_heads * s.spans * s.max_rows : 0;
+    return num_units * kv_heads * s.parts * s.max_rows;
 }
 
 int64_t attn_blocks(const AttnShape& s, int64_t num_units, int64_t kv_heads) {
-    if (s.split) return num_units * kv_heads * ((s.spans * s.row_groups + kWaves - 1) / kWaves);
-    return (num_units + 1) / 2 * kv_heads * 2 * ((s.row_groups + kWaves - 1) / kWaves);
+    if (s.split) return num_units * kv_heads * ((s.parts * s.row_groups + kWaves - 1) / kWaves);
+    return (num_units + 1) / 2 * kv_heads * 2 * ((s.row_groups + kWaves - 1) / kWaves) * s.runs;
 }
 
 template <int D>
 hipError_t launch(const AttnArgs& a, const AttnShape& s, unsigned grid, hipStream_t st) {
-    if (!s.split) {
-        attention_tile_kernel<D><<<grid, kWaves * 64, 0, st>>>(a);
-        return hipGetLastError();
-    }
-    if (s.rt == 1) attention_span_kernel<D, 1><<<grid, kWaves * 64, 0, st>>>(a);
+    if (!s.split) attention_tile_kernel<D><<<grid, kWaves * 64, 0, st>>>(a);
+    else if (s.rt == 1) attention_span_kernel<D, 1><<<grid, kWaves * 64, 0, st>>>(a);
     else attention_span_kernel<D, 2><<<grid, kWaves * 64, 0, st>>>(a);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || s.parts == 0) return e;
     const int64_t rows = (int64_t)a.num_units * a.kv_heads * a.max_rows;
-    attention_join_kernel<D><<<(unsigned)((rows + 3) / 4), 256, 0, st>>>(a);
+    if (!s.split) attention_join_kernel<D, false, 1><<<(unsigned)((rows + 3) / 4), 256, 0, st>>>(a);
+    else if (s.runs == 1) attention_join_kernel<D, true, 1><<<(unsigned)((rows + 3) / 4), 256, 0, st>>>(a);
+    else attention_join_kernel<D, true, 4><<<(unsigned)rows, 256, 0, st>>>(a);
     return hipGetLastError();
 }
 
@@ -808,7 +891,8 @@ hipError_t launch_attention(const uint16_t* q, int64_t ldq, int64_t tokens, cons
     a.group = (int)(q_heads / kv_heads);
     a.max_rows = (int)s.max_rows;
     a.row_groups = (int)s.row_groups;
-    a.spans = (int)s.spans;
+    a.parts = (int)s.parts;
+    a.runs = (int)s.runs;
     const unsigned grid = (unsigned)attn_blocks(s, num_units, kv_heads);
     return D == 64 ? launch<64>(a, s, grid, st) : launch<128>(a, s, grid, st);
 }
