@@ -178,41 +178,41 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, int token, int head
     }
 }
 
-// The scalars of a span.  The values' scales are taken relative to ref, the power of two at or below the largest of
-// the span, so that a block's share r (below 2) can be a factor of its probabilities and the span's products stay in
-// one accumulator; ref returns when the span ends.  The share enters the exponential's argument as its log2, and the
-// denominator is divided by it again.  (A block whose values are 2^-20 of another's of its span, or less, loses bits: an
-// absolute error below 2^-31 of that other block's values.  Shares are held at 2^-60 or more, so that the denominator
-// keeps its terms.)  A block id out of range has no keys: its bit of use is 0.
-struct Span {
-    int at[kSpan];
-    float c[kSpan], r[kSpan];
-    int use;
-    float ref;
+// The scalars of a run, block i in lane i.  The values' scales are taken relative to ref, the power of two at or below
+// the largest of the block's span, so that a block's share (below 2) can be a factor of its probabilities and the
+// span's products stay in one accumulator; ref returns when the span ends.  The share enters the exponential's argument
+// as its log2, and the denominator is divided by it again.  (A block whose values are 2^-20 of another's of its span, or
+// less, loses bits: an absolute error below 2^-31 of that other block's values.  Shares are held at 2^-60 or more, so
+// that the denominator keeps its terms.)  A block id out of range has no keys: its bit of use is 0.
+struct Run {
+    int at;                      // physical block
+    float c, log_r, inv_r, ref;  // the keys' scale * softmax scale * log2(e); the share's log2 and inverse
+    uint64_t use;
 };
 
-// Blocks first .. of a request, of which those before `last` are read and those before `end` (no less) are loaded.
-__device__ __forceinline__ Span load_span(const AttnArgs& a, const int* entries, const float* scales, int first,
-                                          int last, int end) {
-    Span s;
-    float top = 0.0f;
-    s.use = 0;
-#pragma unroll
-    for (int i = 0; i < kSpan; ++i) {
-        const int id = entries[max(min(first + i, end - 1), 0)];
-        s.at[i] = min(max(id, 0), a.num_blocks - 1);
-        const float* p = scales + (int64_t)s.at[i] * a.kv_heads * 2;
-        const bool here = first + i < last && id == s.at[i];
-        s.c[i] = p[0] * a.scale_log2;
-        s.r[i] = here ? p[1] : 0.0f;
-        s.use |= here ? 1 << i : 0;
-        top = fmaxf(top, s.r[i]);
-    }
-    const uint32_t e = min(max(__float_as_uint(top) >> 23, 1u), 253u);
+// Blocks first .. first + 63 of a request, of which those before `last` are used and those before `end` (no less) are
+// loaded.
+__device__ __forceinline__ Run load_run(const AttnArgs& a, int request, int head, int first, int last, int end, int lane) {
+    Run s;
+    const int id = a.table[(int64_t)request * a.width + max(min(first + lane, end - 1), 0)];
+    s.at = min(max(id, 0), a.num_blocks - 1);
+    const float2 scale = *reinterpret_cast<const float2*>(a.scales + ((int64_t)s.at * a.kv_heads + head) * 2);
+    const bool here = first + lane < last && id == s.at;
+    s.use = __ballot(here);
+    s.c = scale.x * a.scale_log2;
+    const float v = here ? scale.y : 0.0f;
+    float top = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, false)));
+    top = fmaxf(top, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(top), 0x4E, 0xF, 0xF, false)));
+    const uint32_t e = min(max(__float_as_uint(top) >> 23, 1u), 253u);      // scales are below 2^120
     s.ref = __uint_as_float(e << 23);
-#pragma unroll
-    for (int i = 0; i < kSpan; ++i) s.r[i] = fmaxf(s.r[i] * __uint_as_float((254u - e) << 23), 0x1p-60f);
+    const float r = fmaxf(v * __uint_as_float((254u - e) << 23), 0x1p-60f);
+    s.log_r = __builtin_amdgcn_logf(r);
+    s.inv_r = __builtin_amdgcn_rcpf(r);
     return s;
+}
+
+__device__ __forceinline__ float lane_value(float x, int i) {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), i));
 }
 
 // The queries of a wave's row tiles, rows (token, query head of the group) from row0 on; rows behind the last are 0.
@@ -232,42 +232,50 @@ __device__ __forceinline__ void load_queries(bf16x8 (&q)[RT][D / 32], const Attn
     }
 }
 
-// Takes the scores of a cache block's 64 keys (s, in units of c) into the rows' states and gives their probabilities,
-// times the values' share r, as operands of the second product.  START: the first block of a span, whose states are
-// empty (whatever the registers hold) and take its maximum as it is.
+// Takes the largest scores of a cache block's 64 keys (s, in units of c) into the rows' references.  START: the first
+// block of a span, whose states are empty (whatever the registers hold) and take its maximum as it is.
 template <bool START, int D, int RT>
-__device__ __forceinline__ void take_block(Softmax<D, RT>& st, const v4f (&s)[RT][4], float c, float r, f16x8 (&p)[RT][2]) {
+__device__ __forceinline__ void take_top(Softmax<D, RT>& st, const v4f (&s)[RT][4], float c) {
     float m[RT];
     bool grown = false;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
         m[rt] = fmaf(top_score(s[rt]), c, -kLead);
-        if (START) st.m[rt] = m[rt];
-        else grown |= m[rt] > st.m[rt] + kSlack;
-    }
-    if (!START && __any(grown)) {
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            const float to = m[rt] > st.m[rt] + kSlack ? m[rt] : st.m[rt];
-            const float f = __builtin_amdgcn_exp2f(st.m[rt] - to);       // 1 for the rows that keep theirs
-            st.l[rt] *= f;
-#pragma unroll
-            for (int t = 0; t < D / 16; ++t) st.o[rt][t] *= f;
-            st.m[rt] = to;
+        if (START) {
+            st.m[rt] = m[rt];
+            st.l[rt] = 0.0f;
+        } else {
+            grown |= m[rt] > st.m[rt] + kSlack;
         }
     }
-    const float log_r = __builtin_amdgcn_logf(r), inv_r = __builtin_amdgcn_rcpf(r);
+    if (START || !__any(grown)) return;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+        const float to = m[rt] > st.m[rt] + kSlack ? m[rt] : st.m[rt];
+        const float f = __builtin_amdgcn_exp2f(st.m[rt] - to);       // 1 for the rows that keep theirs
+        st.l[rt] *= f;
+#pragma unroll
+        for (int t = 0; t < D / 16; ++t) st.o[rt][t] *= f;
+        st.m[rt] = to;
+    }
+}
+
+// The probabilities of half a block's keys (32 k .. 32 k + 31), times the values' share, as an operand of the second
+// product; their sum goes into the denominator.
+template <int D, int RT>
+__device__ __forceinline__ void take_half(Softmax<D, RT>& st, const v4f (&s)[RT][4], float c, float log_r, float inv_r,
+                                          int k, f16x8 (&p)[RT][2]) {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
         const float base = log_r - st.m[rt];
         float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float e = __builtin_amdgcn_exp2f(fmaf(s[rt][i / 4][i % 4], c, base));
+        for (int j = 0; j < 8; ++j) {
+            const float e = __builtin_amdgcn_exp2f(fmaf(s[rt][2 * k + j / 4][j % 4], c, base));
             sum += e;
-            p[rt][i / 8][i % 8] = (_Float16)e;
+            p[rt][k][j] = (_Float16)e;
         }
-        st.l[rt] = START ? sum * inv_r : fmaf(sum, inv_r, st.l[rt]);
+        st.l[rt] = fmaf(sum, inv_r, st.l[rt]);
     }
 }
 
@@ -445,16 +453,17 @@ __global__ __launch_bounds__(kWaves * 64, RT == 1 ? 3 : 2) void attention_span_k
         const int first = span * kSpan, last = min(first + kSpan, u.block);
         const int64_t block_bytes = (int64_t)a.kv_heads * 2 * kKvBlock * D;
         const uint8_t* codes = a.codes + (int64_t)head * 2 * kKvBlock * D;
-        const Span sp = load_span(a, a.table + (int64_t)u.request * a.width, a.scales + head * 2, first, last, last);
-        ref = sp.ref;
-        if (!(sp.use & 1)) st.clear();
+        const Run run = load_run(a, u.request, head, first, last, last, lane);
+        ref = lane_value(run.ref, 0);
+        if (!(run.use & 1)) st.clear();
         Raw<D> kr, vr;
-        load_raw(kr, codes + sp.at[0] * block_bytes, lane);
-        load_raw(vr, codes + sp.at[0] * block_bytes + kKvBlock * D, lane);
+        const uint8_t* here = codes + __builtin_amdgcn_readlane(run.at, 0) * block_bytes;
+        load_raw(kr, here, lane);
+        load_raw(vr, here + kKvBlock * D, lane);
 #pragma unroll
         for (int i = 0; i < kSpan; ++i) {
             if (first + i >= last) break;
-            const uint8_t* next = codes + sp.at[i + 1 < kSpan ? i + 1 : i] * block_bytes;
+            const uint8_t* next = codes + __builtin_amdgcn_readlane(run.at, i + 1) * block_bytes;
             v4f s[RT][4];
 #pragma unroll
             for (int t = 0; t < 4; ++t)
@@ -470,10 +479,13 @@ __global__ __launch_bounds__(kWaves * 64, RT == 1 ? 3 : 2) void attention_span_k
                 }
             const bool more = i + 1 < kSpan && first + i + 1 < last;
             if (more) load_raw(kr, next, lane);
-            if (sp.use >> i & 1) {
+            if (run.use >> i & 1) {
                 f16x8 p[RT][2];
-                if (i == 0) take_block<true>(st, s, sp.c[i], sp.r[i], p);
-                else take_block<false>(st, s, sp.c[i], sp.r[i], p);
+                const float c = lane_value(run.c, i), log_r = lane_value(run.log_r, i), inv_r = lane_value(run.inv_r, i);
+                if (i == 0) take_top<true>(st, s, c);
+                else take_top<false>(st, s, c);
+                take_half(st, s, c, log_r, inv_r, 0, p);
+                take_half(st, s, c, log_r, inv_r, 1, p);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
                     const f16x8 v0 = widen_f16(vr.w[t].x, vr.w[t].y), v1 = widen_f16(vr.w[t].z, vr.w[t].w);
@@ -564,74 +576,91 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attention_tile_kernel(AttnArgs
         }
     };
 
-    const int* entries = a.table + (int64_t)u.request * a.width;
-    const float* scales = a.scales + head * 2;
     const int64_t block_bytes = (int64_t)a.kv_heads * 2 * kKvBlock * D;
     const uint8_t* codes = a.codes + (int64_t)head * 2 * kKvBlock * D + lane * 16 + wave * (NL * 1024);
-    uint4 kr[NL], vr[NL];
+    uint4 raw[2 * NL];               // a wave's share of a block: lines of the keys, then of the values
     auto load = [&](int at) {
         const uint8_t* p = codes + at * block_bytes;
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
-            kr[i] = *reinterpret_cast<const uint4*>(p + i * 1024);
-            vr[i] = *reinterpret_cast<const uint4*>(p + kKvBlock * D + i * 1024);
+            raw[i] = *reinterpret_cast<const uint4*>(p + i * 1024);
+            raw[NL + i] = *reinterpret_cast<const uint4*>(p + kKvBlock * D + i * 1024);
         }
     };
-    auto store = [&](int buf) {
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            const int n = 2 * (wave * NL + i);
-            kt[buf][n][lane] = widen(kr[i].x, kr[i].y);
-            kt[buf][n + 1][lane] = widen(kr[i].z, kr[i].w);
-            vt[buf][n][lane] = widen_f16(vr[i].x, vr[i].y);
-            vt[buf][n + 1][lane] = widen_f16(vr[i].z, vr[i].w);
+    auto store = [&](int buf, int i) {
+        const int n = 2 * (wave * NL + i % NL);
+        if (i < NL) {
+            kt[buf][n][lane] = widen(raw[i].x, raw[i].y);
+            kt[buf][n + 1][lane] = widen(raw[i].z, raw[i].w);
+        } else {
+            vt[buf][n][lane] = widen_f16(raw[i].x, raw[i].y);
+            vt[buf][n + 1][lane] = widen_f16(raw[i].z, raw[i].w);
         }
     };
     if (begin < end) {
-        Span next = load_span(a, entries, scales, begin, last, end);
-        load(next.at[0]);
-        store(0);
-        load(next.at[1]);
+        const Run sc = load_run(a, u.request, head, begin, last, end, lane);
+        load(__builtin_amdgcn_readlane(sc.at, 0));
+#pragma unroll
+        for (int i = 0; i < 2 * NL; ++i) store(0, i);
+        load(__builtin_amdgcn_readlane(sc.at, 1));
         __syncthreads();
-        for (int first = begin; first < end; first += kSpan) {
-            const Span sp = next;
-            if (!(sp.use & 1)) st.clear();
-            next = load_span(a, entries, scales, first + kSpan, last, end);
+        for (int first = 0; first < end - begin; first += kSpan) {
+            if (!(sc.use >> first & 1)) st.clear();
 #pragma unroll
             for (int i = 0; i < kSpan; ++i) {
-                if (first + i >= end) break;
+                const int b = first + i;
+                if (begin + b >= end) break;
                 const int buf = i % 2;
-                const bool here = sp.use >> i & 1;
+                // Operands come from LDS in a ring, kAhead reads under way before the first is used (left to itself
+                // the compiler reads each just before its use, and every read's latency is waited for); the next
+                // block's codes are widened and stored between the matrix instructions.
+                constexpr int kAhead = 3, kGroup = NO / 4;
+                bf16x8 kf[kAhead];
                 v4f s[RT][4];
+                auto read_k = [&](int f) { kf[f % kAhead] = kt[buf][f % 4 * NK + f / 4][lane]; };
 #pragma unroll
-                for (int t = 0; t < 4; ++t)
+                for (int f = 0; f < kAhead; ++f) read_k(f);
 #pragma unroll
-                    for (int k = 0; k < NK; ++k) {
-                        const bf16x8 x = kt[buf][t * NK + k][lane];
+                for (int h = 0; h < 4; ++h) {
+                    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                    for (int f = h * kGroup; f < (h + 1) * kGroup; ++f) {
 #pragma unroll
                         for (int rt = 0; rt < RT; ++rt) {
                             const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
-                            s[rt][t] = mfma16(x, q[rt][k], k ? s[rt][t] : z);
+                            s[rt][f % 4] = mfma16(kf[f % kAhead], q[rt][f / 4], f / 4 ? s[rt][f % 4] : z);
+                        }
+                        if (f + kAhead < NO) read_k(f + kAhead);
+                    }
+                    if (h < 2 * NL) store(buf ^ 1, h);          // block b + 1; nobody reads that buffer before the barrier
+                }
+                __builtin_amdgcn_sched_barrier(0);
+                load(__builtin_amdgcn_readlane(sc.at, min(b + 2, 63)));
+                if (sc.use >> b & 1) {
+                    f16x8 p[RT][2], vf[kAhead];
+                    const float c = lane_value(sc.c, b), log_r = lane_value(sc.log_r, b), inv_r = lane_value(sc.inv_r, b);
+                    if (i == 0) take_top<true>(st, s, c);
+                    else take_top<false>(st, s, c);
+                    take_half(st, s, c, log_r, inv_r, 0, p);
+                    auto read_v = [&](int f) { vf[f % kAhead] = vt[buf][f % NT * 2 + f / NT][lane]; };
+#pragma unroll
+                    for (int f = 0; f < kAhead; ++f) read_v(f);
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        __builtin_amdgcn_sched_barrier(0);
+                        if (h == 0) take_half(st, s, c, log_r, inv_r, 1, p);
+#pragma unroll
+                        for (int f = h * kGroup; f < (h + 1) * kGroup; ++f) {
+                            if (i == 0) add_values<true>(st, f % NT, vf[f % kAhead], p, f / NT);
+                            else add_values<false>(st, f % NT, vf[f % kAhead], p, f / NT);
+                            if (f + kAhead < NO) read_v(f + kAhead);
                         }
                     }
-                store(buf ^ 1);                                 // block i + 1; nobody reads that buffer before the barrier
-                load(i + 2 < kSpan ? sp.at[i + 2 < kSpan ? i + 2 : 0] : next.at[i + 2 < kSpan ? 0 : i + 2 - kSpan]);
-                if (here) {
-                    f16x8 p[RT][2];
-                    if (i == 0) take_block<true>(st, s, sp.c[i], sp.r[i], p);
-                    else take_block<false>(st, s, sp.c[i], sp.r[i], p);
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const f16x8 x = vt[buf][t * 2 + k][lane];
-                            if (i == 0) add_values<true>(st, t, x, p, k);
-                            else add_values<false>(st, t, x, p, k);
-                        }
+                    __builtin_amdgcn_sched_barrier(0);
                 }
                 __syncthreads();
             }
-            if (first < last) join(sp.ref);
+            if (begin + first < last) join(lane_value(sc.ref, first));
         }
     }
     // The own blocks, as they are, through the same buffers: the first unit's (or the only one's) and the second's.
