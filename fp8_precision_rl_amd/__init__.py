@@ -283,36 +283,42 @@ def jetfp8_gemm_wgrad(dyqT, dysT, xqT, xsT, dw_bf16, M: int, N: int, K: int, str
                                                      int(M), int(N), int(K), _stream(stream)))
 
 
-class _on:
-    """The launch of a call: its tensors' device made current, and the stream to enqueue on (the current stream of that
-    device unless one is given)."""
-
-    def __init__(self, device, stream):
-        import torch
-        self.guard = None
-        if device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(device)
-        self.stream = stream
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return _stream(self.stream)
-
-    def __exit__(self, *error):
-        if self.guard is not None:
-            self.guard.__exit__(*error)
+# The key/value cache's calls are made once per layer and decode step, so their marshalling is kept short: one function
+# checks an operand and returns its pointer, the raw stream is read without a stream object, and the helpers below do
+# not check again what they have just allocated.
+def _use(t, shape, dtype, name, device=None) -> int:
+    """Pointer of a contiguous device tensor of exactly this shape and dtype (on `device` when given)."""
+    _need(t, shape, dtype, name, device)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t.data_ptr()
 
 
-def _rows(t, shape, name, device=None):
+def _rows(t, shape, name, device):
     """A bf16 tensor [tokens, heads, head_dim] whose rows lie any distance apart (columns of a fused projection, say),
     each of them contiguous: its pointer and the distance in elements."""
-    torch = _torch_mod()
-    _need(t, shape, torch.bfloat16, name, device)
+    _need(t, shape, _torch_mod().bfloat16, name, device)
     T, H, D = shape
-    if (D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D):
+    row, head, one = t.stride()
+    if one != 1 or (H > 1 and head != D):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return t.data_ptr(), t.stride(0) if T > 1 else H * D
+    return t.data_ptr(), row if T > 1 else H * D
+
+
+def _call(name, device, stream, *args) -> None:
+    """Calls an entry point with the operands' device current, on `stream` or else that device's current stream."""
+    f = getattr(load_library(), name)
+    cuda = _torch_mod().cuda
+    if device.index != cuda.current_device():
+        with cuda.device(device):
+            return _call(name, device, stream, *args)
+    if stream is None:
+        st = _torch._C._cuda_getCurrentRawStream(device.index)
+    else:
+        st = _stream(stream)
+    status = f(*args, st)
+    if status != OK:
+        _check(name, status)
 
 
 def kv_max_units(tokens: int, requests: int) -> int:
@@ -322,57 +328,46 @@ def kv_max_units(tokens: int, requests: int) -> int:
     return n
 
 
+def _plan_inputs(state, new_lens, free_blocks, F, free_head, block_table, R, W):
+    i32 = _torch_mod().int32
+    p_state = _use(state, (R, 2), i32, "state")
+    dev = state.device
+    return (p_state, _use(new_lens, (R,), i32, "new_lens", dev),
+            _use(free_blocks, (F,), i32, "free_blocks", dev) if F else None, F,
+            _use(free_head, (1,), i32, "free_head", dev), _use(block_table, (R, W), i32, "block_table", dev))
+
+
 def jetfp8_kv_plan(state, new_lens, free_blocks, num_free: int, free_head, block_table, max_blocks: int, requests: int,
                    tokens: int, max_new: int, next_state, next_free, status, units, slots=None, stream=None) -> None:
-    L = load_library()
     torch = _torch_mod()
     i32, R, T, F, W = torch.int32, int(requests), int(tokens), int(num_free), int(max_blocks)
-    n = L.jetfp8_kv_max_units(T, R)
-    if n >= 0 and F >= 0 and W >= 1:
-        _need(state, (R, 2), i32, "state")
-        dev = state.device
-        _need(new_lens, (R,), i32, "new_lens", dev)
-        _need(free_head, (1,), i32, "free_head", dev)
-        if F:
-            _need(free_blocks, (F,), i32, "free_blocks", dev)
-        _need(block_table, (R, W), i32, "block_table", dev)
-        _need(next_state, (R, 2), i32, "next_state", dev)
-        _need(next_free, (1,), i32, "next_free", dev)
-        _need(status, (R,), i32, "status", dev)
-        _need(units, (n, KV_UNIT_WORDS), i32, "units", dev)
-        if slots is not None:
-            _need(slots, (T,), torch.int64, "slots", dev)
-    with _on(state.device, stream) as st:
-        st = L.jetfp8_kv_plan(_ptr(state), _ptr(new_lens), _ptr(free_blocks) if F else None, F, _ptr(free_head),
-                              _ptr(block_table), W, R, T, int(max_new), _ptr(next_state), _ptr(next_free),
-                              _ptr(status), _ptr(units), _ptr(slots), st)
-    _check("jetfp8_kv_plan", st)
+    n = kv_max_units(T, R)
+    inputs = _plan_inputs(state, new_lens, free_blocks, F, free_head, block_table, R, W)
+    dev = state.device
+    _call("jetfp8_kv_plan", dev, stream, *inputs, W, R, T, int(max_new), _use(next_state, (R, 2), i32, "next_state", dev),
+          _use(next_free, (1,), i32, "next_free", dev), _use(status, (R,), i32, "status", dev),
+          _use(units, (n, KV_UNIT_WORDS), i32, "units", dev),
+          None if slots is None else _use(slots, (T,), torch.int64, "slots", dev))
 
 
 def _kv_buffers(units, codes, scales, recent, kv_heads, head_dim):
-    """Checks a layer's cache and the units; their counts (units, physical blocks, recent blocks)."""
+    """Checks a layer's cache and the units: the device, the units' pointer and count, the cache's pointers and counts."""
     bf, u8, f32 = _bf16_u8_f32()
     n = kv_heads, 2, KV_BLOCK * head_dim
-    counts = tuple(t.shape[0] if getattr(t, "ndim", 0) else 0 for t in (units, codes, recent))
-    _need(codes, (counts[1],) + n, u8, "codes")
+    num_units, blocks, recent_blocks = (t.shape[0] if getattr(t, "ndim", 0) else 0 for t in (units, codes, recent))
+    p_codes = _use(codes, (blocks,) + n, u8, "codes")
     dev = codes.device
-    _need(units, (counts[0], KV_UNIT_WORDS), _torch_mod().int32, "units", dev)
-    _need(scales, (counts[1],) + n[:2], f32, "scales", dev)
-    _need(recent, (counts[2],) + n, bf, "recent", dev)
-    return counts
+    return (dev, (_use(units, (num_units, KV_UNIT_WORDS), _torch.int32, "units", dev), num_units),
+            (p_codes, _use(scales, (blocks, kv_heads, 2), f32, "scales", dev), blocks,
+             _use(recent, (recent_blocks,) + n, bf, "recent", dev), recent_blocks))
 
 
 def jetfp8_kv_append(k_bf16, v_bf16, units, codes, scales, recent_bf16, tokens: int, kv_heads: int, head_dim: int,
                      stream=None) -> None:
-    L = load_library()
     T, H, D = int(tokens), int(kv_heads), int(head_dim)
-    num_units, blocks, recent_blocks = _kv_buffers(units, codes, scales, recent_bf16, H, D)
-    k, ldk = _rows(k_bf16, (T, H, D), "k", codes.device)
-    v, ldv = _rows(v_bf16, (T, H, D), "v", codes.device)
-    with _on(codes.device, stream) as st:
-        st = L.jetfp8_kv_append(k, ldk, v, ldv, T, _ptr(units), num_units, H, D, _ptr(codes), _ptr(scales), blocks,
-                                _ptr(recent_bf16), recent_blocks, st)
-    _check("jetfp8_kv_append", st)
+    dev, work, cache = _kv_buffers(units, codes, scales, recent_bf16, H, D)
+    _call("jetfp8_kv_append", dev, stream, *_rows(k_bf16, (T, H, D), "k", dev), *_rows(v_bf16, (T, H, D), "v", dev), T,
+          *work, H, D, *cache)
 
 
 def attention_workspace(num_units: int, max_new: int, max_seq: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
@@ -387,30 +382,20 @@ def attention_workspace(num_units: int, max_new: int, max_seq: int, q_heads: int
 def jetfp8_attention(q_bf16, units, block_table, codes, scales, recent_bf16, tokens: int, max_new: int, max_seq: int,
                      q_heads: int, kv_heads: int, head_dim: int, softmax_scale: float, dst_o_bf16=None, dst_codes=None,
                      dst_scales=None, workspace=None, stream=None) -> None:
-    L = load_library()
     bf, u8, f32 = _bf16_u8_f32()
     T, Hq, H, D = int(tokens), int(q_heads), int(kv_heads), int(head_dim)
-    num_units, blocks, recent_blocks = _kv_buffers(units, codes, scales, recent_bf16, H, D)
-    dev = codes.device
-    q, ldq = _rows(q_bf16, (T, Hq, D), "q", dev)
+    dev, work, cache = _kv_buffers(units, codes, scales, recent_bf16, H, D)
     requests, width = block_table.shape if getattr(block_table, "ndim", 0) == 2 else (0, 0)
-    _need(block_table, (requests, width), _torch_mod().int32, "block_table", dev)
-    if dst_o_bf16 is not None:
-        _need(dst_o_bf16, (T, Hq, D), bf, "dst_o_bf16", dev)
-    if dst_codes is not None:
-        _need(dst_codes, (T, Hq * D), u8, "dst_codes", dev)
-    if dst_scales is not None:
-        _need(dst_scales, (Hq * D // 128, T), f32, "dst_scales", dev)
-    size = 0
+    out = (None if dst_o_bf16 is None else _use(dst_o_bf16, (T, Hq, D), bf, "dst_o_bf16", dev),
+           None if dst_codes is None else _use(dst_codes, (T, Hq * D), u8, "dst_codes", dev),
+           None if dst_scales is None else _use(dst_scales, (Hq * D // 128, T), f32, "dst_scales", dev))
+    space = (None, 0)
     if workspace is not None:
-        _need(workspace, workspace.shape, None, "workspace", dev)
-        size = workspace.numel() * workspace.element_size()
-    with _on(dev, stream) as st:
-        st = L.jetfp8_attention(q, ldq, T, _ptr(units), num_units, _ptr(block_table), requests, width, _ptr(codes),
-                                _ptr(scales), blocks, _ptr(recent_bf16), recent_blocks, int(max_new), int(max_seq), Hq,
-                                H, D, float(softmax_scale), _ptr(dst_o_bf16), _ptr(dst_codes), _ptr(dst_scales),
-                                _ptr(workspace), size, st)
-    _check("jetfp8_attention", st)
+        space = (_use(workspace, workspace.shape, None, "workspace", dev),
+                 workspace.numel() * workspace.element_size())
+    _call("jetfp8_attention", dev, stream, *_rows(q_bf16, (T, Hq, D), "q", dev), T, *work,
+          _use(block_table, (requests, width), _torch.int32, "block_table", dev), requests, width, *cache, int(max_new),
+          int(max_seq), Hq, H, D, float(softmax_scale), *out, *space)
 
 
 # ------------------------------------------------------------------------------------------------
@@ -567,12 +552,15 @@ def linear_backward(dy, x, wqT, ws, stream=None):
     return dx, dw
 
 
+_NO_CONTEXT = contextlib.nullcontext()
+
+
 def _memory_of(stream, device):
     """Where a helper allocates: the memory of the stream that the call runs on, so that what the helper frees when it
     returns (a workspace) is handed out again only behind the call."""
     import torch
     if stream is None:
-        return contextlib.nullcontext()
+        return _NO_CONTEXT
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     return torch.cuda.stream(stream)
@@ -602,15 +590,16 @@ def kv_plan(state, new_lens, free_blocks, free_head, block_table, tokens: int, m
     """Plans a step of `tokens` rows: state int32 [R, 2], new_lens int32 [R] (none above max_new), free_blocks int32
     [F] with free_head int32 [1] of them handed out, block_table int32 [R, max_blocks] (entries of the blocks that
     the step completes are written)."""
-    import torch
     R, W = block_table.shape
-    dev = block_table.device
-    new = lambda *shape: torch.empty(shape, dtype=torch.int32, device=dev)
+    n, F, T = kv_max_units(tokens, R), free_blocks.shape[0], int(tokens)
+    inputs = _plan_inputs(state, new_lens, free_blocks, F, free_head, block_table, R, W)
+    dev = state.device
     with _memory_of(stream, dev):
-        p = KVPlan(new(R, 2), new(1), new(R), new(kv_max_units(tokens, R), KV_UNIT_WORDS),
-                   torch.empty((tokens,), dtype=torch.int64, device=dev) if slot_map else None)
-    jetfp8_kv_plan(state, new_lens, free_blocks, free_blocks.shape[0], free_head, block_table, W, R, tokens, max_new,
-                   p.next_state, p.next_free, p.status, p.units, p.slots, stream)
+        new = state.new_empty
+        p = KVPlan(new((R, 2)), new((1,)), new((R,)), new((n, KV_UNIT_WORDS)),
+                   new((T,), dtype=_torch_mod().int64) if slot_map else None)
+    _call("jetfp8_kv_plan", dev, stream, *inputs, W, R, T, int(max_new), p.next_state.data_ptr(), p.next_free.data_ptr(),
+          p.status.data_ptr(), p.units.data_ptr(), p.slots.data_ptr() if slot_map else None)
     return p
 
 
@@ -625,18 +614,15 @@ def attention(q, units, block_table, codes, scales, recent, max_new: int, max_se
     """Causal attention of a step's new tokens, after kv_append: q bf16 [T, Hq, D] -> bf16 [T, Hq, D]; with quantize
     (D = 128) -> (codes [T, Hq * D], scales [Hq, T]) and, with return_o, the bf16 matrix as well.  softmax_scale:
     1 / sqrt(D) unless given.  Rows that belong to no unit are left unwritten."""
-    import torch
     T, Hq, D = q.shape
-    H = codes.shape[1]
-    dev = q.device
-    with _memory_of(stream, dev):
+    with _memory_of(stream, q.device):
         if workspace is None:
-            size = attention_workspace(units.shape[0], max_new, max_seq, Hq, H, D)
-            workspace = torch.empty((size,), dtype=torch.uint8, device=dev) if size else None
-        o = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=dev) if return_o or not quantize else None
-        c = torch.empty((T, Hq * D), dtype=torch.uint8, device=dev) if quantize else None
-        s = torch.empty((Hq * D // 128, T), dtype=torch.float32, device=dev) if quantize else None
-    jetfp8_attention(q, units, block_table, codes, scales, recent, T, max_new, max_seq, Hq, H, D,
+            size = attention_workspace(units.shape[0], max_new, max_seq, Hq, codes.shape[1], D)
+            workspace = codes.new_empty((size,)) if size else None
+        o = q.new_empty((T, Hq, D)) if return_o or not quantize else None
+        c = codes.new_empty((T, Hq * D)) if quantize else None
+        s = scales.new_empty((Hq * D // 128, T)) if quantize else None
+    jetfp8_attention(q, units, block_table, codes, scales, recent, T, max_new, max_seq, Hq, codes.shape[1], D,
                      D ** -0.5 if softmax_scale is None else softmax_scale, o, c, s, workspace, stream)
     if not quantize:
         return o

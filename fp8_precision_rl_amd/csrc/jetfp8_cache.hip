@@ -11,7 +11,7 @@ namespace {
 
 // ------------------------------------------------------------------------------------------------ plan
 constexpr int kPlanThreads = 256;
-constexpr int kPlanItems = 1024;   // units (and rows) written by a block
+constexpr int kPlanItems = 256;    // units and rows written by a block: one of each per thread
 
 struct PlanArgs {
     const int2* state;
@@ -56,7 +56,9 @@ __device__ __forceinline__ int first_above(const uint32_t* ends, int n, uint32_t
 // The step's layout from the requests' lengths: prefix sums over the requests of their new tokens, of the blocks they
 // complete, of their units and of the blocks between their first and last.  Bound by latency (a few KB of data and
 // two dependent sums), so one launch does it all: every block forms the same sums in LDS from the lengths, at
-// most 4096 requests, and then writes its own 1024 units and rows.  Nothing is passed between blocks.
+// most 4096 requests, and then writes one unit and one row per thread.  Nothing is passed between blocks.  A thread
+// takes PER consecutive requests, whose lengths it loads at once and keeps.
+template <int PER>
 __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(PlanArgs a) {
     extern __shared__ uint32_t sums[];              // [3][requests]
     __shared__ uint64_t wave_sums[kPlanThreads / 64];
@@ -64,72 +66,78 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(PlanArgs a) {
     uint32_t* row_end = sums;
     uint32_t* unit_end = sums + a.requests;
     uint32_t* seal_mid = unit_end + a.requests;     // completed blocks before the request << 16 | middle blocks before it
-    const int per = (a.requests + kPlanThreads - 1) / kPlanThreads;
-    const int r0 = min((int)threadIdx.x * per, a.requests), r1 = min(r0 + per, a.requests);
+    const int r0 = threadIdx.x * PER;
     const int head = min(max(*a.free_head, 0), a.num_free);
     if (threadIdx.x == 0) used = 0;
+    int2 s[PER];
+    int n[PER], st[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const int r = min(r0 + i, a.requests - 1);
+        s[i] = a.state[r];
+        n[i] = a.new_lens[r];
+    }
 
     // A request's lengths are in order if they are no less than 0, fit the call's bound and its row of the table.
-    auto in_order = [&](int2 s, int n) {
-        return s.x >= 0 && n >= 0 && n <= a.max_new && (int64_t)s.x + n <= (int64_t)kKvBlock * a.width &&
-               (s.y == 0 || s.y == 1);
-    };
     // Rows count for every request, so that the others' rows stay where the caller has put them; rows behind the
     // call's end all saturate there.  (4096 requests of at most 2^19 + 1 rows stay below 2^32.)
     uint64_t mine = 0;
-    for (int r = r0; r < r1; ++r) {
-        const int2 s = a.state[r];
-        const int n = a.new_lens[r];
-        const uint32_t seals = in_order(s, n) && n > 0 && n <= a.tokens ? (s.x + n) / kKvBlock - s.x / kKvBlock : 0;
-        mine += ((uint64_t)min(max(n, 0), a.tokens + 1) << 32) | seals;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        const bool in_order = s[i].x >= 0 && n[i] >= 0 && n[i] <= a.max_new &&
+                              (int64_t)s[i].x + n[i] <= (int64_t)kKvBlock * a.width && (s[i].y == 0 || s[i].y == 1);
+        st[i] = in_order ? JETFP8_KV_OK : JETFP8_KV_BAD_LENGTH;
+        const uint32_t seals = in_order && n[i] <= a.tokens ? (s[i].x + n[i]) / kKvBlock - s[i].x / kKvBlock : 0;
+        if (r0 + i < a.requests) mine += ((uint64_t)min(max(n[i], 0), a.tokens + 1) << 32) | seals;
     }
     uint64_t before = block_scan(mine, wave_sums) - mine;
     uint64_t units_mids = 0;
     uint32_t rows = before >> 32, seals = (uint32_t)before;
     int most = 0;
-    for (int r = r0; r < r1; ++r) {
-        const int2 s = a.state[r];
-        const int n = a.new_lens[r];
-        rows += min(max(n, 0), a.tokens + 1);
-        row_end[r] = rows;
-        int st = 0;
-        const uint32_t had = seals;
-        if (!in_order(s, n)) st = JETFP8_KV_BAD_LENGTH;
-        else if (rows > (uint32_t)a.tokens) st = JETFP8_KV_NO_ROWS;
-        else if (n > 0) {
-            const uint32_t need = (s.x + n) / kKvBlock - s.x / kKvBlock;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        if (r0 + i >= a.requests) break;
+        rows += min(max(n[i], 0), a.tokens + 1);
+        row_end[r0 + i] = rows;
+        seal_mid[r0 + i] = seals << 16;
+        if (st[i] != JETFP8_KV_OK) continue;
+        if (rows > (uint32_t)a.tokens) {
+            st[i] = JETFP8_KV_NO_ROWS;
+        } else if (n[i] > 0) {
+            const uint32_t need = (s[i].x + n[i]) / kKvBlock - s[i].x / kKvBlock;
             seals += need;
-            if (need > 0 && seals > (uint32_t)(a.num_free - head)) st = JETFP8_KV_NO_BLOCK;
-            else {
-                const int units = (s.x + n - 1) / kKvBlock - s.x / kKvBlock + 1;
+            if (need > 0 && seals > (uint32_t)(a.num_free - head)) {
+                st[i] = JETFP8_KV_NO_BLOCK;
+            } else {
+                const int units = (s[i].x + n[i] - 1) / kKvBlock - s[i].x / kKvBlock + 1;
                 units_mids += ((uint64_t)units << 32) | (uint32_t)max(units - 2, 0);
                 if (need > 0) most = (int)seals;
             }
         }
-        seal_mid[r] = (had << 16) | (uint32_t)st;   // its status, until the second sums are there
     }
     if (most > 0) atomicMax(&used, most);
     before = block_scan(units_mids, wave_sums) - units_mids;
     uint32_t unit = before >> 32, mid = (uint32_t)before;
-    for (int r = r0; r < r1; ++r) {
-        const int2 s = a.state[r];
-        const int n = a.new_lens[r];
-        const int st = seal_mid[r] & 0xFFFF;
-        const int units = st == 0 && n > 0 ? (s.x + n - 1) / kKvBlock - s.x / kKvBlock + 1 : 0;
-        seal_mid[r] = (seal_mid[r] & 0xFFFF0000u) | mid;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        if (r0 + i >= a.requests) break;
+        const bool live = st[i] == JETFP8_KV_OK && n[i] > 0;
+        const int units = live ? (s[i].x + n[i] - 1) / kKvBlock - s[i].x / kKvBlock + 1 : 0;
+        seal_mid[r0 + i] |= mid;
         unit += units;
         mid += max(units - 2, 0);
-        unit_end[r] = unit;
+        unit_end[r0 + i] = unit;
         if (blockIdx.x == 0) {
-            a.status[r] = st;
-            a.next_state[r] = st == 0 ? make_int2(s.x + n, units > 1 ? 1 - s.y : s.y) : s;
+            a.status[r0 + i] = st[i];
+            a.next_state[r0 + i] = live ? make_int2(s[i].x + n[i], units > 1 ? 1 - s[i].y : s[i].y) : s[i];
         }
     }
     __syncthreads();
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.next_free = head + used;
 
-    const int end = min(a.num_units, (int)(blockIdx.x + 1) * kPlanItems);
-    for (int u = blockIdx.x * kPlanItems + threadIdx.x; u < end; u += kPlanThreads) {
+    const int item = blockIdx.x * kPlanItems + threadIdx.x;
+    if (item < a.num_units) {
+        const int u = item;
         const int r = first_above(unit_end, a.requests, u);
         int4 lo = make_int4(-1, -1, -1, -1), hi = lo;
         if (r < a.requests) {
@@ -152,9 +160,8 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(PlanArgs a) {
         a.units[2 * u] = lo;
         a.units[2 * u + 1] = hi;
     }
-    if (!a.slots) return;
-    const int tokens = min(a.tokens, (int)(blockIdx.x + 1) * kPlanItems);
-    for (int t = blockIdx.x * kPlanItems + threadIdx.x; t < tokens; t += kPlanThreads) {
+    if (a.slots && item < a.tokens) {
+        const int t = item;
         const int r = first_above(row_end, a.requests, t);
         int64_t slot = -1;
         if (r < a.requests && unit_end[r] > (r ? unit_end[r - 1] : 0)) {
@@ -327,7 +334,10 @@ hipError_t launch_kv_plan(const int32_t* state, const int32_t* new_lens, const i
     a.num_free = (int)num_free;
     a.num_units = (int)kv_max_units(tokens, requests);
     const int items = slots ? a.tokens : a.num_units;    // never fewer rows than units
-    kv_plan_kernel<<<(items + kPlanItems - 1) / kPlanItems, kPlanThreads, 3 * requests * sizeof(uint32_t), st>>>(a);
+    const unsigned grid = (unsigned)((items + kPlanItems - 1) / kPlanItems), lds = (unsigned)(3 * requests * sizeof(uint32_t));
+    if (requests <= kPlanThreads) kv_plan_kernel<1><<<grid, kPlanThreads, lds, st>>>(a);
+    else if (requests <= 4 * kPlanThreads) kv_plan_kernel<4><<<grid, kPlanThreads, lds, st>>>(a);
+    else kv_plan_kernel<16><<<grid, kPlanThreads, lds, st>>>(a);
     return hipGetLastError();
 }
 
