@@ -126,6 +126,19 @@ __device__ __forceinline__ void join_factors(float& M, float m, float& a, float&
     M = top;
 }
 
+// Joins a row tile's state (m, l, o; o in units of ref) to that of the units before it.
+template <int NT>
+__device__ __forceinline__ void join_state(float& M, float& L, v4f (&O)[NT], float m, float l, const v4f (&o)[NT], float ref) {
+    float x, y;
+    join_factors(M, m, x, y);
+    L = fmaf(L, x, column_sum(l) * y);
+    y *= ref;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) O[t][i] = fmaf(O[t][i], x, o[t][i] * y);
+}
+
 // Sixteen codes of every operand row: a block's keys or values as a wave loads them.
 template <int D>
 struct Raw {
@@ -564,16 +577,7 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attention_tile_kernel(AttnArgs
     all.clear();
     auto join = [&](float ref) {
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            float x, y;
-            join_factors(all.m[rt], st.m[rt], x, y);
-            all.l[rt] = fmaf(all.l[rt], x, column_sum(st.l[rt]) * y);
-            y *= ref;
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) all.o[rt][t][i] = fmaf(all.o[rt][t][i], x, st.o[rt][t][i] * y);
-        }
+        for (int rt = 0; rt < RT; ++rt) join_state(all.m[rt], all.l[rt], all.o[rt], st.m[rt], st.l[rt], st.o[rt], ref);
     };
 
     const int64_t block_bytes = (int64_t)a.kv_heads * 2 * kKvBlock * D;
@@ -681,18 +685,22 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attention_tile_kernel(AttnArgs
     if (a.parts && run < own_part) store_part(all, 1.0f, a, unit, head, run, row0, rows, lane);
     if (run < own_run) return;
     const int buf = two ? which : 0;
-    own_block<false, D, RT>(st, q, a.scale_log2, u.offset, a.group, row0, &kt[buf][0][0],
-                            reinterpret_cast<const uint4*>(&vt[buf][0][0]), lane);
-    if (a.parts) {
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) st.l[rt] = column_sum(st.l[rt]);
-        store_part(st, 1.0f, a, unit, head, own_part, row0, rows, lane);
-        return;
-    }
-    join(1.0f);
+    for (int rt = 0; rt < RT; ++rt) {      // one row tile at a time: both would not fit the registers
+        const int tile_row0 = row0 + rt * 16, row = tile_row0 + lane % 16;
+        if (tile_row0 >= rows) break;
+        Softmax<D, 1> own;
+        bf16x8 q1[1][NK];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const int row = row0 + rt * 16 + lane % 16;
+        for (int k = 0; k < NK; ++k) q1[0][k] = q[rt][k];
+        own_block<false, D, 1>(own, q1, a.scale_log2, u.offset, a.group, tile_row0, &kt[buf][0][0],
+                               reinterpret_cast<const uint4*>(&vt[buf][0][0]), lane);
+        if (a.parts) {
+            own.l[0] = column_sum(own.l[0]);
+            store_part(own, 1.0f, a, unit, head, own_part, tile_row0, rows, lane);
+            continue;
+        }
+        join_state(all.m[rt], all.l[rt], all.o[rt], own.m[0], own.l[0], own.o[0], 1.0f);
         store_row<D>(a, u.row + row / a.group, head * a.group + row % a.group, lane, all.o[rt], 1.0f / all.l[rt],
                      row < rows);
     }
