@@ -287,17 +287,26 @@ def jetfp8_gemm_wgrad(dyqT, dysT, xqT, xsT, dw_bf16, M: int, N: int, K: int, str
 # checks an operand and returns its pointer, the raw stream is read without a stream object, and the helpers below do
 # not check again what they have just allocated.
 def _use(t, shape, dtype, name, device=None) -> int:
-    """Pointer of a contiguous device tensor of exactly this shape and dtype (on `device` when given)."""
-    _need(t, shape, dtype, name, device)
+    """Pointer of a contiguous device tensor of exactly this shape and dtype (dtype None: any), on the device of index
+    `device` when given."""
+    try:
+        if (t.dtype is dtype or dtype is None) and t.shape == shape and t.is_contiguous():
+            if t.get_device() == device or (device is None and t.is_cuda):
+                return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, shape, dtype, name)
     if not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor")
-    return t.data_ptr()
+    raise ValueError(f"{name}: on {t.device}, other operands on device {device}")
 
 
 def _rows(t, shape, name, device):
     """A bf16 tensor [tokens, heads, head_dim] whose rows lie any distance apart (columns of a fused projection, say),
     each of them contiguous: its pointer and the distance in elements."""
-    _need(t, shape, _torch_mod().bfloat16, name, device)
+    _need(t, shape, _torch_mod().bfloat16, name)
+    if t.get_device() != device:
+        raise ValueError(f"{name}: on {t.device}, other operands on device {device}")
     T, H, D = shape
     row, head, one = t.stride()
     if one != 1 or (H > 1 and head != D):
@@ -306,17 +315,14 @@ def _rows(t, shape, name, device):
 
 
 def _call(name, device, stream, *args) -> None:
-    """Calls an entry point with the operands' device current, on `stream` or else that device's current stream."""
+    """Calls an entry point with the operands' device (its index) current, on `stream` or else that device's current
+    stream."""
     f = getattr(load_library(), name)
-    cuda = _torch_mod().cuda
-    if device.index != cuda.current_device():
-        with cuda.device(device):
+    torch = _torch_mod()
+    if device != torch.cuda.current_device():
+        with torch.cuda.device(device):
             return _call(name, device, stream, *args)
-    if stream is None:
-        st = _torch._C._cuda_getCurrentRawStream(device.index)
-    else:
-        st = _stream(stream)
-    status = f(*args, st)
+    status = f(*args, torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream))
     if status != OK:
         _check(name, status)
 
@@ -331,7 +337,7 @@ def kv_max_units(tokens: int, requests: int) -> int:
 def _plan_inputs(state, new_lens, free_blocks, F, free_head, block_table, R, W):
     i32 = _torch_mod().int32
     p_state = _use(state, (R, 2), i32, "state")
-    dev = state.device
+    dev = state.get_device()
     return (p_state, _use(new_lens, (R,), i32, "new_lens", dev),
             _use(free_blocks, (F,), i32, "free_blocks", dev) if F else None, F,
             _use(free_head, (1,), i32, "free_head", dev), _use(block_table, (R, W), i32, "block_table", dev))
@@ -343,7 +349,7 @@ def jetfp8_kv_plan(state, new_lens, free_blocks, num_free: int, free_head, block
     i32, R, T, F, W = torch.int32, int(requests), int(tokens), int(num_free), int(max_blocks)
     n = kv_max_units(T, R)
     inputs = _plan_inputs(state, new_lens, free_blocks, F, free_head, block_table, R, W)
-    dev = state.device
+    dev = state.get_device()
     _call("jetfp8_kv_plan", dev, stream, *inputs, W, R, T, int(max_new), _use(next_state, (R, 2), i32, "next_state", dev),
           _use(next_free, (1,), i32, "next_free", dev), _use(status, (R,), i32, "status", dev),
           _use(units, (n, KV_UNIT_WORDS), i32, "units", dev),
@@ -356,7 +362,7 @@ def _kv_buffers(units, codes, scales, recent, kv_heads, head_dim):
     n = kv_heads, 2, KV_BLOCK * head_dim
     num_units, blocks, recent_blocks = (t.shape[0] if getattr(t, "ndim", 0) else 0 for t in (units, codes, recent))
     p_codes = _use(codes, (blocks,) + n, u8, "codes")
-    dev = codes.device
+    dev = codes.get_device()
     return (dev, (_use(units, (num_units, KV_UNIT_WORDS), _torch.int32, "units", dev), num_units),
             (p_codes, _use(scales, (blocks, kv_heads, 2), f32, "scales", dev), blocks,
              _use(recent, (recent_blocks,) + n, bf, "recent", dev), recent_blocks))
@@ -593,12 +599,11 @@ def kv_plan(state, new_lens, free_blocks, free_head, block_table, tokens: int, m
     R, W = block_table.shape
     n, F, T = kv_max_units(tokens, R), free_blocks.shape[0], int(tokens)
     inputs = _plan_inputs(state, new_lens, free_blocks, F, free_head, block_table, R, W)
-    dev = state.device
-    with _memory_of(stream, dev):
-        new = state.new_empty
-        p = KVPlan(new((R, 2)), new((1,)), new((R,)), new((n, KV_UNIT_WORDS)),
-                   new((T,), dtype=_torch_mod().int64) if slot_map else None)
-    _call("jetfp8_kv_plan", dev, stream, *inputs, W, R, T, int(max_new), p.next_state.data_ptr(), p.next_free.data_ptr(),
+    with _memory_of(stream, state.device):
+        new, like = state.new_empty, _torch_mod().empty_like
+        p = KVPlan(like(state), like(free_head), like(new_lens), new(n, KV_UNIT_WORDS),
+                   new(T, dtype=_torch.int64) if slot_map else None)
+    _call("jetfp8_kv_plan", state.get_device(), stream, *inputs, W, R, T, int(max_new), p.next_state.data_ptr(), p.next_free.data_ptr(),
           p.status.data_ptr(), p.units.data_ptr(), p.slots.data_ptr() if slot_map else None)
     return p
 
@@ -618,8 +623,8 @@ def attention(q, units, block_table, codes, scales, recent, max_new: int, max_se
     with _memory_of(stream, q.device):
         if workspace is None:
             size = attention_workspace(units.shape[0], max_new, max_seq, Hq, codes.shape[1], D)
-            workspace = codes.new_empty((size,)) if size else None
-        o = q.new_empty((T, Hq, D)) if return_o or not quantize else None
+            workspace = codes.new_empty(size) if size else None
+        o = q.new_empty(T, Hq, D) if return_o or not quantize else None
         c = codes.new_empty((T, Hq * D)) if quantize else None
         s = scales.new_empty((Hq * D // 128, T)) if quantize else None
     jetfp8_attention(q, units, block_table, codes, scales, recent, T, max_new, max_seq, Hq, codes.shape[1], D,
