@@ -17,8 +17,11 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 4;          // waves of a thread block; they share nothing but caches
-constexpr int kSpan = 4;           // cache blocks of a span, the unit of summation
-constexpr int kRun = 16;           // spans of a run, the unit of joining
+// Cache blocks of a span, the unit of summation, and spans of a run, the unit of joining.  Spans of 4 blocks measured
+// 4 % slower where the cache is long (256 requests up to 8192 tokens 421 against 405 us: twice the partial results)
+// and 6 % in the tile kernel (twice the joining), and 4 % faster for 32 requests up to 4096 tokens.
+constexpr int kSpan = 8;
+constexpr int kRun = 8;
 constexpr int kRunBlocks = kRun * kSpan;
 // The cache's probabilities enter the second product as fp16, in which the values' codes are exact.  A row's reference m
 // follows its running maximum only when that has grown by more than 2^8 (in 16 rows of fresh spans some maximum grows
@@ -144,10 +147,15 @@ template <int D>
 struct Raw {
     uint4 w[D / 16];
 };
-template <int D>
+template <bool ONCE, int D>
 __device__ __forceinline__ void load_raw(Raw<D>& r, const uint8_t* block, int lane) {
+    typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) r.w[i] = *reinterpret_cast<const uint4*>(block + i * 1024 + lane * 16);
+    for (int i = 0; i < D / 16; ++i) {
+        const u32x4* p = reinterpret_cast<const u32x4*>(block + i * 1024 + lane * 16);
+        const u32x4 x = ONCE ? __builtin_nontemporal_load(p) : *p;
+        r.w[i] = make_uint4(x.x, x.y, x.z, x.w);
+    }
 }
 
 // One query row's results: bf16 channels, and their 1x128 codes where they are wanted.
@@ -211,11 +219,13 @@ __device__ __forceinline__ Run load_run(const AttnArgs& a, int request, int head
     s.at = min(max(id, 0), a.num_blocks - 1);
     const float2 scale = *reinterpret_cast<const float2*>(a.scales + ((int64_t)s.at * a.kv_heads + head) * 2);
     const bool here = first + lane < last && id == s.at;
+    static_assert(kSpan == 8 && kRunBlocks == 64, "the maximum over a span is that of eight lanes, a run's blocks are the lanes");
     s.use = __ballot(here);
     s.c = scale.x * a.scale_log2;
     const float v = here ? scale.y : 0.0f;
     float top = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, false)));
     top = fmaxf(top, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(top), 0x4E, 0xF, 0xF, false)));
+    top = fmaxf(top, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(top), 0x141, 0xF, 0xF, false)));
     const uint32_t e = min(max(__float_as_uint(top) >> 23, 1u), 253u);      // scales are below 2^120
     s.ref = __uint_as_float(e << 23);
     const float r = fmaxf(v * __uint_as_float((254u - e) << 23), 0x1p-60f);
@@ -430,7 +440,7 @@ __device__ __forceinline__ const uint4* recent_block(const AttnArgs& a, int rece
 // would cost, whose error alone equals that of the results' own rounding), and the results.
 //
 // Blocks before the unit's own are complete and precede every query of the unit: no mask.  A row's sums have one order.
-// Its blocks are taken in spans of 4, each from an empty state; the spans are joined in ascending order in runs of 16,
+// Its blocks are taken in spans of 8, each from an empty state; the spans are joined in ascending order in runs of 8,
 // each run from an empty state; the runs are joined in ascending order, and the own block last.  Two kernels do this,
 // with the same operations on a row whatever rows share the call, so that a token's result is bitwise the same decoded
 // alone, in a batch, or within a prompt:
@@ -438,7 +448,8 @@ __device__ __forceinline__ const uint4* recent_block(const AttnArgs& a, int rece
 // attention_span_kernel gives every span of a row group a wave of its own and leaves the joining to
 // attention_join_kernel: for few rows, where the time is that of reading the cache and every wave must read.  Codes go
 // from memory to registers in whole lines (1 KB per load of a wave) and the next block's are loaded while this one's
-// are used; there is no LDS.
+// are used; there is no LDS.  With RT = 1 all rows are one wave's and nobody else reads its codes: the loads are marked
+// as not to be kept, which leaves the caches to the partial results (256 requests up to 8192 tokens: 477 -> 422 us).
 template <int D, int RT>
 __global__ __launch_bounds__(kWaves * 64, RT == 1 ? 3 : 2) void attention_span_kernel(AttnArgs a) {
     constexpr int NT = D / 16;      // output tiles, and loads of a block's keys or values
@@ -471,8 +482,8 @@ __global__ __launch_bounds__(kWaves * 64, RT == 1 ? 3 : 2) void attention_span_k
         if (!(run.use & 1)) st.clear();
         Raw<D> kr, vr;
         const uint8_t* here = codes + __builtin_amdgcn_readlane(run.at, 0) * block_bytes;
-        load_raw(kr, here, lane);
-        load_raw(vr, here + kKvBlock * D, lane);
+        load_raw<RT == 1>(kr, here, lane);
+        load_raw<RT == 1>(vr, here + kKvBlock * D, lane);
 #pragma unroll
         for (int i = 0; i < kSpan; ++i) {
             if (first + i >= last) break;
@@ -491,7 +502,7 @@ __global__ __launch_bounds__(kWaves * 64, RT == 1 ? 3 : 2) void attention_span_k
                     }
                 }
             const bool more = i + 1 < kSpan && first + i + 1 < last;
-            if (more) load_raw(kr, next, lane);
+            if (more) load_raw<RT == 1>(kr, next, lane);
             if (run.use >> i & 1) {
                 f16x8 p[RT][2];
                 const float c = lane_value(run.c, i), log_r = lane_value(run.log_r, i), inv_r = lane_value(run.inv_r, i);
@@ -507,7 +518,7 @@ __global__ __launch_bounds__(kWaves * 64, RT == 1 ? 3 : 2) void attention_span_k
                     add_values<false>(st, t, v1, p, 1);
                 }
             }
-            if (more) load_raw(vr, next + kKvBlock * D, lane);
+            if (more) load_raw<RT == 1>(vr, next + kKvBlock * D, lane);
         }
     }
 #pragma unroll
@@ -706,20 +717,21 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attention_tile_kernel(AttnArgs
     }
 }
 
-// Joins n <= 16 consecutive partial results of a row to the state (M, L, o) of those before them.  Lane s forms the
+// Joins n <= N consecutive partial results of a row to the state (M, L, o) of those before them.  Lane s forms the
 // factors of the s-th from the running maximum before it (a maximum has no rounding, so the prefix maxima may be formed
 // in any order); then they are added one after the other, as the tile kernel does.  ml: lane s's (m, l).
+constexpr int kJoin = kRun + 1;
 template <int W>
 __device__ __forceinline__ void join_parts(const float2& ml, const float* from, int64_t step, int n, int lane, float& M,
                                            float& L, float (&o)[W]) {
-    float v[kRun][W];
+    float v[kJoin][W];
 #pragma unroll
-    for (int s = 0; s < kRun; ++s)
+    for (int s = 0; s < kJoin; ++s)
 #pragma unroll
         for (int i = 0; i < W; ++i) v[s][i] = from[min(s, n - 1) * step + i];
     float top = lane < n ? ml.x : -INFINITY;         // maximum of the parts up to this lane's
 #pragma unroll
-    for (int d = 1; d < kRun; d *= 2) {
+    for (int d = 1; d < kJoin; d *= 2) {
         const float y = __shfl_up(top, d);
         if (lane >= d) top = fmaxf(top, y);
     }
@@ -728,21 +740,21 @@ __device__ __forceinline__ void join_parts(const float2& ml, const float* from, 
     if (lane == 0) before = M;
     join_factors(before, ml.x, x, y);
     const float ly = ml.y * y;
-    M = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(top), kRun - 1));
+    M = lane_value(top, kJoin - 1);
 #pragma unroll
-    for (int s = 0; s < kRun; ++s)
+    for (int s = 0; s < kJoin; ++s)
         if (s < n) {
-            const float fx = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), s));
-            const float fy = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(y), s));
-            L = fmaf(L, fx, __int_as_float(__builtin_amdgcn_readlane(__float_as_int(ly), s)));
+            const float fx = lane_value(x, s), fy = lane_value(y, s);
+            L = fmaf(L, fx, lane_value(ly, s));
 #pragma unroll
             for (int i = 0; i < W; ++i) o[i] = fmaf(o[i], fx, v[s][i] * fy);
         }
 }
 
-// Joins the partial results of a row: those of its spans (SPANS) to runs, the runs, and the own block's.  Bound by the
-// latency of a few dependent loads where there are few rows, so all of a run's parts are loaded at once and, where
-// rows may have several runs, WAVES waves form them at the same time.
+// Joins the partial results of a row: those of its spans (SPANS) to runs, the runs, and the own block's.  (One run's
+// spans and then the own block are one sequence: joining a state to an empty one changes nothing.)  Bound by the
+// latency of a few dependent loads, so all of a run's parts are loaded at once and, where rows are few and may have
+// several runs, WAVES waves form them at the same time.
 template <int D, bool SPANS, int WAVES>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
     constexpr int W = D / 64;       // channels of a lane
@@ -767,44 +779,47 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
     auto load_ml = [&](int first, int n) {
         return lane < n ? pml[(int64_t)(first + lane) * a.max_rows] : make_float2(-INFINITY, 0.0f);
     };
-    const float2 own_ml = load_ml(parts, 1);
     float M = -INFINITY, L = 0.0f, o[W];
 #pragma unroll
     for (int i = 0; i < W; ++i) o[i] = 0.0f;
-    for (int r0 = 0; r0 < runs; r0 += kRun) {
-        const int n = min(kRun, runs - r0);
-        if (!SPANS) {
-            join_parts<W>(load_ml(r0, n), po + r0 * step, step, n, lane, M, L, o);
-            continue;
+    if (!SPANS || runs <= 1) {
+        if (WAVES > 1 && wave) return;
+        for (int s0 = 0; s0 <= parts; s0 += kJoin) {
+            const int n = min(kJoin, parts + 1 - s0);
+            join_parts<W>(load_ml(s0, n), po + s0 * step, step, n, lane, M, L, o);
         }
-        for (int r = wave % WAVES; r < n; r += WAVES) {
-            const int s0 = (r0 + r) * kRun, m = min(kRun, parts - s0);
-            float rm = -INFINITY, rl = 0.0f, ro[W];
+    } else {
+        for (int r0 = 0; r0 < runs; r0 += kRun) {
+            const int n = min(kRun, runs - r0);
+            for (int r = wave % WAVES; r < n; r += WAVES) {
+                const int s0 = (r0 + r) * kRun, m = min(kRun, parts - s0);
+                float rm = -INFINITY, rl = 0.0f, ro[W];
 #pragma unroll
-            for (int i = 0; i < W; ++i) ro[i] = 0.0f;
-            join_parts<W>(load_ml(s0, m), po + s0 * step, step, m, lane, rm, rl, ro);
-            if (WAVES == 1) {
-                float x, y;
-                join_factors(M, rm, x, y);
-                L = fmaf(L, x, rl * y);
+                for (int i = 0; i < W; ++i) ro[i] = 0.0f;
+                join_parts<W>(load_ml(s0, m), po + s0 * step, step, m, lane, rm, rl, ro);
+                if (WAVES == 1) {
+                    float x, y;
+                    join_factors(M, rm, x, y);
+                    L = fmaf(L, x, rl * y);
 #pragma unroll
-                for (int i = 0; i < W; ++i) o[i] = fmaf(o[i], x, ro[i] * y);
-            } else {
+                    for (int i = 0; i < W; ++i) o[i] = fmaf(o[i], x, ro[i] * y);
+                } else {
 #pragma unroll
-                for (int i = 0; i < W; ++i) run_o[WAVES > 1 ? r : 0][lane * W + i] = ro[i];
-                if (lane == 0) run_ml[WAVES > 1 ? r : 0] = make_float2(rm, rl);
+                    for (int i = 0; i < W; ++i) run_o[WAVES > 1 ? r : 0][lane * W + i] = ro[i];
+                    if (lane == 0) run_ml[WAVES > 1 ? r : 0] = make_float2(rm, rl);
+                }
+            }
+            if (WAVES > 1) {
+                __syncthreads();
+                if (wave == 0)
+                    join_parts<W>(lane < n ? run_ml[WAVES > 1 ? lane : 0] : make_float2(-INFINITY, 0.0f),
+                                  &run_o[0][lane * W], D, n, lane, M, L, o);
+                __syncthreads();
             }
         }
-        if (WAVES > 1) {
-            __syncthreads();
-            if (wave == 0)
-                join_parts<W>(lane < n ? run_ml[WAVES > 1 ? lane : 0] : make_float2(-INFINITY, 0.0f), &run_o[0][lane * W],
-                              D, n, lane, M, L, o);
-            __syncthreads();
-        }
+        if (WAVES > 1 && wave) return;
+        join_parts<W>(load_ml(parts, 1), po + parts * step, step, 1, lane, M, L, o);
     }
-    if (WAVES > 1 && wave) return;
-    join_parts<W>(own_ml, po + parts * step, step, 1, lane, M, L, o);
     const float inv = 1.0f / L;
     const int token = u.row + row / a.group, qh = head * a.group + row % a.group;
     uint32_t y[W];
@@ -877,7 +892,7 @@ hipError_t launch(const AttnArgs& a, const AttnShape& s, unsigned grid, hipStrea
     if (e != hipSuccess || s.parts == 0) return e;
     const int64_t rows = (int64_t)a.num_units * a.kv_heads * a.max_rows;
     if (!s.split) attention_join_kernel<D, false, 1><<<(unsigned)((rows + 3) / 4), 256, 0, st>>>(a);
-    else if (s.runs == 1) attention_join_kernel<D, true, 1><<<(unsigned)((rows + 3) / 4), 256, 0, st>>>(a);
+    else if (s.runs == 1 || rows >= 8192) attention_join_kernel<D, true, 1><<<(unsigned)((rows + 3) / 4), 256, 0, st>>>(a);
     else attention_join_kernel<D, true, 4><<<(unsigned)rows, 256, 0, st>>>(a);
     return hipGetLastError();
 }

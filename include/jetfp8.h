@@ -266,7 +266,7 @@ int jetfp8_kv_append(const void* k_bf16, int64_t ldk, const void* v_bf16, int64_
  *   matrix [tokens][q_heads * 128], bit for bit: the activation of the output projection, quantized by the operator
  *   that produces it (Jet-RL explainers, "Schema de Quantification").
  * fp32 scores, softmax and sums; the probabilities are rounded to 11 bits or more for the second product.  A row's sums have one
- * fixed order (spans of 4 blocks, joined in ascending order, then its own block), so a token's result is bitwise the
+ * fixed order (spans of 8 blocks, joined in ascending order, then its own block), so a token's result is bitwise the
  * same decoded alone, in a batch, or within a prompt.
  * max_new: no request has more new tokens; max_seq: nor more tokens after the step.  A unit beyond either, or whose
  * fields do not fit the buffers, is left out (its rows stay as they were); a block id outside 0 .. num_blocks - 1
