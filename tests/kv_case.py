@@ -67,7 +67,7 @@ class TwinCache:
         self.orc.append(host[1], host[2], ref["units"], self.codes, self.scales, self.recent)
         self.jf.kv_append(dev[1], dev[2], got.units, self.dev["codes"], self.dev["scales"], self.dev["recent"])
         assert np.array_equal(self.dev["codes"].cpu().numpy(), self.codes), "codes"
-        assert np.array_equal(self.dev["scales"].cpu().numpy(), self.scales), "scales"
+        assert np.array_equal(self.dev["scales"].cpu().numpy().view(np.uint32), self.scales.view(np.uint32)), "scales"
         assert np.array_equal(self.down_bits(self.dev["recent"]), self.recent), "recent"
 
     def attend(self, ref, got, host, dev, max_new, max_seq, scale=None):

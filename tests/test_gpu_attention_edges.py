@@ -1,0 +1,413 @@
+"""Calls of the key/value cache's operators at their edges: fused codes, values of every code and scale, what masked and
+unused places may hold, bad ids, shared blocks, other streams, graphs, large offsets, the largest batch."""
+import numpy as np
+import pytest
+
+from kv_case import TwinCache, check_rows
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True, scope="module")
+def library():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import fp8_precision_rl_amd as jf
+    jf.load_library()
+    return jf
+
+
+def start(requests, past, q_heads, kv_heads, head_dim, tokens, seed, blocks=None, width=None):
+    """A cache whose requests hold `past` tokens each (appended in one call)."""
+    past = np.asarray(past)
+    width = width or int(past.max()) // 64 + 8
+    c = TwinCache(requests, q_heads, kv_heads, head_dim, blocks or int((past // 64).sum()) + 4 * requests, width,
+                  max(tokens, int(past.sum())), seed)
+    if past.any():
+        ref, got = c.plan(past, int(past.sum()), int(past.max()))
+        host, dev = c.qkv(int(past.sum()))
+        c.append(ref, got, host, dev)
+        c.advance(ref, got)
+    return c
+
+
+# ------------------------------------------------------------------------------------------------ fused codes
+@pytest.mark.parametrize("requests,past,new,q_heads,kv_heads", [(3, 0, 1, 4, 2), (3, 700, 1, 5, 1), (2, 600, 70, 8, 2),
+                                                                (40, 10, 150, 32, 8)])
+def test_codes_are_the_quantized_output(library, requests, past, new, q_heads, kv_heads):
+    """dst_codes, dst_scales: bit for bit the 1x128 quantization of the bf16 output, in every form of the call."""
+    import torch
+    jf = library
+    c = start(requests, [past] * requests, q_heads, kv_heads, 128, requests * new, 21)
+    T = requests * new
+    p = jf.kv_plan(c.dev["state"], c.up(np.full(requests, new, np.int32)), c.dev["free"], c.dev["head"], c.dev["table"], T, new)
+    _, (q, k, v) = c.qkv(T)
+    jf.kv_append(k, v, p.units, c.dev["codes"], c.dev["scales"], c.dev["recent"])
+    args = (q, p.units, c.dev["table"], c.dev["codes"], c.dev["scales"], c.dev["recent"], new, past + new)
+    codes, scales, o = jf.attention(*args, quantize=True)
+    plain = jf.attention(*args)
+    only = jf.attention(*args, quantize=True, return_o=False)
+    want = jf.quantize_rows(plain.view(T, -1))
+    assert torch.equal(o.view(torch.int16), plain.view(torch.int16))
+    for a, b, z in zip((codes, scales), want, only):
+        assert torch.equal(a, b) and torch.equal(z, b)
+
+
+# ------------------------------------------------------------------------------------------------ values
+def custom(c, r, blocks, spread, rng):
+    """Writes `blocks` complete blocks of every finite code and scales spread over 2^+-spread for request r."""
+    ids = c.free[r * blocks:(r + 1) * blocks]
+    codes = rng.integers(0, 254, c.codes[ids].shape).astype(np.uint8)
+    codes = np.where(codes >= 127, codes + 1, codes).astype(np.uint8)          # without 0x7F and 0xFF
+    scales = np.exp2(rng.uniform(-spread, spread, c.scales[ids].shape)).astype(np.float32)
+    scales[..., 0] = np.exp2(rng.uniform(-12, -8, scales[..., 0].shape))
+    if spread:
+        scales[-1, ..., 1] = 0.0
+        scales[0, ..., 1] = 2.0 ** -100
+    c.codes[ids], c.scales[ids], c.table[r, :blocks] = codes, scales, ids
+
+
+@pytest.mark.parametrize("new", [1, 70])
+@pytest.mark.parametrize("spread", [0, 6, 30])
+@pytest.mark.parametrize("head_dim", [64, 128])
+def test_every_code_and_scale(library, head_dim, spread, new):
+    rng = np.random.default_rng(spread + new)
+    c = TwinCache(2, 4, 2, head_dim, 60, 24, 2 * new, 3)
+    for r in range(2):
+        custom(c, r, 9 + 8 * r, spread, rng)
+    c.free = c.free[40:]
+    c.state = np.array([[9 * 64, 0], [17 * 64, 1]], np.int32)
+    for k in ("codes", "scales", "table", "state", "free"):
+        c.dev[k] = c.up(getattr(c, k))
+    c.step([new, new])
+
+
+@pytest.mark.parametrize("scale", [1e-6, 0.5, 30.0])
+@pytest.mark.parametrize("past,new", [(0, 66), (300, 3)])
+def test_softmax_scales(scale, past, new):
+    """From the mean of all values to the value of the best key alone."""
+    c = start(2, [past] * 2, 3, 1, 128, 2 * new, 8)
+    ref, got = c.plan([new, new], 2 * new, new)
+    host, dev = c.qkv(2 * new)
+    c.append(ref, got, host, dev)
+    c.attend(ref, got, host, dev, new, past + new, scale)
+
+
+def test_zero_keys_and_values():
+    c = start(1, [200], 2, 1, 64, 70, 8)
+    ref, got = c.plan([70], 70, 70)
+    host, dev = c.qkv(70)
+    host[1][:40], host[2][:60] = 0, 0x8000            # zeros, and negative zeros
+    dev = (dev[0], c.up_bits(host[1]), c.up_bits(host[2]))
+    c.append(ref, got, host, dev)
+    c.attend(ref, got, host, dev, 70, 270)
+
+
+@pytest.mark.parametrize("past,lens", [(0, [60]), (130, [40]), (576, [90]), (0, [64, 64, 64] * 80)])
+def test_masked_infinities_and_nan(library, past, lens):
+    """A token's non-finite key or value reaches the rows that see it and no others: those keep their bits."""
+    import torch
+    jf, R, T = library, len(lens), sum(lens)
+    H, Hq = 8, 16
+    c = start(R, [past] * R, Hq, H, 128, T, 5)
+    p = jf.kv_plan(c.dev["state"], c.up(np.asarray(lens, np.int32)), c.dev["free"], c.dev["head"], c.dev["table"], T, max(lens))
+    _, (q, k, v) = c.qkv(T)
+    outs = []
+    for bad in (False, True):
+        k2, v2 = k.clone(), v.clone()
+        at = lens[0] - 9                              # row of request 0
+        if bad:
+            v2[at, 1, 3], v2[at + 1, 2, 70], k2[at, 3, 5] = float("nan"), float("-inf"), float("inf")
+        jf.kv_append(k2, v2, p.units, c.dev["codes"], c.dev["scales"], c.dev["recent"])
+        o = jf.attention(q, p.units, c.dev["table"], c.dev["codes"], c.dev["scales"], c.dev["recent"], max(lens), past + max(lens))
+        outs.append(o.view(torch.int16).cpu().numpy().reshape(T, H, Hq // H, 128))
+    clean, dirty = outs
+    same = (clean == dirty)
+    last = (past + at) // 64 * 64 + 64 - past         # first row of request 0 that is in a later block
+    later = np.zeros(T, bool)
+    later[min(last, lens[0]):lens[0]] = True          # it reads codes quantized from non-finite values: unspecified
+    expect = np.ones(clean.shape, bool)
+    seen = slice(at, min(last, lens[0]))
+    expect[seen, 1, :, 3] = expect[seen, 3] = False
+    expect[at + 1:seen.stop, 2, :, 70] = False
+    expect[later] = same[later]
+    assert np.array_equal(same | ~expect, np.ones_like(same)), "a row that sees only finite values changed"
+    poisoned = c.orc.bf16(dirty.view(np.uint16)[seen])
+    assert np.isnan(poisoned[:, 1, :, 3]).all() and np.isnan(poisoned[1:, 2, :, 70]).all()
+
+
+@pytest.mark.parametrize("new", [1, 65])
+def test_unused_places_may_hold_anything(library, new):
+    """NaN in blocks that no request has, in rows behind the last and in the recent blocks' free places."""
+    import torch
+    c = start(2, [150, 70], 4, 2, 128, 2 * new + 4, 5)
+    ref, got = c.plan([new, new], 2 * new + 4, new)
+    used = set(ref["table"][ref["table"] >= 0].tolist())
+    idle = torch.tensor([b for b in range(len(c.codes)) if b not in used])
+    c.dev["codes"][idle] = 0x7F
+    c.dev["scales"][idle] = float("nan")
+    c.codes[idle.numpy()], c.scales[idle.numpy()] = 0x7F, np.nan
+    spare = [i for i in range(len(c.recent)) if i not in set(ref["units"][:, 2].tolist())]
+    c.dev["recent"][spare] = float("nan")
+    c.recent[spare] = c.down_bits(c.dev["recent"])[spare]
+    host, dev = c.qkv(2 * new + 4)
+    c.append(ref, got, host, dev)
+    c.attend(ref, got, host, dev, new, 150 + new)
+
+
+@pytest.mark.parametrize("bad", [[0], [3], [0, 1, 2, 3, 4, 5, 6, 7], [8, 9], list(range(10)), [1, 9]])
+@pytest.mark.parametrize("new", [1, 70])
+def test_block_ids_out_of_range_have_no_keys(library, bad, new):
+    c = start(1, [640], 4, 2, 128, new, 5)
+    ids = np.array([-1, len(c.codes), 2 ** 31 - 1, -2 ** 31] * 3)[:len(bad)]
+    ref, got = c.plan([new], new, new)
+    host, dev = c.qkv(new)
+    c.append(ref, got, host, dev)
+    c.table[0, bad] = ids
+    c.dev["table"] = c.up(c.table)
+    c.attend(ref, got, host, dev, new, 640 + new)
+
+
+@pytest.mark.parametrize("q_heads,head_dim,past", [(32, 128, 600), (8, 64, 1000), (24, 128, 4300)])
+def test_prompts_over_any_codes_and_ids(library, q_heads, head_dim, past):
+    """The prompts' kernel over every code, spread scales, zero blocks and ids out of range, bitwise equal to each request
+    on its own; its first rows against the oracle."""
+    import torch
+    jf, R, new = library, (6 if past > 4000 else 20), 150
+    rng = np.random.default_rng(past)
+    blocks = past // 64
+    c = TwinCache(R, q_heads, 8, head_dim, R * (blocks + 3), blocks + 4, R * new, 3)
+    for r in range(R):
+        custom(c, r, blocks, 8, rng)
+        bad = rng.random(blocks) < 0.15
+        bad[:16] |= r % 3 == 0
+        c.table[r, :blocks][bad] = rng.choice([-1, len(c.codes), 2 ** 31 - 1], bad.sum())
+    c.free = c.free[R * blocks:]
+    c.state = np.stack([np.full(R, blocks * 64), np.arange(R) % 2], 1).astype(np.int32)
+    for k in ("codes", "scales", "table", "state", "free"):
+        c.dev[k] = c.up(getattr(c, k))
+    ref, got = c.plan([new] * R, R * new, new)
+    host, dev = c.qkv(R * new)
+    c.append(ref, got, host, dev)
+    seq = blocks * 64 + new
+    args = (c.dev["table"], c.dev["codes"], c.dev["scales"], c.dev["recent"], new, seq)
+    o = jf.attention(dev[0], got.units, *args)
+    for r in range(R):
+        mine = np.flatnonzero(ref["units"][:, 0] == r)
+        alone = jf.attention(dev[0], got.units[torch.from_numpy(mine).cuda()].contiguous(), *args)
+        rows = slice(r * new, (r + 1) * new)
+        assert torch.equal(o[rows].view(torch.int16), alone[rows].view(torch.int16)), r
+    few = ref["units"][:1].copy()
+    few[0, 4] = 2
+    want, bound = c.orc.attention(c.orc.bf16(host[0][:2]), few, c.table, c.codes, c.scales, c.recent,
+                                  np.float64(np.float32(head_dim ** -0.5)))
+    check_rows(c.orc.bf16(c.down_bits(o[:2])), want, bound)
+
+
+def test_units_that_do_not_fit_are_left_out(library):
+    """Records that point outside the buffers, beyond max_new or beyond max_seq: nothing of them is read or written."""
+    import torch
+    jf = library
+    c = start(3, [100, 200, 300], 4, 2, 64, 30, 5)
+    ref, got = c.plan([10, 10, 10], 30, 10)
+    host, dev = c.qkv(30)
+    for field, value in ((0, 3), (0, -2), (1, -1), (1, 1 << 20), (2, len(c.recent)), (2, -1), (3, 21), (3, -1), (4, 0),
+                         (4, 65), (4, 2 ** 31 - 1), (5, 60), (5, -1), (6, len(c.codes)), (6, -2)):
+        units = ref["units"].copy()
+        units[1, field] = value
+        dropped = units.copy()
+        if field > 1 or value < 0 or value == 3:
+            dropped[1] = -1
+        for append in (True, False):
+            if append and field in (0, 1) and value >= 0:
+                continue                      # append asks neither for the request's nor the block's number
+            before = [c.dev[k].clone() for k in ("codes", "scales", "recent")]
+            o = torch.full((30, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+            outs = []
+            for u in (units, dropped if field != 1 or value < 0 else np.delete(units, 1, 0)):
+                u = c.up(u)
+                cache = [b.clone() for b in before]
+                if append:
+                    jf.kv_append(dev[1], dev[2], u, *cache)
+                    outs.append(cache)
+                else:
+                    ws = torch.zeros(1 << 22, dtype=torch.uint8, device="cuda")
+                    out = o.clone()
+                    jf.jetfp8_attention(dev[0], u, c.dev["table"], *before, 30, 10, 310, 4, 2, 64, 0.1, out, workspace=ws)
+                    outs.append([out])
+            for a, b in zip(*outs):
+                assert torch.equal(a.view(torch.uint8), b.view(torch.uint8)), (field, value, append)
+    # bounds below what the requests have: their rows stay
+    jf.kv_append(dev[1], dev[2], got.units, c.dev["codes"], c.dev["scales"], c.dev["recent"])
+    for max_new, max_seq in ((9, 400), (10, 192), (10, 300)):
+        out = torch.full((30, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+        ws = torch.zeros(1 << 22, dtype=torch.uint8, device="cuda")
+        jf.jetfp8_attention(dev[0], got.units, c.dev["table"], c.dev["codes"], c.dev["scales"], c.dev["recent"], 30,
+                            max_new, max_seq, 4, 2, 64, 0.1, out, workspace=ws)
+        kept = [bool((out[10 * r:10 * r + 10] == 7.0).all()) for r in range(3)]
+        assert kept == [max_new < 10 or s // 64 > (max_seq - 1) // 64 for s in (100, 200, 300)]
+
+
+# ------------------------------------------------------------------------------------------------ steps
+def test_refused_requests_and_padding(library):
+    """A step in which requests are refused: their rows stay, the others are right."""
+    c = start(4, [100, 60, 0, 30], 4, 2, 64, 80, 5, blocks=3, width=3)
+    ref, out = c.step([5, 10, 40, 9], pad=6, max_new=39)
+    assert list(ref["status"]) == [0, 4, 1, 0] or list(ref["status"]) == [0, 0, 1, 0]
+
+
+def test_requests_share_a_prompt(library):
+    """Several rollouts of one prompt: the same physical blocks in each row of the table, each its own unfinished block."""
+    c = start(1, [330], 8, 2, 128, 40, 5, blocks=40)
+    R = 5
+    state, table = np.repeat(c.state, R, 0), np.repeat(c.table, R, 0)
+    recent = c.recent.copy()
+    c.recent = np.concatenate([np.repeat(recent[:2][None], R, 0).reshape(2 * R, *recent.shape[1:]), recent[2:]])
+    c.R, c.state, c.table = R, state, table
+    c.dev["recent"] = c.up_bits(c.recent)
+    for k in ("state", "table"):
+        c.dev[k] = c.up(getattr(c, k))
+    for lens in ([1] * R, [3, 0, 70, 1, 20], [1] * R):
+        c.step(lens)
+
+
+def test_single_rows_and_strides(library):
+    """One token, one head; rows a wide pitch apart; heads that are not contiguous are refused."""
+    import torch
+    jf = library
+    c = TwinCache(1, 1, 1, 64, 4, 4, 64, 1)
+    c.step([1])
+    c.step([63])
+    wide = torch.randn((4, 9, 64), device="cuda").to(torch.bfloat16)
+    p = jf.kv_plan(c.dev["state"], c.up(np.array([4], np.int32)), c.dev["free"], c.dev["head"], c.dev["table"], 4, 4)
+    cache = (c.dev["codes"], c.dev["scales"], c.dev["recent"])
+    jf.kv_append(wide[:, 3:4], wide[:, 8:9], p.units, *cache)
+    a = jf.attention(wide[:, 5:6], p.units, c.dev["table"], *cache, max_new=4, max_seq=68)
+    jf.kv_append(wide[:, 3:4].contiguous(), wide[:, 8:9].contiguous(), p.units, *cache)
+    b = jf.attention(wide[:, 5:6].contiguous(), p.units, c.dev["table"], *cache, max_new=4, max_seq=68)
+    assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    with pytest.raises(ValueError):
+        jf.attention(wide[:, ::2][:, :2], p.units, c.dev["table"], *cache, max_new=4, max_seq=68)
+    with pytest.raises(ValueError):
+        jf.kv_append(wide[:, 3:4, ::1].transpose(0, 1)[:, :1].transpose(1, 2), wide[:1, 3:4], p.units, *cache)
+    with pytest.raises(TypeError):
+        jf.attention(wide[:, 5:6].float(), p.units, c.dev["table"], *cache, max_new=4, max_seq=68)
+    with pytest.raises(ValueError):
+        jf.attention(wide[:, 5:6], p.units.t().contiguous().t(), c.dev["table"], *cache, max_new=4, max_seq=68)
+    with pytest.raises(ValueError):
+        jf.attention(wide[:, 5:6], p.units, c.dev["table"].cpu(), *cache, max_new=4, max_seq=68)
+
+
+def test_streams(library):
+    """Two caches on two streams at once, by stream object and by handle, against the same calls one by one."""
+    import torch
+    jf = library
+    cs = [start(6, [700 + 40 * i] * 6, 8, 2, 128, 12, 30 + i) for i in range(2)]
+    ps = [jf.kv_plan(c.dev["state"], c.up(np.full(6, 2, np.int32)), c.dev["free"], c.dev["head"], c.dev["table"], 12, 2) for c in cs]
+    ins = [c.qkv(12)[1] for c in cs]
+
+    def one(i, stream):
+        c, p, (q, k, v) = cs[i], ps[i], ins[i]
+        cache = (c.dev["codes"], c.dev["scales"], c.dev["recent"])
+        jf.kv_append(k, v, p.units, *cache, stream=stream)
+        return jf.attention(q, p.units, c.dev["table"], *cache, max_new=2, max_seq=800, stream=stream)
+
+    want = [one(i, None) for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(20):
+        for i in range(2):
+            got[i].append(one(i, streams[i] if i else streams[i].cuda_stream))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(g.view(torch.int16), want[i].view(torch.int16)) for g in got[i])
+
+
+@pytest.mark.parametrize("new", [1, 3])
+def test_a_decode_step_in_a_graph(library, new):
+    """Plan, append and attention captured once and replayed while the lengths move on, against the same steps outside
+    (a second cache), with eager work in between."""
+    import torch
+    jf, R, steps = library, 3, 70 // new
+    a, b = (start(R, [100, 62, 0], 8, 2, 128, R * new, 3, blocks=60, width=12) for _ in range(2))
+    lens = torch.full((R,), new, dtype=torch.int32, device="cuda")
+    T, seq = R * new, 12 * 64
+    q, k, v = (x.clone() for x in a.qkv(T)[1])
+
+    def step(c):
+        d = c.dev
+        p = jf.kv_plan(d["state"], lens, d["free"], d["head"], d["table"], T, new)
+        jf.kv_append(k, v, p.units, d["codes"], d["scales"], d["recent"])
+        o = jf.attention(q, p.units, d["table"], d["codes"], d["scales"], d["recent"], new, seq)
+        d["state"].copy_(p.next_state)
+        d["head"].copy_(p.next_free)
+        return o
+
+    keep = {n: t.clone() for n, t in a.dev.items()}
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(a)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(a)
+    for n, t in keep.items():
+        a.dev[n].copy_(t)
+    for i in range(steps):
+        for x in (q, k, v):
+            x.copy_(torch.randn(x.shape, device="cuda"))
+        graph.replay()
+        want = step(b)
+        torch.cuda.synchronize()
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16)), i
+    for n in ("state", "head", "table", "codes", "scales", "recent"):
+        assert torch.equal(a.dev[n].view(torch.uint8), b.dev[n].view(torch.uint8)), n
+
+
+# ------------------------------------------------------------------------------------------------ sizes
+def test_offsets_beyond_32_bits(library):
+    """A cache of 5 GiB: its last blocks are written and read like the first."""
+    import torch
+    jf = library
+    H, D, N = 8, 128, 40 * 1024
+    codes, scales, recent = jf.kv_cache(N, 1, 300, H, D)
+    small = jf.kv_cache(8, 1, 300, H, D)
+    x = torch.randn((300, 4 * H, D), device="cuda").to(torch.bfloat16)
+    outs = []
+    for cache, free in (((codes, scales, recent), [N - 1, N - 2, N - 33, N - 4000]), (small, [5, 3, 1, 0])):
+        table = torch.full((1, 8), -1, dtype=torch.int32, device="cuda")
+        i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+        p = jf.kv_plan(i32([[0, 0]]), i32([300]), i32(free), i32([0]), table, 300, 300)
+        jf.kv_append(x[:, :H], x[:, H:2 * H], p.units, *cache)
+        outs.append((jf.attention(x[:, 2 * H:], p.units, table, *cache, max_new=300, max_seq=300),
+                     cache[0][torch.tensor(free)], cache[1][torch.tensor(free)]))
+    assert int(codes[:N - 4000].any()) == 0
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+
+
+def test_the_largest_batch(library):
+    """4096 requests of one token each, in blocks that fill at every place."""
+    import torch
+    jf, R = library, 4096
+    c = TwinCache(R, 2, 1, 64, 2 * R, 3, R, 6)
+    c.state = np.stack([np.arange(R) % 130, np.arange(R) % 2], 1).astype(np.int32)
+    c.table[:, :2] = np.arange(2 * R).reshape(R, 2)
+    c.free = np.arange(2 * R, dtype=np.int32)[::-1].copy()
+    for k in ("state", "table", "free"):
+        c.dev[k] = c.up(getattr(c, k))
+    ref, got = c.plan(np.ones(R, int), R, 1)
+    host, dev = c.qkv(R)
+    o = jf.attention(dev[0], got.units, c.dev["table"], c.dev["codes"], c.dev["scales"], c.dev["recent"], 1, 131)
+    rows = np.arange(0, R, 111)
+    units = ref["units"][rows]
+    want, bound = c.orc.attention(c.orc.bf16(host[0]), units, c.table, c.codes, c.scales, c.recent, 0.125)
+    check_rows(c.orc.bf16(c.down_bits(o))[rows], want[rows], bound[rows])
+
+
+def test_many_query_heads_of_one_kv_head(library):
+    c = start(2, [130, 5], 128, 1, 64, 70, 2)
+    c.step([1, 1])
+    c.step([3, 66])
