@@ -63,6 +63,12 @@ def parse():
     p.add_argument("--decode-rowmajor", action="store_true",
                    help="decode over row-major FP8 weights (jetfp8_gemm_fwd) instead of the fragment order "
                         "(JETFP8_BLOCKS_128x128_FRAG + jetfp8_gemm_fwd_frag, used up to 64 rows)")
+    p.add_argument("--attention", action="store_true",
+                   help="instead of the training step, time a rollout decode step's key/value cache work (workload "
+                        "llama3_8b_decode_m32's heads: plan, then append and attention over the FP8 cache with the fused "
+                        "1x128 codes of its output) and print its own JSON line")
+    p.add_argument("--attention-context", type=int, default=4096,
+                   help="tokens that each of the 32 requests has in the cache")
     p.add_argument("--calibrate-copy", action="store_true",
                    help="first run a 1 GiB device-to-device copy (known bytes) to scale rocprofv3 byte counters")
     return p.parse_args()
@@ -495,6 +501,86 @@ def run_decode(args, torch, jf, workloads):
     print(json.dumps(out), flush=True)
 
 
+def attention_decode_bytes(requests, context, q_heads, kv_heads, head_dim):
+    """Bytes that a decode step's attention cannot do without: complete blocks as codes and two scales per head, the
+    unfinished block's tokens as bf16 (the new one among them), queries in, codes and scales out."""
+    blocks, rest = context // 64, context % 64 + 1
+    cache = kv_heads * (blocks * (128 * head_dim + 8) + rest * 4 * head_dim)
+    return requests * (cache + q_heads * (3 * head_dim + 4 * (head_dim // 128)))
+
+
+ATTENTION_LAYERS = 3     # caches cycled by --attention: beyond the 256 MB MALL at the default context
+
+
+def run_attention(args, torch, jf, workloads):
+    wl = workloads.WORKLOADS["llama3_8b_decode_m32"]
+    (_, K, N), R, D, ctx = wl.linears[0], wl.M, 128, args.attention_context
+    Hq, H = K // D, (N - K) // (2 * D)
+    blocks = ctx // 64 + 2
+    g = torch.Generator(device="cuda")
+    g.manual_seed(41)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    state = torch.tensor([[ctx, 0]] * R, **i32)
+    lens, head = torch.ones((R,), **i32), torch.zeros((1,), **i32)
+    ids = torch.randperm(R * blocks, device="cuda", generator=g).to(torch.int32)
+    table, free = ids[:R * (blocks - 1)].view(R, blocks - 1).contiguous(), ids[R * (blocks - 1):].clone()
+    caches = []
+    for _ in range(ATTENTION_LAYERS):
+        codes, scales, recent = jf.kv_cache(R * blocks, R, R, H, D)
+        codes.random_(0, 127, generator=g)
+        scales.fill_(1.0 / 128)
+        recent.normal_(generator=g)
+        caches.append((codes, scales, recent))
+    qkv = torch.randn((R, Hq + 2 * H, D), device="cuda", generator=g).to(torch.bfloat16)
+    q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + H], qkv[:, Hq + H:]
+    st = torch.cuda.current_stream()
+
+    def step(c, ev):
+        def call(kind, f):
+            a = b = None
+            if ev is not None:
+                a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+                a.record(st)
+            r = f()
+            if ev is not None:
+                b.record(st)
+                ev.append((kind, a, b))
+            return r
+        p = call("plan", lambda: jf.kv_plan(state, lens, free, head, table, R, 1))
+        for cache in caches:
+            call("append", lambda: jf.kv_append(k, v, p.units, *cache))
+            call("attention", lambda: jf.attention(q, p.units, table, *cache, max_new=1, max_seq=ctx + 1, quantize=True,
+                                                   return_o=False))
+
+    for c in range(args.warmup):
+        step(c, None)
+    torch.cuda.synchronize()
+    ms_step, _ = timed_steps(torch, st, args.steps, step, with_events=False)
+    ms_step_ev, ev = timed_steps(torch, st, args.steps, step, with_events=True)
+    per = {}
+    for kind, a, b in ev:
+        per.setdefault(kind, []).append(a.elapsed_time(b))
+    byts = attention_decode_bytes(R, ctx, Hq, H, D)
+    us = {kind: 1e3 * sum(t) / len(t) for kind, t in per.items()}
+    achieved = byts / us["attention"] / 1e3
+    print(json.dumps({
+        "metric": "rollout decode attention over the FP8 key/value cache, algorithmic GB/s",
+        "value": round(ATTENTION_LAYERS * byts / (ms_step * 1e-3) / 1e9, 1), "unit": "GB/s", "n_gpus": 1,
+        "steps": args.steps, "warmup": args.warmup, "ms_per_step": round(ms_step, 4), "higher_is_better": True,
+        "scaling": "weak", "vs_baseline": None, "dtype": "bf16 in, fp8_e4m3 cache, fp32 softmax, fp8_e4m3 out",
+        "data": "synthetic (seeded torch generator on device: N(0,1) queries, keys and values, random cache codes)",
+        "config": {"workload": wl.name, "requests": R, "context": ctx, "q_heads": Hq, "kv_heads": H, "head_dim": D,
+                   "step": f"1 x plan + {ATTENTION_LAYERS} x (append + attention -> 1x128 codes), a cache each"},
+        "roofline": {"bound": "hbm", "kernel": "attention_span_kernel + attention_join_kernel",
+                     "bytes_per_launch": byts, "mean_launch_us": round(us["attention"], 2),
+                     "achieved": round(achieved, 1), "peak": HBM_PEAK_GBS, "unit": "GB/s",
+                     "frac": round(achieved / HBM_PEAK_GBS, 4),
+                     "timing": f"HIP events around each call, over {args.steps} more steps "
+                               f"({ms_step_ev * 1e3:.1f} us per step with the events)"},
+        "per_call_us": {kind: round(t, 2) for kind, t in us.items()},
+    }), flush=True)
+
+
 def main():
     args = parse()
     if args.gpus != 1:
@@ -517,6 +603,9 @@ def main():
         return
     if args.decode:
         run_decode(args, torch, jf, workloads)
+        return
+    if args.attention:
+        run_attention(args, torch, jf, workloads)
         return
     layers = [Linear(wl, i, torch, workloads) for i in range(len(wl.linears))]
     torch.cuda.synchronize()

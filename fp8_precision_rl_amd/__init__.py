@@ -385,13 +385,22 @@ def attention_workspace(num_units: int, max_new: int, max_seq: int, q_heads: int
     return n
 
 
+def _attention_inputs(q, units, block_table, codes, scales, recent, T, Hq, H, D, max_new, max_seq, softmax_scale):
+    """The device and the arguments of jetfp8_attention up to its outputs."""
+    dev, work, cache = _kv_buffers(units, codes, scales, recent, H, D)
+    requests, width = block_table.shape if getattr(block_table, "ndim", 0) == 2 else (0, 0)
+    return dev, (*_rows(q, (T, Hq, D), "q", dev), T, *work,
+                 _use(block_table, (requests, width), _torch.int32, "block_table", dev), requests, width, *cache,
+                 int(max_new), int(max_seq), Hq, H, D, float(softmax_scale))
+
+
 def jetfp8_attention(q_bf16, units, block_table, codes, scales, recent_bf16, tokens: int, max_new: int, max_seq: int,
                      q_heads: int, kv_heads: int, head_dim: int, softmax_scale: float, dst_o_bf16=None, dst_codes=None,
                      dst_scales=None, workspace=None, stream=None) -> None:
     bf, u8, f32 = _bf16_u8_f32()
     T, Hq, H, D = int(tokens), int(q_heads), int(kv_heads), int(head_dim)
-    dev, work, cache = _kv_buffers(units, codes, scales, recent_bf16, H, D)
-    requests, width = block_table.shape if getattr(block_table, "ndim", 0) == 2 else (0, 0)
+    dev, inputs = _attention_inputs(q_bf16, units, block_table, codes, scales, recent_bf16, T, Hq, H, D, max_new, max_seq,
+                                    softmax_scale)
     out = (None if dst_o_bf16 is None else _use(dst_o_bf16, (T, Hq, D), bf, "dst_o_bf16", dev),
            None if dst_codes is None else _use(dst_codes, (T, Hq * D), u8, "dst_codes", dev),
            None if dst_scales is None else _use(dst_scales, (Hq * D // 128, T), f32, "dst_scales", dev))
@@ -399,9 +408,7 @@ def jetfp8_attention(q_bf16, units, block_table, codes, scales, recent_bf16, tok
     if workspace is not None:
         space = (_use(workspace, workspace.shape, None, "workspace", dev),
                  workspace.numel() * workspace.element_size())
-    _call("jetfp8_attention", dev, stream, *_rows(q_bf16, (T, Hq, D), "q", dev), T, *work,
-          _use(block_table, (requests, width), _torch.int32, "block_table", dev), requests, width, *cache, int(max_new),
-          int(max_seq), Hq, H, D, float(softmax_scale), *out, *space)
+    _call("jetfp8_attention", dev, stream, *inputs, *out, *space)
 
 
 # ------------------------------------------------------------------------------------------------
@@ -620,15 +627,25 @@ def attention(q, units, block_table, codes, scales, recent, max_new: int, max_se
     (D = 128) -> (codes [T, Hq * D], scales [Hq, T]) and, with return_o, the bf16 matrix as well.  softmax_scale:
     1 / sqrt(D) unless given.  Rows that belong to no unit are left unwritten."""
     T, Hq, D = q.shape
+    H = codes.shape[1]
+    dev, inputs = _attention_inputs(q, units, block_table, codes, scales, recent, T, Hq, H, D, max_new, max_seq,
+                                    D ** -0.5 if softmax_scale is None else softmax_scale)
+    size = attention_workspace(units.shape[0], max_new, max_seq, Hq, H, D)
+    space = (None, 0)
+    if workspace is not None:
+        space = (_use(workspace, workspace.shape, None, "workspace", dev),
+                 workspace.numel() * workspace.element_size())
+    o = c = s = None
     with _memory_of(stream, q.device):
-        if workspace is None:
-            size = attention_workspace(units.shape[0], max_new, max_seq, Hq, codes.shape[1], D)
-            workspace = codes.new_empty(size) if size else None
-        o = q.new_empty(T, Hq, D) if return_o or not quantize else None
-        c = codes.new_empty((T, Hq * D)) if quantize else None
-        s = scales.new_empty((Hq * D // 128, T)) if quantize else None
-    jetfp8_attention(q, units, block_table, codes, scales, recent, T, max_new, max_seq, Hq, codes.shape[1], D,
-                     D ** -0.5 if softmax_scale is None else softmax_scale, o, c, s, workspace, stream)
+        if size and workspace is None:
+            workspace = codes.new_empty(size)
+            space = workspace.data_ptr(), size
+        if return_o or not quantize:
+            o = q.new_empty(T, Hq, D)
+        if quantize:
+            c, s = codes.new_empty(T, Hq * D), scales.new_empty(Hq * D // 128, T)
+    _call("jetfp8_attention", dev, stream, *inputs, None if o is None else o.data_ptr(),
+          None if c is None else c.data_ptr(), None if s is None else s.data_ptr(), *space)
     if not quantize:
         return o
     return (c, s, o) if return_o else (c, s)

@@ -867,8 +867,11 @@ AttnShape attn_shape(int64_t num_units, int64_t max_new, int64_t max_seq, int64_
     s.max_blocks = (max_seq - 1) / kKvBlock;
     const int64_t spans = (s.max_blocks + kSpan - 1) / kSpan;
     s.runs = (spans + kRun - 1) / kRun;
-    // Waves of the tile kernel; four per compute unit keep the memory and the matrix units busy.
-    const int64_t waves = num_units * kv_heads * ((s.max_rows + 31) / 32);
+    // Rows that one wave holds read the cache once either way, and a wave per span reads it sooner.  More rows go to
+    // the tile kernel if that has enough waves (32 rows each) for the chip's 1024 SIMDs: below, spans in parallel win (256
+    // tokens at 4096, 320 waves: 54 against 106 us), at 1072 and 1472 waves the two are within 5 %, above the
+    // partial results cost more than they bring (16 times 64 tokens at 4096, 3008 waves: 157 against 109 us).
+    const double waves = (double)num_units * kv_heads * ((s.max_rows + 31) / 32);
     s.split = spans > 0 && (s.max_rows <= 16 || waves < 1024);
     s.rt = s.split && s.max_rows <= 16 ? 1 : 2;
     s.row_groups = (s.max_rows + 16 * s.rt - 1) / (16 * s.rt);
@@ -881,9 +884,10 @@ int64_t partial_rows(const AttnShape& s, int64_t num_units, int64_t kv_heads) {
     return num_units * kv_heads * s.parts * s.max_rows;
 }
 
-int64_t attn_blocks(const AttnShape& s, int64_t num_units, int64_t kv_heads) {
-    if (s.split) return num_units * kv_heads * ((s.parts * s.row_groups + kWaves - 1) / kWaves);
-    return (num_units + 1) / 2 * kv_heads * 2 * ((s.row_groups + kWaves - 1) / kWaves) * s.runs;
+// Thread blocks of the first kernel.  In double: sizes at their limits would overflow 64 bits.
+double attn_blocks(const AttnShape& s, int64_t num_units, int64_t kv_heads) {
+    if (s.split) return (double)num_units * kv_heads * ((s.parts * s.row_groups + kWaves - 1) / kWaves);
+    return (double)((num_units + 1) / 2 * 2) * kv_heads * ((s.row_groups + kWaves - 1) / kWaves) * s.runs;
 }
 
 template <int D>
@@ -910,7 +914,7 @@ int64_t attention_workspace(int64_t num_units, int64_t max_new, int64_t max_seq,
 
 bool attention_fits(int64_t num_units, int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads) {
     const AttnShape s = attn_shape(num_units, max_new, max_seq, q_heads, kv_heads);
-    return attn_blocks(s, num_units, kv_heads) <= INT32_MAX && num_units * kv_heads * s.max_rows <= INT32_MAX;
+    return attn_blocks(s, num_units, kv_heads) <= INT32_MAX && (double)num_units * kv_heads * s.max_rows <= INT32_MAX;
 }
 
 hipError_t launch_attention(const uint16_t* q, int64_t ldq, int64_t tokens, const int32_t* units, int64_t num_units,

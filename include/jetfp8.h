@@ -270,7 +270,8 @@ int jetfp8_kv_append(const void* k_bf16, int64_t ldk, const void* v_bf16, int64_
  * same decoded alone, in a batch, or within a prompt.
  * max_new: no request has more new tokens; max_seq: nor more tokens after the step.  A unit beyond either, or whose
  * fields do not fit the buffers, is left out (its rows stay as they were); a block id outside 0 .. num_blocks - 1
- * reads as a block without keys.  Infinities and NaN reach only the rows that may see them.
+ * reads as a block without keys.  Infinities and NaN reach only the rows that may see them.  Values below 2^90 (sums over
+ * the keys are taken before they are divided by the denominator).
  * workspace: jetfp8_attention_workspace() bytes (its content is not kept between calls; calls that may run at the same
  * time need one each); JETFP8_ERR_SHAPE if workspace_bytes is less. */
 int jetfp8_attention(const void* q_bf16, int64_t ldq, int64_t tokens, const int32_t* units, int64_t num_units,

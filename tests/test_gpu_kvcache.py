@@ -3,7 +3,7 @@ the error of fp32 arithmetic with 11-bit probabilities (the bound is derived in 
 import numpy as np
 import pytest
 
-from kv_case import TwinCache
+from kv_case import TwinCache, check_rows
 
 pytestmark = pytest.mark.gpu
 
@@ -167,13 +167,13 @@ def test_prompts_equal_the_same_prompts_alone(library, q_heads, kv_heads, head_d
         rows = slice(int(new[:r].sum()), int(new[:r + 1].sum()))
         assert torch.equal(o[rows].view(torch.int16), alone[rows].view(torch.int16)), r
         kind = (min(int(new[r]), 65) // 64, int(past[r]) % 64 == 0)
-        if kind in seen or len(seen) > 2 or new[r] > 400:
+        if kind in seen or len(seen) > 2:
             continue
         seen.add(kind)
-        from kv_case import check_rows
         down = lambda t: t.cpu().numpy()
-        local = mine.cpu().numpy().copy()
-        local[:, 3] -= rows.start
-        want, bound = c.orc.attention(c.orc.bf16(host[0][rows]), local, down(c.dev["table"]), down(c.dev["codes"]),
+        few = mine.cpu().numpy()[[0, -1]].copy()             # the first rows of its first and last unit
+        few[:, 4] = np.minimum(few[:, 4], 3)
+        want, bound = c.orc.attention(c.orc.bf16(host[0]), few, down(c.dev["table"]), down(c.dev["codes"]),
                                       down(c.dev["scales"]), c.down_bits(c.dev["recent"]), head_dim ** -0.5)
-        check_rows(c.orc.bf16(c.down_bits(o[rows])), want, bound)
+        at = np.concatenate([np.arange(x, x + n) for x, n in few[:, 3:5]])
+        check_rows(c.orc.bf16(c.down_bits(o))[at], want[at], bound[at])

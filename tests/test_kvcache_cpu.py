@@ -76,7 +76,8 @@ def test_workspace_sizes(lib):
     one, two = f(8, 1, 4096, 32, 8, 128), f(16, 1, 4096, 32, 8, 128)
     assert one > 0 and two == 2 * one and one % 16 == 0
     for kw in ((0, 1, 64, 32, 8, 128), (8, 0, 64, 32, 8, 128), (8, 1, 0, 32, 8, 128), (8, 1, 64, 33, 8, 128),
-               (8, 1, 64, 32, 8, 80)):
+               (8, 1, 64, 32, 8, 80), ((1 << 31) - 1, 64, (1 << 31) - 1, 65536, 65536, 128),
+               ((1 << 31) - 1, (1 << 31) - 1, (1 << 31) - 1, 65536, 1, 128), (1 << 20, 64, 64, 1 << 15, 1 << 10, 64)):
         assert f(*kw) == -2, kw
 
 
@@ -153,3 +154,11 @@ def test_oracle_attention_reads_the_cache():
     units = np.array([[0, 1, 0, 0, 2, 0, -1, 0]])
     o, bound = kc.attention(q, units, np.array([[1]]), codes, scales, recent, 1.0)
     assert np.allclose(o[0], 2.0) and np.allclose(o[1], 3.0) and (bound < 1).all()
+
+
+def test_bench_bytes_of_decode_attention():
+    import bench
+    # 64 blocks of 64 tokens: 2 * 64 * 128 codes and two scales each, per kv head; one bf16 token (key and value) beside
+    # them; per query head 128 bf16 in, 128 codes and a scale out
+    assert bench.attention_decode_bytes(1, 4096, 32, 8, 128) == 8 * (64 * (2 * 64 * 128 + 8) + 512) + 32 * (256 + 128 + 4)
+    assert bench.attention_decode_bytes(3, 100, 4, 2, 128) == 3 * (2 * (16384 + 8 + 37 * 512) + 4 * 388)
