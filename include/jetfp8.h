@@ -21,7 +21,8 @@
  *
  * Conventions for every entry point:
  *   - Matrices are dense, row-major, last index contiguous; bf16 tensors are passed as raw 16-bit
- *     patterns (void*), FP8 codes as uint8_t, scales as float.  No strides.
+ *     patterns (void*), FP8 codes as uint8_t, scales as float.  No strides, but for the row pitches (ldq, ldk, ldv) of
+ *     the key/value cache's calls.
  *   - Every pointer is a DEVICE pointer owned by the caller; the library never allocates, frees or
  *     synchronizes.  Work is enqueued on `stream` (a hipStream_t; NULL = the default stream) and runs
  *     asynchronously; outputs are valid once the stream has reached that point.
