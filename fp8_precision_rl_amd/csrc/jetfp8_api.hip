@@ -248,9 +248,10 @@ int jetfp8_attention(const void* q_bf16, int64_t ldq, int64_t tokens, const int3
         return JETFP8_ERR_NULL;
     if (!attention_dims_ok(num_units, max_new, max_seq, q_heads, kv_heads, head_dim) ||
         !kv_dims_ok(tokens, num_units, kv_heads, head_dim, num_blocks, recent_blocks) || !dim_ok(requests) ||
-        !dim_ok(max_blocks) || !row_pitch_ok(ldq, q_heads, head_dim) || (dst_codes && head_dim != 128))
+        !dim_ok(max_blocks) || !row_pitch_ok(ldq, q_heads, head_dim) || (dst_codes && head_dim != 128) ||
+        recent_blocks < 2 * requests + tokens / JETFP8_KV_BLOCK)
         return JETFP8_ERR_SHAPE;
-    if (!(softmax_scale > 0.0f && softmax_scale <= FLT_MAX)) return JETFP8_ERR_VALUE;
+    if (!(softmax_scale > 0.0f && softmax_scale <= FLT_MAX / 2)) return JETFP8_ERR_VALUE;
     const int64_t need = jetfp8::attention_workspace(num_units, max_new, max_seq, q_heads, kv_heads, head_dim);
     if (need > 0 && !workspace) return JETFP8_ERR_NULL;
     if (need > workspace_bytes) return JETFP8_ERR_SHAPE;

@@ -195,9 +195,10 @@ int jetfp8_gemm_wgrad(const uint8_t* dyqT, const float* dysT, const uint8_t* xqT
  *   codes  uint8 [num_blocks][H][2][64 D], scales float [num_blocks][H][2]: keys (0) and values (1) of the physical
  *          blocks.  Complete blocks are never written again, so requests may share them (a prompt that several
  *          rollouts start from: the same physical ids in several rows of the block table);
- *   recent bf16 [recent_blocks][H][2][64 D], recent_blocks >= 2 requests + tokens / 64 for the largest call:
- *          blocks 2 r and 2 r + 1 belong to request r and keep its unfinished block from call to call; those from
- *          2 requests on hold the blocks that a call's prompts pass through;
+ *   recent bf16 [recent_blocks][H][2][64 D], recent_blocks >= 2 requests + tokens / 64 for the largest call
+ *          (jetfp8_attention refuses less): blocks 2 r and 2 r + 1 belong to request r and keep its unfinished block from
+ *          call to call; those from 2 requests on hold the blocks that a call's prompts pass through.  So every step
+ *          is planned for the same number of requests (one that is idle has no new tokens);
  *   block_table int32 [requests][max_blocks]: physical block of each complete block of each request.
  * Inside a block the 64 D values are in the order in which the attention kernel's waves read them.  For key n and
  * channel d:
@@ -273,6 +274,7 @@ int jetfp8_kv_append(const void* k_bf16, int64_t ldk, const void* v_bf16, int64_
  * fields do not fit the buffers, is left out (its rows stay as they were); a block id outside 0 .. num_blocks - 1
  * reads as a block without keys.  Infinities and NaN reach only the rows that may see them.  Values below 2^90 (sums over
  * the keys are taken before they are divided by the denominator).
+ * 0 < softmax_scale <= FLT_MAX / 2 (JETFP8_ERR_VALUE otherwise).
  * workspace: jetfp8_attention_workspace() bytes (its content is not kept between calls; calls that may run at the same
  * time need one each); JETFP8_ERR_SHAPE if workspace_bytes is less. */
 int jetfp8_attention(const void* q_bf16, int64_t ldq, int64_t tokens, const int32_t* units, int64_t num_units,

@@ -64,9 +64,9 @@ def test_attention_refusals(lib):
     for kw in (dict(ldq=4088), dict(ldq=4100), dict(T=0), dict(n=0), dict(R=0), dict(width=0), dict(blocks=0),
                dict(rb=0), dict(max_new=0), dict(max_seq=0), dict(max_seq=1 << 31), dict(Hq=12), dict(Hq=0), dict(H=0),
                dict(D=64, oq=P, os=P), dict(D=192), dict(wsb=16), dict(Hq=1 << 17, ldq=1 << 24),
-               dict(n=1 << 20, max_seq=1 << 30, Hq=32)):
+               dict(n=1 << 20, max_seq=1 << 30, Hq=32), dict(R=5), dict(T=64, rb=8), dict(R=1, T=1 << 20, rb=1 << 14)):
         assert _attention(lib, **kw) == -2, kw
-    for scale in (0.0, -1.0, float("inf"), float("nan")):
+    for scale in (0.0, -1.0, float("inf"), float("nan"), 3e38):
         assert _attention(lib, scale=scale) == -6, scale
 
 
