@@ -534,8 +534,10 @@ __global__ __launch_bounds__(kWaves * 64, RT == 1 ? 3 : 2) void attention_span_k
 // ahead.  A wave forming scores has priority over its SIMD's other wave (a chunk of 2048 at 14336: 777 -> 724 us; giving it
 // to the second product as well changes nothing).  Units are taken in pairs: two of one request share thread blocks, the waves of the first leaving out the last
 // block or so, since a unit's rows (64 query heads per kv head) need not be a multiple of 128.
+// With D = 64 a wave needs 170 registers if it may; held to 168 a third thread block fits a CU (4 prompts of 2048, 16
+// kv heads: 129 -> 113 us; a chunk of 300 at 30000: 481 -> 450 us; held to 128 for a fourth it spills).
 template <int D>
-__global__ __launch_bounds__(kWaves * 64, 2) void attention_tile_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kWaves * 64, D == 64 ? 3 : 2) void attention_tile_kernel(AttnArgs a) {
     constexpr int RT = 2, NT = D / 16, NK = D / 32;
     constexpr int NL = NT / kWaves;        // loads of a block's keys, and of its values, per wave
     constexpr int NO = kKvBlock * D / 8 / 64;   // operands of a block's keys, and of its values

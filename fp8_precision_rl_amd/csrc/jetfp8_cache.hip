@@ -57,7 +57,8 @@ __device__ __forceinline__ int first_above(const uint32_t* ends, int n, uint32_t
 // complete, of their units and of the blocks between their first and last.  Bound by latency (a few KB of data and
 // two dependent sums), so one launch does it all: every block forms the same sums in LDS from the lengths, at
 // most 4096 requests, and then writes one unit and one row per thread.  Nothing is passed between blocks.  A thread
-// takes PER consecutive requests, whose lengths it loads at once and keeps.
+// takes PER consecutive requests, whose lengths it loads at once and keeps (1000 requests with 64440 new tokens: 9.3 us,
+// 17 us when a thread loaded one request after the other; 32 single tokens: 3.9 us).
 template <int PER>
 __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(PlanArgs a) {
     extern __shared__ uint32_t sums[];              // [3][requests]
@@ -219,7 +220,8 @@ __device__ __forceinline__ uint2 encode_chunk(const uint4& c, const GroupScale& 
 // attention may read it whole.  When the block completes, all its 64 tokens (those of earlier calls from the bf16
 // block, the new ones from the call) are quantized at once: amax over 64 x D, scale = fl32(amax / 448), codes
 // rounded to nearest even as everywhere in this library.  The codes therefore depend on the 64 tokens alone, not on
-// how many came with which call.  Bound by HBM for prompts, by latency for single tokens.
+// how many came with which call.  Bound by HBM for prompts, by latency for single tokens (8 kv heads, D = 128:
+// 16384 tokens 43-45 us, 3.7-3.9 TB/s of reads and writes together; 32 single tokens 5.0 us).
 template <int D>
 __global__ __launch_bounds__(kAppendThreads) void kv_append_kernel(AppendArgs a) {
     constexpr int kChunks = kKvBlock * D / 8 / kAppendThreads;   // 16-byte pieces of a block per thread
