@@ -50,6 +50,7 @@ struct AttnArgs {
     int row_groups;                // row groups of 16 RT rows that cover them
     int parts;                     // partial results that a row may have, its own block's among them
     int runs;                      // tile kernel: runs, a thread block each
+    int ordered;                   // tile kernel: units taken by length
 };
 
 // Eight E4M3 codes -> bf16, exact.
@@ -526,6 +527,61 @@ __global__ __launch_bounds__(kWaves * 64, RT == 1 ? 3 : 2) void attention_span_k
     store_part(st, ref, a, unit, head, span, row0, rows, lane);
 }
 
+// The pair of units that stands at place x if all are ordered by the blocks that precede them, most first (64 classes;
+// one class in any order, unused units last).  A counting sort that every thread block does for itself, about 1 us of
+// latency: against that, thread blocks of long requests that start last and then run on alone, with ragged requests
+// up to a quarter of the time.  x is below pairs, and pairs no more than 256 kOrder.
+constexpr int kOrder = 4;              // pairs of a thread
+__device__ __forceinline__ int ordered_pair(const AttnArgs& a, int pairs, int x) {
+    __shared__ int count[64], sums[kWaves], found;
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    if (threadIdx.x < 64) count[lane] = 0;
+    if (threadIdx.x == 0) found = 0;
+    __syncthreads();
+    int key[kOrder];
+#pragma unroll
+    for (int i = 0; i < kOrder; ++i) {
+        const int p = threadIdx.x * kOrder + i;
+        key[i] = -1;
+        if (p >= pairs) continue;
+        const int most = min(max(max(a.units[2 * p].block, a.units[min(2 * p + 1, a.num_units - 1)].block), 0), a.max_blocks);
+        key[i] = 63 - (int)((uint32_t)most * 63u / (uint32_t)max(a.max_blocks, 1));
+        atomicAdd(&count[key[i]], 1);
+    }
+    __syncthreads();
+    const int mine = count[lane];
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int y = __shfl_up(upto, d);
+        if (lane >= d) upto += y;
+    }
+    const int b = __builtin_ctzll(__ballot(upto > x) | 1ull << 63);
+    int y = x - __builtin_amdgcn_readlane(upto - mine, b);
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kOrder; ++i) n += key[i] == b;
+    int before = n;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int z = __shfl_up(before, d);
+        if (lane >= d) before += z;
+    }
+    if (lane == 63) sums[wave] = before;
+    before -= n;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) before += sums[w];
+    y -= before;
+    if (y >= 0 && y < n) {
+#pragma unroll
+        for (int i = 0; i < kOrder; ++i) {
+            if (key[i] == b && y-- == 0) found = threadIdx.x * kOrder + i;
+        }
+    }
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(found);
+}
+
 // attention_tile_kernel walks a run of 128 rows in one block of four waves, and where that is all (up to 4096 tokens
 // before the own block) finishes the rows, else leaves the joining of the runs to attention_join_kernel: for prompts, where the time is that of
 // the arithmetic.  Each wave widens a quarter of a block's codes into LDS, as operands, and all four read them there,
@@ -546,7 +602,8 @@ __global__ __launch_bounds__(kWaves * 64, D == 64 ? 3 : 2) void attention_tile_k
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int head = blockIdx.x % a.kv_heads, chunks = (a.row_groups + kWaves - 1) / kWaves;
     const int pairs = (a.num_units + 1) / 2;
-    const int first_unit = 2 * (pairs - 1 - blockIdx.x / a.kv_heads / (2 * chunks * a.runs));   // the longest rows first
+    const int place = blockIdx.x / a.kv_heads / (2 * chunks * a.runs);         // the longest rows first, also without order
+    const int first_unit = 2 * (a.ordered ? ordered_pair(a, pairs, place) : pairs - 1 - place);
     const int chunk = blockIdx.x / a.kv_heads % (2 * chunks), run = blockIdx.x / a.kv_heads / (2 * chunks) % a.runs;
     KvUnit us[2];
     int tiles[2];                          // row tiles of 32 that the two units have
@@ -863,6 +920,11 @@ struct AttnShape {
     bool split;
 };
 
+// Waves of 32 rows.
+double attn_waves(const AttnShape& s, int64_t num_units, int64_t kv_heads) {
+    return (double)num_units * kv_heads * ((s.max_rows + 31) / 32);
+}
+
 AttnShape attn_shape(int64_t num_units, int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads) {
     AttnShape s;
     s.max_rows = (max_new < kKvBlock ? max_new : kKvBlock) * (q_heads / kv_heads);
@@ -873,8 +935,7 @@ AttnShape attn_shape(int64_t num_units, int64_t max_new, int64_t max_seq, int64_
     // the tile kernel if that has enough waves (32 rows each) for the chip's 1024 SIMDs: below, spans in parallel win (256
     // tokens at 4096, 320 waves: 54 against 106 us), at 1072 and 1472 waves the two are within 5 %, above the
     // partial results cost more than they bring (16 times 64 tokens at 4096, 3008 waves: 157 against 109 us).
-    const double waves = (double)num_units * kv_heads * ((s.max_rows + 31) / 32);
-    s.split = spans > 0 && (s.max_rows <= 16 || waves < 1024);
+    s.split = spans > 0 && (s.max_rows <= 16 || attn_waves(s, num_units, kv_heads) < 1024);
     s.rt = s.split && s.max_rows <= 16 ? 1 : 2;
     s.row_groups = (s.max_rows + 16 * s.rt - 1) / (16 * s.rt);
     s.parts = s.split ? spans + 1 : s.runs > 1 ? s.runs + 1 : 0;
@@ -954,6 +1015,10 @@ hipError_t launch_attention(const uint16_t* q, int64_t ldq, int64_t tokens, cons
     a.row_groups = (int)s.row_groups;
     a.parts = (int)s.parts;
     a.runs = (int)s.runs;
+    // Units of one request come in the order of their lengths already.  With several, ordering them shortens the end of
+    // the call and costs each thread block its sort: at 3232 waves 79 -> 65 us, at 10048 238 -> 218, at 9040 within 2 %,
+    // at 17344 344 -> 360, at 31840 405 -> 428.
+    a.ordered = requests > 1 && s.max_blocks > 0 && num_units <= 2 * 256 * kOrder && attn_waves(s, num_units, kv_heads) < 12288;
     const unsigned grid = (unsigned)attn_blocks(s, num_units, kv_heads);
     return D == 64 ? launch<64>(a, s, grid, st) : launch<128>(a, s, grid, st);
 }

@@ -411,3 +411,41 @@ def test_many_query_heads_of_one_kv_head(library):
     c = start(2, [130, 5], 128, 1, 64, 70, 2)
     c.step([1, 1])
     c.step([3, 66])
+
+
+@pytest.mark.parametrize("requests,past,new,q_heads,kv_heads,head_dim", [(3, 900, 700, 24, 8, 64), (40, 1500, 130, 8, 8, 128),
+                                                                         (301, 700, 90, 2, 2, 64), (700, 200, 128, 1, 1, 64),
+                                                                         (900, 130, 60, 1, 1, 128), (9, 9000, 200, 40, 8, 128)])
+def test_ragged_requests_equal_a_few_units_at_a_time(library, requests, past, new, q_heads, kv_heads, head_dim):
+    """The order in which units are taken, and the form of the call, change nothing: all units at once, and a few of
+    them per call, in any order."""
+    import torch
+    jf = library
+    rng = np.random.default_rng(requests)
+    had, lens = rng.integers(0, past + 1, requests), rng.integers(0, new + 1, requests)
+    had[-1], lens[-1] = past, new
+    c = start(requests, had, q_heads, kv_heads, head_dim, int(lens.sum()), requests,
+              blocks=int(((had + lens) // 64).sum()) + 1, width=(past + new) // 64 + 1)
+    T = int(lens.sum())
+    ref, got = c.plan(lens, T, new)
+    assert not ref["status"].any()
+    host, (q, k, v) = c.qkv(T)
+    c.append(ref, got, host, (q, k, v))
+    U, seq = len(got.units), past + new
+
+    def run(units, o):
+        need = jf.attention_workspace(len(units), new, seq, q_heads, kv_heads, head_dim)
+        ws = torch.full((max(need, 16),), 255, dtype=torch.uint8, device="cuda")
+        jf.jetfp8_attention(q, units, c.dev["table"], c.dev["codes"], c.dev["scales"], c.dev["recent"], T, new, seq,
+                            q_heads, kv_heads, head_dim, head_dim ** -0.5, o, workspace=ws)
+        return o
+
+    def blank():
+        return torch.full((T, q_heads, head_dim), 7.0, dtype=torch.bfloat16, device="cuda")
+    whole, parts = run(got.units, blank()), blank()
+    assert not bool((whole == 7.0).all(-1).any()), "a row was left out"
+    mixed = got.units[torch.from_numpy(rng.permutation(U)).cuda()].contiguous()
+    for i in range(0, U, 37):
+        run(mixed[i:i + 37].contiguous(), parts)
+    assert torch.equal(whole.view(torch.int16), parts.view(torch.int16))
+    assert torch.equal(whole.view(torch.int16), run(mixed, blank()).view(torch.int16))
