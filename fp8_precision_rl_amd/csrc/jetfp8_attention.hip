@@ -313,13 +313,25 @@ __device__ __forceinline__ void add_values(Softmax<D, RT>& st, int t, const T& v
     }
 }
 
-// The unit's own block, bf16 with the causal mask, into an empty state (whatever the registers hold).  keys, values: the block's operands, 64 lanes
-// of 16 bytes each; AHEAD: the values are loaded before the scores are formed (from memory, not from LDS).
+// Whether some of a value operand's exponents are all ones (infinities, NaN): then bit 15 or 31 of the result is set.
+__device__ __forceinline__ uint32_t all_ones(const uint4& v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t odd = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) odd |= (w[i] & 0x7F807F80u) + 0x00800080u;
+    return odd & 0x80008000u;
+}
+
+// The unit's own block, bf16 with the causal mask, into an empty state (whatever the registers hold).  keys, values:
+// the block's operands, 64 lanes of 16 bytes each.  AHEAD: the values are loaded before the scores are formed (from
+// memory, not from LDS); otherwise odd says whether there are infinities or NaN among the values.  Keys behind the last
+// row's own come in halves of the block: the second is left out where no row reaches it (it would add zeros).
 template <bool AHEAD, int D, int RT>
 __device__ __forceinline__ void own_block(Softmax<D, RT>& st, const bf16x8 (&q)[RT][D / 32], float scale_log2,
                                           int offset, int group, int row0, const bf16x8* keys, const uint4* values,
-                                          int lane) {
+                                          bool odd, int lane) {
     constexpr int NK = D / 32, NT = D / 16;
+    const bool both = offset + (row0 + 16 * RT - 1) / group >= 32;
     uint4 ahead[AHEAD ? NT : 1][2];
     if (AHEAD) {
 #pragma unroll
@@ -327,85 +339,115 @@ __device__ __forceinline__ void own_block(Softmax<D, RT>& st, const bf16x8 (&q)[
 #pragma unroll
             for (int k = 0; k < 2; ++k) ahead[AHEAD ? t : 0][k] = values[(t * 2 + k) * 64 + lane];
     }
+    auto value = [&](int t, int k) { return AHEAD ? ahead[AHEAD ? t : 0][k] : values[(t * 2 + k) * 64 + lane]; };
     v4f s[RT][4];
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+    for (int h = 0; h < 2; ++h) {
+        if (h && !both) break;
 #pragma unroll
-        for (int k = 0; k < NK; ++k) {
-            const bf16x8 x = keys[(t * NK + k) * 64 + lane];
+        for (int t = 2 * h; t < 2 * h + 2; ++t)
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
-                s[rt][t] = mfma16(x, q[rt][k], k ? s[rt][t] : z);
+            for (int k = 0; k < NK; ++k) {
+                const bf16x8 x = keys[(t * NK + k) * 64 + lane];
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
+                    s[rt][t] = mfma16(x, q[rt][k], k ? s[rt][t] : z);
+                }
             }
-        }
+    }
     // The values are bf16 here, and so are the probabilities, each as a sum of two (16 significant bits).
     bf16x8 p[RT][2], rest[RT][2];
     int place[RT];                      // of the query in the block
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
         place[rt] = offset + (row0 + rt * 16 + lane % 16) / group;
+        auto mask = [&](int h) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (i / 4 * 16 + lane / 16 * 4 + i % 4 > place[rt]) s[rt][i / 4][i % 4] = -INFINITY;
+            for (int i = 8 * h; i < 8 * h + 8; ++i)
+                if (i / 4 * 16 + lane / 16 * 4 + i % 4 > place[rt]) s[rt][i / 4][i % 4] = -INFINITY;
+        };
+        auto take = [&](int h) {
+#pragma unroll
+            for (int i = 8 * h; i < 8 * h + 8; ++i) {
+                const float e = __builtin_amdgcn_exp2f(fmaf(s[rt][i / 4][i % 4], scale_log2, -st.m[rt]));
+                st.l[rt] += e;
+                p[rt][h][i % 8] = (__bf16)e;
+                rest[rt][h][i % 8] = (__bf16)(e - (float)(__bf16)e);
+            }
+        };
+        mask(0);
+        if (both) {
+            mask(1);
+        } else {
+#pragma unroll
+            for (int i = 8; i < 16; ++i) s[rt][i / 4][i % 4] = -INFINITY;
+        }
         st.m[rt] = top_score(s[rt]) * scale_log2;
         st.l[rt] = 0.0f;
+        take(0);
+        if (both) {
+            take(1);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float e = __builtin_amdgcn_exp2f(fmaf(s[rt][i / 4][i % 4], scale_log2, -st.m[rt]));
-            st.l[rt] += e;
-            p[rt][i / 8][i % 8] = (__bf16)e;
-            rest[rt][i / 8][i % 8] = (__bf16)(e - (float)(__bf16)e);
+            for (int i = 0; i < 8; ++i) p[rt][1][i] = rest[rt][1][i] = (__bf16)0.0f;
         }
     }
+    if (AHEAD) {
+        uint32_t any = 0;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        uint4 v[2];
-        uint32_t odd = 0;             // bit 15 of a half: some value's exponent is all ones (infinity or NaN)
+        for (int t = 0; t < NT; ++t) any |= all_ones(ahead[AHEAD ? t : 0][0]) | all_ones(ahead[AHEAD ? t : 0][1]);
+        odd = __any(any != 0);
+    }
+    if (__builtin_expect(!odd, 1)) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            v[k] = AHEAD ? ahead[AHEAD ? t : 0][k] : values[(t * 2 + k) * 64 + lane];
-            const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+            if (k && !both) break;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) odd |= (w[i] & 0x7F807F80u) + 0x00800080u;
+            for (int t = 0; t < NT; ++t) {
+                const bf16x8 x = __builtin_bit_cast(bf16x8, value(t, k));
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
+                    st.o[rt][t] = mfma16(x, p[rt][k], mfma16(x, rest[rt][k], k ? st.o[rt][t] : z));
+                }
+            }
         }
+        return;
+    }
+    // 0 * infinity and 0 * NaN would carry a masked key's values into the rows before it: such values count as 0 in
+    // the product, and the channels of the rows that see one become NaN.
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
         v4f bad[RT];                  // above 0: the row sees such a value in this channel
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) bad[rt] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-        if (__any((odd & 0x80008000u) != 0)) {
-            // 0 * infinity and 0 * NaN would carry a masked key's values into the rows before it: such values count
-            // as 0 in the product, and the channels of the rows that see one become NaN.
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w}, mark[4];
+        for (int k = 0; k < 2; ++k) {
+            const uint4 v = value(t, k);
+            uint32_t w[4] = {v.x, v.y, v.z, v.w}, mark[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    mark[i] = ((w[i] & 0x7F80u) == 0x7F80u ? 0x3F80u : 0u) |
-                              ((w[i] & 0x7F800000u) == 0x7F800000u ? 0x3F800000u : 0u);
-                    w[i] &= ~((mark[i] & 0xFFFFu ? 0xFFFFu : 0u) | (mark[i] >> 16 ? 0xFFFF0000u : 0u));
-                }
-                v[k] = make_uint4(w[0], w[1], w[2], w[3]);
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    bf16x8 seen;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        seen[j] = (__bf16)(k * 32 + j / 4 * 16 + lane / 16 * 4 + j % 4 <= place[rt] ? 1.0f : 0.0f);
-                    bad[rt] = mfma16(__builtin_bit_cast(bf16x8, make_uint4(mark[0], mark[1], mark[2], mark[3])), seen, bad[rt]);
-                }
+            for (int i = 0; i < 4; ++i) {
+                mark[i] = ((w[i] & 0x7F80u) == 0x7F80u ? 0x3F80u : 0u) |
+                          ((w[i] & 0x7F800000u) == 0x7F800000u ? 0x3F800000u : 0u);
+                w[i] &= ~((mark[i] & 0xFFFFu ? 0xFFFFu : 0u) | (mark[i] >> 16 ? 0xFFFF0000u : 0u));
             }
-        }
+            const bf16x8 x = __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
+            for (int rt = 0; rt < RT; ++rt) {
+                bf16x8 seen;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const bf16x8 x = __builtin_bit_cast(bf16x8, v[k]);
+                for (int j = 0; j < 8; ++j)
+                    seen[j] = (__bf16)(k * 32 + j / 4 * 16 + lane / 16 * 4 + j % 4 <= place[rt] ? 1.0f : 0.0f);
+                bad[rt] = mfma16(__builtin_bit_cast(bf16x8, make_uint4(mark[0], mark[1], mark[2], mark[3])), seen, bad[rt]);
                 const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
                 st.o[rt][t] = mfma16(x, p[rt][k], mfma16(x, rest[rt][k], k ? st.o[rt][t] : z));
             }
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) st.o[rt][t][i] = bad[rt][i] > 0.0f ? NAN : st.o[rt][t][i];
-        }
     }
 }
 
@@ -473,7 +515,7 @@ __global__ __launch_bounds__(kWaves * 64, RT == 1 ? 3 : 2) void attention_span_k
     if (span == own) {
         const uint4* mem = recent_block<D>(a, u.recent, head);
         own_block<true, D, RT>(st, q, a.scale_log2, u.offset, a.group, row0, reinterpret_cast<const bf16x8*>(mem),
-                               mem + kKvBlock * D / 8, lane);
+                               mem + kKvBlock * D / 8, false, lane);
     } else {
         const int first = span * kSpan, last = min(first + kSpan, u.block);
         const int64_t block_bytes = (int64_t)a.kv_heads * 2 * kKvBlock * D;
@@ -741,6 +783,7 @@ __global__ __launch_bounds__(kWaves * 64, D == 64 ? 3 : 2) void attention_tile_k
         }
     }
     // The own blocks, as they are, through the same buffers: the first unit's (or the only one's) and the second's.
+    uint32_t found = 0;               // infinities or NaN among their values
     const int owns[2] = {two ? us[0].recent : u.recent, us[1].recent};
 #pragma unroll
     for (int buf = 0; buf < 2; ++buf) {
@@ -749,33 +792,41 @@ __global__ __launch_bounds__(kWaves * 64, D == 64 ? 3 : 2) void attention_tile_k
 #pragma unroll
         for (int i = 0; i < NO / kWaves; ++i) {
             kt[buf][wave * (NO / kWaves) + i][lane] = __builtin_bit_cast(bf16x8, mem[i * 64]);
-            vt[buf][wave * (NO / kWaves) + i][lane] = __builtin_bit_cast(f16x8, mem[kKvBlock * D / 8 + i * 64]);
+            const uint4 v = mem[kKvBlock * D / 8 + i * 64];
+            vt[buf][wave * (NO / kWaves) + i][lane] = __builtin_bit_cast(f16x8, v);
+            found |= all_ones(v);
         }
     }
-    __syncthreads();
+    const bool odd = __syncthreads_or(found != 0);
     if (!busy) return;
     const int unit = first_unit + which, own_part = (u.block + kRunBlocks - 1) / kRunBlocks;
     if (a.parts && run < own_part) store_part(all, 1.0f, a, unit, head, run, row0, rows, lane);
     if (run < own_run) return;
     const int buf = two ? which : 0;
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {      // one row tile at a time: both would not fit the registers
+    // One row tile at a time, the next one moved to the first's place: both would not fit the registers, and the code
+    // of both would not fit the instruction cache beside the walk's (30 ragged prompts up to 1500: 387 -> 380 us).
+#pragma unroll 1
+    for (int rt = 0; rt < RT; ++rt) {
         const int tile_row0 = row0 + rt * 16, row = tile_row0 + lane % 16;
         if (tile_row0 >= rows) break;
         Softmax<D, 1> own;
         bf16x8 q1[1][NK];
 #pragma unroll
-        for (int k = 0; k < NK; ++k) q1[0][k] = q[rt][k];
+        for (int k = 0; k < NK; ++k) q1[0][k] = q[0][k], q[0][k] = q[1][k];
         own_block<false, D, 1>(own, q1, a.scale_log2, u.offset, a.group, tile_row0, &kt[buf][0][0],
-                               reinterpret_cast<const uint4*>(&vt[buf][0][0]), lane);
+                               reinterpret_cast<const uint4*>(&vt[buf][0][0]), odd, lane);
         if (a.parts) {
             own.l[0] = column_sum(own.l[0]);
             store_part(own, 1.0f, a, unit, head, own_part, tile_row0, rows, lane);
             continue;
         }
-        join_state(all.m[rt], all.l[rt], all.o[rt], own.m[0], own.l[0], own.o[0], 1.0f);
-        store_row<D>(a, u.row + row / a.group, head * a.group + row % a.group, lane, all.o[rt], 1.0f / all.l[rt],
+        join_state(all.m[0], all.l[0], all.o[0], own.m[0], own.l[0], own.o[0], 1.0f);
+        store_row<D>(a, u.row + row / a.group, head * a.group + row % a.group, lane, all.o[0], 1.0f / all.l[0],
                      row < rows);
+        all.m[0] = all.m[1];
+        all.l[0] = all.l[1];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) all.o[0][t] = all.o[1][t];
     }
 }
 
