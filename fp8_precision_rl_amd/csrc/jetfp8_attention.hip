@@ -14,6 +14,7 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float v16f __attribute__((ext_vector_type(16)));
 typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 4;          // waves of a thread block; they share nothing but caches
@@ -77,20 +78,33 @@ __device__ __forceinline__ v4f mfma16(const f16x8& a, const f16x8& b, const v4f&
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
+__device__ __forceinline__ v16f mfma32(const bf16x8& a, const bf16x8& b, const v16f& c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ v16f mfma32(const f16x8& a, const f16x8& b, const v16f& c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+}
+
 // Maximum that keeps a NaN (one instruction for three operands, no quieting of its inputs).
 __device__ __forceinline__ float max_of(float a, float b) { return __builtin_elementwise_maximum(a, b); }
 
-// Maximum and sum over the four lanes that hold one query's column (lanes l, l + 16, l + 32, l + 48).
+// Maximum and sum over the lanes that hold one query's column: l and l + 32, or l, l + 16, l + 32 and l + 48.
+__device__ __forceinline__ float pair_max(float x) {
+    const u32x2 s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return max_of(__uint_as_float(s.x), __uint_as_float(s.y));
+}
+__device__ __forceinline__ float pair_sum(float x) {
+    const u32x2 s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(s.x) + __uint_as_float(s.y);
+}
 __device__ __forceinline__ float column_max(float x) {
-    u32x2 s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    x = max_of(__uint_as_float(s.x), __uint_as_float(s.y));
-    s = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = pair_max(x);
+    const u32x2 s = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
     return max_of(__uint_as_float(s.x), __uint_as_float(s.y));
 }
 __device__ __forceinline__ float column_sum(float x) {
-    u32x2 s = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    x = __uint_as_float(s.x) + __uint_as_float(s.y);
-    s = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = pair_sum(x);
+    const u32x2 s = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
     return __uint_as_float(s.x) + __uint_as_float(s.y);
 }
 
@@ -130,19 +144,6 @@ __device__ __forceinline__ void join_factors(float& M, float m, float& a, float&
     M = top;
 }
 
-// Joins a row tile's state (m, l, o; o in units of ref) to that of the units before it.
-template <int NT>
-__device__ __forceinline__ void join_state(float& M, float& L, v4f (&O)[NT], float m, float l, const v4f (&o)[NT], float ref) {
-    float x, y;
-    join_factors(M, m, x, y);
-    L = fmaf(L, x, column_sum(l) * y);
-    y *= ref;
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) O[t][i] = fmaf(O[t][i], x, o[t][i] * y);
-}
-
 // Sixteen codes of every operand row: a block's keys or values as a wave loads them.
 template <int D>
 struct Raw {
@@ -159,44 +160,83 @@ __device__ __forceinline__ void load_raw(Raw<D>& r, const uint8_t* block, int la
     }
 }
 
-// One query row's results: bf16 channels, and their 1x128 codes where they are wanted.
+// The running softmax state of 32 query rows, as 32x32 products leave it.  Lane l holds query l % 32, with l / 32 = h: the
+// 4 channels 32 t + 8 j + 4 h .. + 3 of every t and j < 4, and of a block's keys those at 32 t + 8 j + 4 h .. + 3.  Their
+// shares of the denominator are kept in two, j even and j odd: the shares of the lanes h and h + 2 of four that hold a
+// query in the 16-row state.
 template <int D>
-__device__ __forceinline__ void store_row(const AttnArgs& a, int token, int head, int lane, const v4f (&o)[D / 16],
+struct Wide {
+    float m, l[2];
+    v16f o[D / 32];
+    __device__ __forceinline__ void clear() {
+        m = -INFINITY;
+        l[0] = l[1] = 0.0f;
+#pragma unroll
+        for (int t = 0; t < D / 32; ++t) o[t] = v16f{};
+    }
+    __device__ __forceinline__ float sum() const { return pair_sum(l[0] + l[1]); }
+};
+
+__device__ __forceinline__ float top_score(const v16f (&s)[2]) {
+    float top = max_of(max_of(s[0][0], s[0][1]), s[0][2]);
+#pragma unroll
+    for (int i = 3; i < 31; i += 2) top = max_of(max_of(top, s[i / 16][i % 16]), s[(i + 1) / 16][(i + 1) % 16]);
+    return pair_max(max_of(top, s[1][15]));
+}
+
+// Joins a state (m, l, o; l summed over the column, o in units of ref) to that of the units before it.
+template <int NT>
+__device__ __forceinline__ void join_state(float& M, float& L, v16f (&O)[NT], float m, float l, const v16f (&o)[NT], float ref) {
+    float x, y;
+    join_factors(M, m, x, y);
+    L = fmaf(L, x, l * y);
+    y *= ref;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) O[t][i] = fmaf(O[t][i], x, o[t][i] * y);
+}
+
+// One query row's results: bf16 channels, and their 1x128 codes where they are wanted.  The two lanes of a row exchange
+// groups of 4 channels, so that each stores 8 in a row.
+template <int D>
+__device__ __forceinline__ void store_row(const AttnArgs& a, int token, int head, int lane, const v16f (&o)[D / 32],
                                           float inv, bool live) {
-    uint2 y[D / 16];
+    uint4 y[D / 16];
     uint32_t most = 0;
 #pragma unroll
-    for (int t = 0; t < D / 16; ++t) {
-        const bf16x2 lo = {(__bf16)(o[t].x * inv), (__bf16)(o[t].y * inv)};
-        const bf16x2 hi = {(__bf16)(o[t].z * inv), (__bf16)(o[t].w * inv)};
-        y[t] = make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
-        most = pkmax16(most, max_mag2(y[t].x, y[t].y));
+    for (int n = 0; n < D / 16; ++n) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bf16x2 b = {(__bf16)(o[n / 2][n % 2 * 8 + 2 * i] * inv), (__bf16)(o[n / 2][n % 2 * 8 + 2 * i + 1] * inv)};
+            w[i] = __builtin_bit_cast(uint32_t, b);
+        }
+        const u32x2 u = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+        const u32x2 v = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+        y[n] = make_uint4(u.x, v.x, u.y, v.y);
+        most = pkmax16(most, pkmax16(max_mag2(w[0], w[1]), max_mag2(w[2], w[3])));
     }
-    const int64_t at = ((int64_t)token * a.q_heads + head) * D + lane / 16 * 4;
+    const int64_t at = ((int64_t)token * a.q_heads + head) * D + lane / 32 * 8;
     if (a.o && live) {
 #pragma unroll
-        for (int t = 0; t < D / 16; ++t) *reinterpret_cast<uint2*>(a.o + at + t * 16) = y[t];
+        for (int n = 0; n < D / 16; ++n) *reinterpret_cast<uint4*>(a.o + at + n * 16) = y[n];
     }
     if (D == 128 && a.oq) {
         most = max(most & 0xFFFFu, most >> 16);
-        most = max(most, (uint32_t)__shfl_xor((int)most, 16));
         most = max(most, (uint32_t)__shfl_xor((int)most, 32));
         const GroupScale g = make_group_scale(bf16_to_f32(most));
 #pragma unroll
-        for (int t = 0; t < D / 16; t += 2) {
+        for (int n = 0; n < D / 16; ++n) {
+            const uint32_t w[4] = {y[n].x, y[n].y, y[n].z, y[n].w};
             float x[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const uint32_t w = j % 4 < 2 ? y[t + j / 4].x : y[t + j / 4].y;
-                x[j] = j % 2 ? __uint_as_float(w & 0xFFFF0000u) : bf16_to_f32(w & 0xFFFFu);
-            }
+            for (int j = 0; j < 8; ++j)
+                x[j] = j % 2 ? __uint_as_float(w[j / 2] & 0xFFFF0000u) : bf16_to_f32(w[j / 2] & 0xFFFFu);
             const uint2 codes = encode8(x, g);
-            if (live) {
-                *reinterpret_cast<uint32_t*>(a.oq + at + t * 16) = codes.x;
-                *reinterpret_cast<uint32_t*>(a.oq + at + t * 16 + 16) = codes.y;
-            }
+            if (live) *reinterpret_cast<uint2*>(a.oq + at + n * 16) = codes;
         }
-        if (live && lane < 16) a.os[(int64_t)head * a.tokens + token] = g.s;
+        if (live && lane < 32) a.os[(int64_t)head * a.tokens + token] = g.s;
     }
 }
 
@@ -253,6 +293,19 @@ __device__ __forceinline__ void load_queries(bf16x8 (&q)[RT][D / 32], const Attn
             if (row < rows) x = *reinterpret_cast<const uint4*>(p + k * 32);
             q[rt][k] = __builtin_bit_cast(bf16x8, x);
         }
+    }
+}
+
+template <int D>
+__device__ __forceinline__ void load_queries(bf16x8 (&q)[D / 16], const AttnArgs& a, const KvUnit& u, int head, int row0,
+                                             int rows, int lane) {
+    const int row = row0 + lane % 32, tok = row / a.group;
+    const uint16_t* p = a.q + (u.row + tok) * a.ldq + ((int64_t)head * a.group + row % a.group) * D + lane / 32 * 8;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (row < rows) x = *reinterpret_cast<const uint4*>(p + k * 16);
+        q[k] = __builtin_bit_cast(bf16x8, x);
     }
 }
 
@@ -313,6 +366,42 @@ __device__ __forceinline__ void add_values(Softmax<D, RT>& st, int t, const T& v
     }
 }
 
+// The same for 32 rows.
+template <bool START, int D>
+__device__ __forceinline__ void take_top(Wide<D>& st, const v16f (&s)[2], float c) {
+    const float m = fmaf(top_score(s), c, -kLead);
+    if (START) {
+        st.m = m;
+        st.l[0] = st.l[1] = 0.0f;
+        return;
+    }
+    const bool grown = m > st.m + kSlack;
+    if (!__any(grown)) return;
+    const float to = grown ? m : st.m;
+    const float f = __builtin_amdgcn_exp2f(st.m - to);
+    st.l[0] *= f;
+    st.l[1] *= f;
+#pragma unroll
+    for (int t = 0; t < D / 32; ++t) st.o[t] *= f;
+    st.m = to;
+}
+template <int D>
+__device__ __forceinline__ void take_half(Wide<D>& st, const v16f (&s)[2], float c, float log_r, float inv_r, int k,
+                                          f16x8 (&p)[2][2]) {
+    const float base = log_r - st.m;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float e = __builtin_amdgcn_exp2f(fmaf(s[k][j / 4 * 8 + g * 4 + j % 4], c, base));
+            sum += e;
+            p[k][g][j] = (_Float16)e;
+        }
+        st.l[g] = fmaf(sum, inv_r, st.l[g]);
+    }
+}
+
 // Whether some of a value operand's exponents are all ones (infinities, NaN): then bit 15 or 31 of the result is set.
 __device__ __forceinline__ uint32_t all_ones(const uint4& v) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -322,24 +411,32 @@ __device__ __forceinline__ uint32_t all_ones(const uint4& v) {
     return odd & 0x80008000u;
 }
 
+// Takes such values out of an operand; mark: 1 in their places.
+__device__ __forceinline__ bf16x8 part_odd(const uint4& v, bf16x8& mark) {
+    uint32_t w[4] = {v.x, v.y, v.z, v.w}, m[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m[i] = ((w[i] & 0x7F80u) == 0x7F80u ? 0x3F80u : 0u) | ((w[i] & 0x7F800000u) == 0x7F800000u ? 0x3F800000u : 0u);
+        w[i] &= ~((m[i] & 0xFFFFu ? 0xFFFFu : 0u) | (m[i] >> 16 ? 0xFFFF0000u : 0u));
+    }
+    mark = __builtin_bit_cast(bf16x8, make_uint4(m[0], m[1], m[2], m[3]));
+    return __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
+}
+
 // The unit's own block, bf16 with the causal mask, into an empty state (whatever the registers hold).  keys, values:
-// the block's operands, 64 lanes of 16 bytes each.  AHEAD: the values are loaded before the scores are formed (from
-// memory, not from LDS); otherwise odd says whether there are infinities or NaN among the values.  Keys behind the last
-// row's own come in halves of the block: the second is left out where no row reaches it (it would add zeros).
-template <bool AHEAD, int D, int RT>
+// the block's operands, 64 lanes of 16 bytes each; the values are loaded before the scores are formed.  Keys behind the
+// last row's own come in halves of the block: the second is left out where no row reaches it (it would add zeros).
+template <int D, int RT>
 __device__ __forceinline__ void own_block(Softmax<D, RT>& st, const bf16x8 (&q)[RT][D / 32], float scale_log2,
                                           int offset, int group, int row0, const bf16x8* keys, const uint4* values,
-                                          bool odd, int lane) {
+                                          int lane) {
     constexpr int NK = D / 32, NT = D / 16;
     const bool both = offset + (row0 + 16 * RT - 1) / group >= 32;
-    uint4 ahead[AHEAD ? NT : 1][2];
-    if (AHEAD) {
+    uint4 value[NT][2];
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) ahead[AHEAD ? t : 0][k] = values[(t * 2 + k) * 64 + lane];
-    }
-    auto value = [&](int t, int k) { return AHEAD ? ahead[AHEAD ? t : 0][k] : values[(t * 2 + k) * 64 + lane]; };
+        for (int k = 0; k < 2; ++k) value[t][k] = values[(t * 2 + k) * 64 + lane];
     v4f s[RT][4];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -393,19 +490,16 @@ __device__ __forceinline__ void own_block(Softmax<D, RT>& st, const bf16x8 (&q)[
             for (int i = 0; i < 8; ++i) p[rt][1][i] = rest[rt][1][i] = (__bf16)0.0f;
         }
     }
-    if (AHEAD) {
-        uint32_t any = 0;
+    uint32_t odd = 0;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) any |= all_ones(ahead[AHEAD ? t : 0][0]) | all_ones(ahead[AHEAD ? t : 0][1]);
-        odd = __any(any != 0);
-    }
-    if (__builtin_expect(!odd, 1)) {
+    for (int t = 0; t < NT; ++t) odd |= all_ones(value[t][0]) | all_ones(value[t][1]);
+    if (__builtin_expect(!__any(odd != 0), 1)) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             if (k && !both) break;
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                const bf16x8 x = __builtin_bit_cast(bf16x8, value(t, k));
+                const bf16x8 x = __builtin_bit_cast(bf16x8, value[t][k]);
 #pragma unroll
                 for (int rt = 0; rt < RT; ++rt) {
                     const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -424,22 +518,15 @@ __device__ __forceinline__ void own_block(Softmax<D, RT>& st, const bf16x8 (&q)[
         for (int rt = 0; rt < RT; ++rt) bad[rt] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const uint4 v = value(t, k);
-            uint32_t w[4] = {v.x, v.y, v.z, v.w}, mark[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                mark[i] = ((w[i] & 0x7F80u) == 0x7F80u ? 0x3F80u : 0u) |
-                          ((w[i] & 0x7F800000u) == 0x7F800000u ? 0x3F800000u : 0u);
-                w[i] &= ~((mark[i] & 0xFFFFu ? 0xFFFFu : 0u) | (mark[i] >> 16 ? 0xFFFF0000u : 0u));
-            }
-            const bf16x8 x = __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
+            bf16x8 mark;
+            const bf16x8 x = part_odd(value[t][k], mark);
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) {
                 bf16x8 seen;
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     seen[j] = (__bf16)(k * 32 + j / 4 * 16 + lane / 16 * 4 + j % 4 <= place[rt] ? 1.0f : 0.0f);
-                bad[rt] = mfma16(__builtin_bit_cast(bf16x8, make_uint4(mark[0], mark[1], mark[2], mark[3])), seen, bad[rt]);
+                bad[rt] = mfma16(mark, seen, bad[rt]);
                 const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
                 st.o[rt][t] = mfma16(x, p[rt][k], mfma16(x, rest[rt][k], k ? st.o[rt][t] : z));
             }
@@ -448,6 +535,89 @@ __device__ __forceinline__ void own_block(Softmax<D, RT>& st, const bf16x8 (&q)[
         for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) st.o[rt][t][i] = bad[rt][i] > 0.0f ? NAN : st.o[rt][t][i];
+    }
+}
+
+// The same for 32 rows whose operands are in LDS; odd: there are infinities or NaN among the values.
+template <int D>
+__device__ __forceinline__ void own_block(Wide<D>& st, const bf16x8 (&q)[D / 16], float scale_log2, int offset, int group,
+                                          int row0, const bf16x8 (*keys)[64], const f16x8 (*values)[64], bool odd, int lane) {
+    constexpr int NK = D / 16, NT = D / 32;
+    const bool both = offset + (row0 + 31) / group >= 32;
+    const int place = offset + (row0 + lane % 32) / group;
+    v16f s[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (h && !both) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[h][i] = -INFINITY;
+            break;
+        }
+#pragma unroll
+        for (int k = 0; k < NK; ++k) s[h] = mfma32(keys[h * NK + k][lane], q[k], k ? s[h] : v16f{});
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (h * 32 + i / 4 * 8 + lane / 32 * 4 + i % 4 > place) s[h][i] = -INFINITY;
+    }
+    st.m = top_score(s) * scale_log2;
+    st.l[0] = st.l[1] = 0.0f;
+    bf16x8 p[2][2], rest[2][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (h && !both) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) p[h][i / 8][i % 8] = rest[h][i / 8][i % 8] = (__bf16)0.0f;
+            break;
+        }
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float e = __builtin_amdgcn_exp2f(fmaf(s[h][j / 4 * 8 + g * 4 + j % 4], scale_log2, -st.m));
+                st.l[g] += e;
+                p[h][g][j] = (__bf16)e;
+                rest[h][g][j] = (__bf16)(e - (float)(__bf16)e);
+            }
+    }
+    if (__builtin_expect(!odd, 1)) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            if (h && !both) break;
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                bf16x8 x[2];
+#pragma unroll
+                for (int g = 0; g < 2; ++g) x[g] = __builtin_bit_cast(bf16x8, values[t * 4 + h * 2 + g][lane]);
+#pragma unroll
+                for (int g = 0; g < 2; ++g) st.o[t] = mfma32(x[g], rest[h][g], h || g ? st.o[t] : v16f{});
+#pragma unroll
+                for (int g = 0; g < 2; ++g) st.o[t] = mfma32(x[g], p[h][g], st.o[t]);
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        v16f bad = {};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            bf16x8 x[2];
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                bf16x8 mark, seen;
+                x[g] = part_odd(__builtin_bit_cast(uint4, values[t * 4 + h * 2 + g][lane]), mark);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    seen[j] = (__bf16)(h * 32 + j / 4 * 16 + g * 8 + lane / 32 * 4 + j % 4 <= place ? 1.0f : 0.0f);
+                bad = mfma32(mark, seen, bad);
+            }
+#pragma unroll
+            for (int g = 0; g < 2; ++g) st.o[t] = mfma32(x[g], rest[h][g], h || g ? st.o[t] : v16f{});
+#pragma unroll
+            for (int g = 0; g < 2; ++g) st.o[t] = mfma32(x[g], p[h][g], st.o[t]);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) st.o[t][i] = bad[i] > 0.0f ? NAN : st.o[t][i];
     }
 }
 
@@ -467,6 +637,18 @@ __device__ __forceinline__ void store_part(const Softmax<D, RT>& st, float ref, 
     }
 }
 
+template <int D>
+__device__ __forceinline__ void store_part(float m, float l, const v16f (&o)[D / 32], const AttnArgs& a, int unit, int head,
+                                           int part, int row, int rows, int lane) {
+    if (row >= rows) return;
+    const int64_t at = (((int64_t)unit * a.kv_heads + head) * a.parts + part) * a.max_rows + row;
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n)
+        *reinterpret_cast<v4f*>(a.part_o + at * D + n * 8 + lane / 32 * 4) =
+            v4f{o[n / 4][n % 4 * 4], o[n / 4][n % 4 * 4 + 1], o[n / 4][n % 4 * 4 + 2], o[n / 4][n % 4 * 4 + 3]};
+    if (lane < 32) a.part_ml[at] = make_float2(m, l);
+}
+
 // The operands of a recent block: its keys, and behind them (64 D elements on) its values.
 template <int D>
 __device__ __forceinline__ const uint4* recent_block(const AttnArgs& a, int recent, int head) {
@@ -478,7 +660,7 @@ __device__ __forceinline__ const uint4* recent_block(const AttnArgs& a, int rece
 // and sum need two exchanges between lanes, the factors of a row are plain lane values, and the probabilities
 // are the second product's operand as they are (O^T = V^T P^T; the cache keeps the values in that key order).  Codes
 // are widened to the queries' bf16 and the probabilities' fp16 (both exact) and multiplied by
-// v_mfma_f32_16x16x32; the scales enter in fp32, the keys' in the exponent's argument, the values' on the
+// v_mfma_f32_16x16x32 (or the same in two halves, below); the scales enter in fp32, the keys' in the exponent's argument, the values' on the
 // probabilities.  Rounded below fp32 are only the probabilities (at most 2^-12 of each, an eighth of what bf16
 // would cost, whose error alone equals that of the results' own rounding), and the results.
 //
@@ -514,8 +696,8 @@ __global__ __launch_bounds__(kWaves * 64, RT == 1 ? 3 : 2) void attention_span_k
     float ref = 1.0f;
     if (span == own) {
         const uint4* mem = recent_block<D>(a, u.recent, head);
-        own_block<true, D, RT>(st, q, a.scale_log2, u.offset, a.group, row0, reinterpret_cast<const bf16x8*>(mem),
-                               mem + kKvBlock * D / 8, false, lane);
+        own_block<D, RT>(st, q, a.scale_log2, u.offset, a.group, row0, reinterpret_cast<const bf16x8*>(mem),
+                               mem + kKvBlock * D / 8, lane);
     } else {
         const int first = span * kSpan, last = min(first + kSpan, u.block);
         const int64_t block_bytes = (int64_t)a.kv_heads * 2 * kKvBlock * D;
@@ -625,19 +807,27 @@ __device__ __forceinline__ int ordered_pair(const AttnArgs& a, int pairs, int x)
 }
 
 // attention_tile_kernel walks a run of 128 rows in one block of four waves, and where that is all (up to 4096 tokens
-// before the own block) finishes the rows, else leaves the joining of the runs to attention_join_kernel: for prompts, where the time is that of
-// the arithmetic.  Each wave widens a quarter of a block's codes into LDS, as operands, and all four read them there,
-// so that a code is widened once per 128 rows instead of once per 32 (the conversions would otherwise take a third
-// of the vector unit's time).  Two buffers, one barrier per block; a block's codes are loaded from memory two blocks
-// ahead.  A wave forming scores has priority over its SIMD's other wave (a chunk of 2048 at 14336: 777 -> 724 us; giving it
-// to the second product as well changes nothing).  Units are taken in pairs: two of one request share thread blocks, the waves of the first leaving out the last
-// block or so, since a unit's rows (64 query heads per kv head) need not be a multiple of 128.
-// With D = 64 a wave needs 170 registers if it may; held to 168 a third thread block fits a CU (4 prompts of 2048, 16
-// kv heads: 129 -> 113 us; a chunk of 300 at 30000: 481 -> 450 us; held to 128 for a fourth it spills).
+// before the own block) finishes the rows, else leaves the joining of the runs to attention_join_kernel: for prompts,
+// where the time is that of the arithmetic.  Each wave widens a quarter of a block's codes into LDS, as operands, and
+// all four read them there, so that a code is widened once per 128 rows instead of once per 32 (the conversions would
+// otherwise take a third of the vector unit's time).  Two buffers, one barrier per block; a block's codes are loaded
+// from memory two blocks ahead.  A wave forming scores has priority over its SIMD's other wave (a chunk of 2048 at
+// 14336: 777 -> 724 us; giving it to the second product as well changes nothing).
+//
+// A wave multiplies by v_mfma_f32_32x32x16: a lane then holds half of a query's scores instead of a quarter of two
+// queries', and a block takes 300 instructions instead of 375, 11 % fewer cycles (64 ragged requests up to 4000: 210 ->
+// 191 us; 64 channels, 4 prompts of 2048: 105 -> 97).  Long prompts of 128 channels gain nothing (a chunk of 2048 at 14336:
+// 698 -> 700 us, 8 prompts of 2048: 330 -> 335): the card lowers its clock there, from 2.1 to 1.9 GHz.  Two such products
+// in ascending order of the contraction give bit for bit what one 16x16x32 product gives (the tests compare the forms).
+//
+// Units are taken in pairs: two of one request share thread blocks, the waves of the first leaving out the last block or
+// so, since a unit's rows (64 query heads per kv head) need not be a multiple of 128.  With D = 64 a third thread block
+// fits a CU if a wave is held to 168 registers (4 prompts of 2048, 16 kv heads: 129 -> 113 us; a chunk of 300 at 30000:
+// 481 -> 450 us; held to 128 for a fourth it spills).
 template <int D>
 __global__ __launch_bounds__(kWaves * 64, D == 64 ? 3 : 2) void attention_tile_kernel(AttnArgs a) {
-    constexpr int RT = 2, NT = D / 16, NK = D / 32;
-    constexpr int NL = NT / kWaves;        // loads of a block's keys, and of its values, per wave
+    constexpr int NT = D / 32, NK = D / 16;     // output tiles, contraction steps of the score product
+    constexpr int NL = D / 16 / kWaves;         // loads of a block's keys, and of its values, per wave
     constexpr int NO = kKvBlock * D / 8 / 64;   // operands of a block's keys, and of its values
     __shared__ bf16x8 kt[2][NO][64];
     __shared__ f16x8 vt[2][NO][64];
@@ -656,7 +846,7 @@ __global__ __launch_bounds__(kWaves * 64, D == 64 ? 3 : 2) void attention_tile_k
         const bool fits = first_unit + i < a.num_units &&
                           unit_fits(us[i], a.requests, a.tokens, a.recent_blocks, a.num_blocks) &&
                           rows <= a.max_rows && us[i].block <= a.max_blocks;
-        tiles[i] = fits ? (rows + 16 * RT - 1) / (16 * RT) : 0;
+        tiles[i] = fits ? (rows + 31) / 32 : 0;
     }
     const bool shared = tiles[0] && tiles[1] && us[0].request == us[1].request;
     const int own_chunks = (tiles[0] + kWaves - 1) / kWaves;      // of the first unit, where the two do not share
@@ -682,16 +872,14 @@ __global__ __launch_bounds__(kWaves * 64, D == 64 ? 3 : 2) void attention_tile_k
     const KvUnit u = us[which];
     const int own_run = max(u.block - 1, 0) / kRunBlocks;         // the run whose thread block takes the own block too
     const bool busy = tile < tiles[which] && run <= own_run;
-    const int row0 = tile * (16 * RT), rows = busy ? u.rows * a.group : 0, last = busy ? min(u.block, end) : 0;
+    const int row0 = tile * 32, rows = busy ? u.rows * a.group : 0, last = busy ? min(u.block, end) : 0;
 
-    bf16x8 q[RT][NK];
-    load_queries<D, RT>(q, a, u, head, row0, rows, lane);
-    Softmax<D, RT> st, all;
-    all.clear();
-    auto join = [&](float ref) {
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) join_state(all.m[rt], all.l[rt], all.o[rt], st.m[rt], st.l[rt], st.o[rt], ref);
-    };
+    bf16x8 q[NK];
+    load_queries<D>(q, a, u, head, row0, rows, lane);
+    Wide<D> st;
+    float all_m = -INFINITY, all_l = 0.0f;      // the units joined so far
+    v16f all_o[NT] = {};
+    auto join = [&](float ref) { join_state(all_m, all_l, all_o, st.m, st.sum(), st.o, ref); };
 
     const int64_t block_bytes = (int64_t)a.kv_heads * 2 * kKvBlock * D;
     const uint8_t* codes = a.codes + (int64_t)head * 2 * kKvBlock * D + lane * 16 + wave * (NL * 1024);
@@ -704,14 +892,20 @@ __global__ __launch_bounds__(kWaves * 64, D == 64 ? 3 : 2) void attention_tile_k
             raw[NL + i] = *reinterpret_cast<const uint4*>(p + kKvBlock * D + i * 1024);
         }
     };
+    // Where a lane's 8 elements of operand k of 16 keys or channels t, in the order of 16x16x32 products as memory has it,
+    // belong in that of 32x32x16 products: two t make a tile, and half of the lanes hold each of the two steps that k is.
+    auto place_at = [&](int t, int steps, int k) {
+        return (t / 2 * steps + 2 * k + lane / 32) * 64 + lane / 16 % 2 * 32 + t % 2 * 16 + lane % 16;
+    };
     auto store = [&](int buf, int i) {
-        const int n = 2 * (wave * NL + i % NL);
+        const int n = wave * NL + i % NL;       // line of a block's keys or values
         if (i < NL) {
-            kt[buf][n][lane] = widen(raw[i].x, raw[i].y);
-            kt[buf][n + 1][lane] = widen(raw[i].z, raw[i].w);
+            const int t = n / (NK / 4), k = n % (NK / 4) * 2;
+            (&kt[buf][0][0])[place_at(t, NK, k)] = widen(raw[i].x, raw[i].y);
+            (&kt[buf][0][0])[place_at(t, NK, k + 1)] = widen(raw[i].z, raw[i].w);
         } else {
-            vt[buf][n][lane] = widen_f16(raw[i].x, raw[i].y);
-            vt[buf][n + 1][lane] = widen_f16(raw[i].z, raw[i].w);
+            (&vt[buf][0][0])[place_at(n, 4, 0)] = widen_f16(raw[i].x, raw[i].y);
+            (&vt[buf][0][0])[place_at(n, 4, 1)] = widen_f16(raw[i].z, raw[i].w);
         }
     };
     if (begin < end) {
@@ -729,13 +923,13 @@ __global__ __launch_bounds__(kWaves * 64, D == 64 ? 3 : 2) void attention_tile_k
                 if (begin + b >= end) break;
                 const int buf = i % 2;
                 // Operands come from LDS in a ring, kAhead reads under way before the first is used (left to itself
-                // the compiler reads each just before its use, and every read's latency is waited for); the next
-                // block's codes are widened and stored between the matrix instructions.
-                constexpr int kAhead = 3, kGroup = NO / 4;
+                // the compiler reads each just before its use, and every read's latency is waited for; 3 and 4 ahead
+                // measure the same and spill); the next block's codes are widened and stored between the products.
+                constexpr int kAhead = 2, kGroup = NO / 4;
                 bf16x8 kf[kAhead];
                 __builtin_amdgcn_s_setprio(1);                  // the other wave's vector work fits between these
-                v4f s[RT][4];
-                auto read_k = [&](int f) { kf[f % kAhead] = kt[buf][f % 4 * NK + f / 4][lane]; };
+                v16f s[2];
+                auto read_k = [&](int f) { kf[f % kAhead] = kt[buf][f % 2 * NK + f / 2][lane]; };
 #pragma unroll
                 for (int f = 0; f < kAhead; ++f) read_k(f);
 #pragma unroll
@@ -743,11 +937,7 @@ __global__ __launch_bounds__(kWaves * 64, D == 64 ? 3 : 2) void attention_tile_k
                     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                     for (int f = h * kGroup; f < (h + 1) * kGroup; ++f) {
-#pragma unroll
-                        for (int rt = 0; rt < RT; ++rt) {
-                            const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
-                            s[rt][f % 4] = mfma16(kf[f % kAhead], q[rt][f / 4], f / 4 ? s[rt][f % 4] : z);
-                        }
+                        s[f % 2] = mfma32(kf[f % kAhead], q[f / 2], f / 2 ? s[f % 2] : v16f{});
                         if (f + kAhead < NO) read_k(f + kAhead);
                     }
                     if (h < 2 * NL) store(buf ^ 1, h);          // block b + 1; nobody reads that buffer before the barrier
@@ -756,23 +946,32 @@ __global__ __launch_bounds__(kWaves * 64, D == 64 ? 3 : 2) void attention_tile_k
                 __builtin_amdgcn_s_setprio(0);
                 load(__builtin_amdgcn_readlane(sc.at, min(b + 2, 63)));
                 if (sc.use >> b & 1) {
-                    f16x8 p[RT][2], vf[kAhead];
+                    f16x8 p[2][2], vf[kAhead];
                     const float c = lane_value(sc.c, b), log_r = lane_value(sc.log_r, b), inv_r = lane_value(sc.inv_r, b);
                     if (i == 0) take_top<true>(st, s, c);
                     else take_top<false>(st, s, c);
                     take_half(st, s, c, log_r, inv_r, 0, p);
-                    auto read_v = [&](int f) { vf[f % kAhead] = vt[buf][f % NT * 2 + f / NT][lane]; };
+                    auto read_v = [&](int f) { vf[f % kAhead] = vt[buf][f % NT * 4 + f / NT][lane]; };
 #pragma unroll
                     for (int f = 0; f < kAhead; ++f) read_v(f);
 #pragma unroll
                     for (int h = 0; h < 4; ++h) {
-                        __builtin_amdgcn_sched_barrier(0);
+                        // the second half's exponentials between the first half's products
+                        if (h != 1) __builtin_amdgcn_sched_barrier(0);
                         if (h == 0) take_half(st, s, c, log_r, inv_r, 1, p);
 #pragma unroll
                         for (int f = h * kGroup; f < (h + 1) * kGroup; ++f) {
-                            if (i == 0) add_values<true>(st, f % NT, vf[f % kAhead], p, f / NT);
-                            else add_values<false>(st, f % NT, vf[f % kAhead], p, f / NT);
+                            st.o[f % NT] = mfma32(vf[f % kAhead], p[f / NT / 2][f / NT % 2],
+                                                  i == 0 && f / NT == 0 ? v16f{} : st.o[f % NT]);
                             if (f + kAhead < NO) read_v(f + kAhead);
+                        }
+                        if (h == 1) {
+#pragma unroll
+                            for (int g = 0; g < NO / 2; ++g) {       // a product, a read from LDS, 6 vector instructions
+                                __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);
+                                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                                __builtin_amdgcn_sched_group_barrier(0x2, 6, 0);
+                            }
                         }
                     }
                     __builtin_amdgcn_sched_barrier(0);
@@ -788,46 +987,30 @@ __global__ __launch_bounds__(kWaves * 64, D == 64 ? 3 : 2) void attention_tile_k
 #pragma unroll
     for (int buf = 0; buf < 2; ++buf) {
         if (!tail || (buf && !two)) break;
-        const uint4* mem = recent_block<D>(a, owns[buf], head) + wave * (NO / kWaves * 64) + lane;
+        const uint4* mem = recent_block<D>(a, owns[buf], head) + lane;
 #pragma unroll
         for (int i = 0; i < NO / kWaves; ++i) {
-            kt[buf][wave * (NO / kWaves) + i][lane] = __builtin_bit_cast(bf16x8, mem[i * 64]);
-            const uint4 v = mem[kKvBlock * D / 8 + i * 64];
-            vt[buf][wave * (NO / kWaves) + i][lane] = __builtin_bit_cast(f16x8, v);
+            const int n = wave * (NO / kWaves) + i;
+            const uint4 v = mem[kKvBlock * D / 8 + n * 64];
+            (&kt[buf][0][0])[place_at(n / (NK / 2), NK, n % (NK / 2))] = __builtin_bit_cast(bf16x8, mem[n * 64]);
+            (&vt[buf][0][0])[place_at(n / 2, 4, n % 2)] = __builtin_bit_cast(f16x8, v);
             found |= all_ones(v);
         }
     }
     const bool odd = __syncthreads_or(found != 0);
     if (!busy) return;
     const int unit = first_unit + which, own_part = (u.block + kRunBlocks - 1) / kRunBlocks;
-    if (a.parts && run < own_part) store_part(all, 1.0f, a, unit, head, run, row0, rows, lane);
+    const int row = row0 + lane % 32;
+    if (a.parts && run < own_part) store_part<D>(all_m, all_l, all_o, a, unit, head, run, row, rows, lane);
     if (run < own_run) return;
     const int buf = two ? which : 0;
-    // One row tile at a time, the next one moved to the first's place: both would not fit the registers, and the code
-    // of both would not fit the instruction cache beside the walk's (30 ragged prompts up to 1500: 387 -> 380 us).
-#pragma unroll 1
-    for (int rt = 0; rt < RT; ++rt) {
-        const int tile_row0 = row0 + rt * 16, row = tile_row0 + lane % 16;
-        if (tile_row0 >= rows) break;
-        Softmax<D, 1> own;
-        bf16x8 q1[1][NK];
-#pragma unroll
-        for (int k = 0; k < NK; ++k) q1[0][k] = q[0][k], q[0][k] = q[1][k];
-        own_block<false, D, 1>(own, q1, a.scale_log2, u.offset, a.group, tile_row0, &kt[buf][0][0],
-                               reinterpret_cast<const uint4*>(&vt[buf][0][0]), odd, lane);
-        if (a.parts) {
-            own.l[0] = column_sum(own.l[0]);
-            store_part(own, 1.0f, a, unit, head, own_part, tile_row0, rows, lane);
-            continue;
-        }
-        join_state(all.m[0], all.l[0], all.o[0], own.m[0], own.l[0], own.o[0], 1.0f);
-        store_row<D>(a, u.row + row / a.group, head * a.group + row % a.group, lane, all.o[0], 1.0f / all.l[0],
-                     row < rows);
-        all.m[0] = all.m[1];
-        all.l[0] = all.l[1];
-#pragma unroll
-        for (int t = 0; t < NT; ++t) all.o[0][t] = all.o[1][t];
+    own_block<D>(st, q, a.scale_log2, u.offset, a.group, row0, kt[buf], vt[buf], odd, lane);
+    if (a.parts) {
+        store_part<D>(st.m, st.sum(), st.o, a, unit, head, own_part, row, rows, lane);
+        return;
     }
+    join(1.0f);
+    store_row<D>(a, u.row + row / a.group, head * a.group + row % a.group, lane, all_o, 1.0f / all_l, row < rows);
 }
 
 // Joins n <= N consecutive partial results of a row to the state (M, L, o) of those before them.  Lane s forms the
