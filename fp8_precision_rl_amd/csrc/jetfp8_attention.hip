@@ -48,7 +48,7 @@ struct AttnArgs {
     int tokens, requests, width, num_blocks, recent_blocks, num_units, max_blocks;
     int q_heads, kv_heads, group;  // group: query heads of a kv head
     int max_rows;                  // rows (token, query head) that a unit may have
-    int row_groups;                // row groups of 16 RT rows that cover them
+    int row_groups;                // row groups, each a wave's, that cover them
     int parts;                     // partial results that a row may have, its own block's among them
     int runs;                      // tile kernel: runs, a thread block each
     int ordered;                   // tile kernel: units taken by length
@@ -71,17 +71,17 @@ __device__ __forceinline__ f16x8 widen_f16(uint32_t lo, uint32_t hi) {
     return f16x8{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
 }
 
-__device__ __forceinline__ v4f mfma16(const bf16x8& a, const bf16x8& b, const v4f& c) {
+__device__ __forceinline__ v4f mfma(const bf16x8& a, const bf16x8& b, const v4f& c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
-__device__ __forceinline__ v4f mfma16(const f16x8& a, const f16x8& b, const v4f& c) {
+__device__ __forceinline__ v4f mfma(const f16x8& a, const f16x8& b, const v4f& c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
-__device__ __forceinline__ v16f mfma32(const bf16x8& a, const bf16x8& b, const v16f& c) {
+__device__ __forceinline__ v16f mfma(const bf16x8& a, const bf16x8& b, const v16f& c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
 }
-__device__ __forceinline__ v16f mfma32(const f16x8& a, const f16x8& b, const v16f& c) {
+__device__ __forceinline__ v16f mfma(const f16x8& a, const f16x8& b, const v16f& c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
@@ -108,31 +108,66 @@ __device__ __forceinline__ float column_sum(float x) {
     return __uint_as_float(s.x) + __uint_as_float(s.y);
 }
 
-// Running softmax state of 16 RT query rows.  Lane l holds query l % 16 of each tile: the reference m of its
-// exponentials (in log2), its own share of the denominator, and the 4 channels 16 t + 4 (l / 16) .. + 3 of every t.
-template <int D, int RT>
-struct Softmax {
-    float m[RT], l[RT];
-    v4f o[RT][D / 16];
-    __device__ __forceinline__ void clear() {
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-            m[rt] = -INFINITY;
-            l[rt] = 0.0f;
-#pragma unroll
-            for (int t = 0; t < D / 16; ++t) o[rt][t] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-        }
-    }
+template <int R>
+struct AccOf {
+    typedef v4f type;
+};
+template <>
+struct AccOf<32> {
+    typedef v16f type;
 };
 
-// Largest of the 64 scores that a query has in a block.
-__device__ __forceinline__ float top_score(const v4f (&s)[4]) {
-    float top = max_of(max_of(s[0].x, s[0].y), s[0].z);
-    top = max_of(max_of(top, s[0].w), s[1].x);
+// Running softmax state of R query rows: 16, for products of 16x16x32, or 32, for products of 32x32x16.  Lane l, with
+// g = l / R, holds query l % R: the reference m of its exponentials (in log2); of a block's keys and of each R channels
+// those at 8 j + 4 g .. + 3 (R = 32, j < 4; R = 16: j = 0); its shares l of the denominator.  With R = 32 these are two,
+// those that lanes g and g + 2 hold with R = 16, and two products in ascending order of the contraction give what one
+// of 16x16x32 gives, bit for bit: a row's results are the same in both.
+template <int D, int R>
+struct State {
+    typedef typename AccOf<R>::type Acc;
+    static constexpr int kShares = R / 16;             // operands of a 32-long contraction
+    static constexpr int kTiles = kKvBlock / R;        // of a block's keys
+    static constexpr int kOut = D / R;                 // of the channels
+    static constexpr int kSteps = D / 32 * kShares;    // of the score product
+    typedef Acc Scores[kTiles];
+    typedef bf16x8 Queries[kSteps];
+    float m, l[kShares];
+    Acc o[kOut];
+    __device__ __forceinline__ void empty() {
 #pragma unroll
-    for (int i = 5; i < 15; i += 2) top = max_of(max_of(top, s[i / 4][i % 4]), s[(i + 1) / 4][(i + 1) % 4]);
-    return column_max(max_of(top, s[3].w));
-}
+        for (int g = 0; g < kShares; ++g) l[g] = 0.0f;
+    }
+    __device__ __forceinline__ void clear() {
+        m = -INFINITY;
+        empty();
+#pragma unroll
+        for (int t = 0; t < kOut; ++t) o[t] = Acc{};
+    }
+    __device__ __forceinline__ float sum() const {
+        return R == 32 ? pair_sum(l[0] + l[kShares - 1]) : column_sum(l[0]);
+    }
+    // Score j of share g of half h of a block's keys, and the key that it belongs to.
+    static __device__ __forceinline__ float score(const Scores& s, int h, int g, int j) {
+        return R == 32 ? s[h][j / 4 * 8 + g * 4 + j % 4] : s[h * (kTiles / 2) + j / 4][j % 4];
+    }
+    static __device__ __forceinline__ void set_score(Scores& s, int h, int g, int j, float x) {
+        if (R == 32) s[h][j / 4 * 8 + g * 4 + j % 4] = x;
+        else s[h * (kTiles / 2) + j / 4][j % 4] = x;
+    }
+    static __device__ __forceinline__ int key(int h, int g, int j, int lane) {
+        return h * 32 + j / 4 * 16 + g * 8 + lane / R * 4 + j % 4;
+    }
+    // Largest of the 64 scores that a query has in a block.
+    static __device__ __forceinline__ float top_score(const Scores& s) {
+        constexpr int n = 16 * kShares;                // of a lane
+        auto at = [&](int i) { return R == 32 ? s[i / 16][i % 16] : s[i / 4 % kTiles][i % 4]; };
+        float top = max_of(max_of(at(0), at(1)), at(2));
+#pragma unroll
+        for (int i = 3; i < n - 1; i += 2) top = max_of(max_of(top, at(i)), at(i + 1));
+        top = max_of(top, at(n - 1));
+        return R == 32 ? pair_max(top) : column_max(top);
+    }
+};
 
 // Joins the state of the next summation unit (its l already summed over the column) to that of those before it.
 // A unit that has no keys at all (every block id out of range) has m = -inf and adds nothing.
@@ -144,49 +179,37 @@ __device__ __forceinline__ void join_factors(float& M, float m, float& a, float&
     M = top;
 }
 
-// Sixteen codes of every operand row: a block's keys or values as a wave loads them.
+// Where a lane's 8 elements (16 bytes) of operand `step` of tile `tile` lie in a fragment of memory's order, which is that
+// of 16x16x32 products: fragments of 16 rows and 32 of the contraction, `steps` of them after another for the same rows.
+// With R = 32 a tile's rows are those of two fragments, and a step is half of one.
+template <int R>
+__device__ __forceinline__ int operand_at(int tile, int step, int steps, int lane) {
+    if (R == 16) return (tile * steps + step) * 64 + lane;
+    return ((2 * tile + lane % 32 / 16) * steps + step / 2) * 64 + (step % 2 * 2 + lane / 32) * 16 + lane % 16;
+}
+
+// A block's keys or values as a wave loads them: 16 codes, of two fragments after another.
 template <int D>
 struct Raw {
     uint4 w[D / 16];
 };
-template <bool ONCE, int D>
+template <int R, bool VALUES, int D>
 __device__ __forceinline__ void load_raw(Raw<D>& r, const uint8_t* block, int lane) {
     typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+    constexpr int steps = VALUES ? 1 : D / 64, shares = R / 16;
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {
-        const u32x4* p = reinterpret_cast<const u32x4*>(block + i * 1024 + lane * 16);
-        const u32x4 x = ONCE ? __builtin_nontemporal_load(p) : *p;
+        const int at = operand_at<R>(i / (steps * shares), i % (steps * shares), steps, lane);
+        const u32x4* p = reinterpret_cast<const u32x4*>(block) + at;
+        const u32x4 x = R == 16 ? __builtin_nontemporal_load(p) : *p;
         r.w[i] = make_uint4(x.x, x.y, x.z, x.w);
     }
 }
 
-// The running softmax state of 32 query rows, as 32x32 products leave it.  Lane l holds query l % 32, with l / 32 = h: the
-// 4 channels 32 t + 8 j + 4 h .. + 3 of every t and j < 4, and of a block's keys those at 32 t + 8 j + 4 h .. + 3.  Their
-// shares of the denominator are kept in two, j even and j odd: the shares of the lanes h and h + 2 of four that hold a
-// query in the 16-row state.
-template <int D>
-struct Wide {
-    float m, l[2];
-    v16f o[D / 32];
-    __device__ __forceinline__ void clear() {
-        m = -INFINITY;
-        l[0] = l[1] = 0.0f;
-#pragma unroll
-        for (int t = 0; t < D / 32; ++t) o[t] = v16f{};
-    }
-    __device__ __forceinline__ float sum() const { return pair_sum(l[0] + l[1]); }
-};
-
-__device__ __forceinline__ float top_score(const v16f (&s)[2]) {
-    float top = max_of(max_of(s[0][0], s[0][1]), s[0][2]);
-#pragma unroll
-    for (int i = 3; i < 31; i += 2) top = max_of(max_of(top, s[i / 16][i % 16]), s[(i + 1) / 16][(i + 1) % 16]);
-    return pair_max(max_of(top, s[1][15]));
-}
-
 // Joins a state (m, l, o; l summed over the column, o in units of ref) to that of the units before it.
 template <int NT>
-__device__ __forceinline__ void join_state(float& M, float& L, v16f (&O)[NT], float m, float l, const v16f (&o)[NT], float ref) {
+__device__ __forceinline__ void join_state(float& M, float& L, v16f (&O)[NT], float m, float l, const v16f (&o)[NT],
+                                           float ref) {
     float x, y;
     join_factors(M, m, x, y);
     L = fmaf(L, x, l * y);
@@ -279,124 +302,55 @@ __device__ __forceinline__ float lane_value(float x, int i) {
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(x), i));
 }
 
-// The queries of a wave's row tiles, rows (token, query head of the group) from row0 on; rows behind the last are 0.
-template <int D, int RT>
-__device__ __forceinline__ void load_queries(bf16x8 (&q)[RT][D / 32], const AttnArgs& a, const KvUnit& u, int head,
+// The queries of a wave's rows, (token, query head of the group) from row0 on; rows behind the last are 0.
+template <int D, int R>
+__device__ __forceinline__ void load_queries(bf16x8 (&q)[D / 32 * (R / 16)], const AttnArgs& a, const KvUnit& u, int head,
                                              int row0, int rows, int lane) {
+    const int row = row0 + lane % R, tok = row / a.group;
+    const uint16_t* p = a.q + (u.row + tok) * a.ldq + ((int64_t)head * a.group + row % a.group) * D + lane / R * 8;
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const int row = row0 + rt * 16 + lane % 16, tok = row / a.group;
-        const uint16_t* p = a.q + (u.row + tok) * a.ldq + ((int64_t)head * a.group + row % a.group) * D + lane / 16 * 8;
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (row < rows) x = *reinterpret_cast<const uint4*>(p + k * 32);
-            q[rt][k] = __builtin_bit_cast(bf16x8, x);
-        }
-    }
-}
-
-template <int D>
-__device__ __forceinline__ void load_queries(bf16x8 (&q)[D / 16], const AttnArgs& a, const KvUnit& u, int head, int row0,
-                                             int rows, int lane) {
-    const int row = row0 + lane % 32, tok = row / a.group;
-    const uint16_t* p = a.q + (u.row + tok) * a.ldq + ((int64_t)head * a.group + row % a.group) * D + lane / 32 * 8;
-#pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
+    for (int k = 0; k < D / 32 * (R / 16); ++k) {
         uint4 x = make_uint4(0, 0, 0, 0);
-        if (row < rows) x = *reinterpret_cast<const uint4*>(p + k * 16);
+        if (row < rows) x = *reinterpret_cast<const uint4*>(p + k * (512 / R));
         q[k] = __builtin_bit_cast(bf16x8, x);
     }
 }
 
 // Takes the largest scores of a cache block's 64 keys (s, in units of c) into the rows' references.  START: the first
-// block of a span, whose states are empty (whatever the registers hold) and take its maximum as it is.
-template <bool START, int D, int RT>
-__device__ __forceinline__ void take_top(Softmax<D, RT>& st, const v4f (&s)[RT][4], float c) {
-    float m[RT];
-    bool grown = false;
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        m[rt] = fmaf(top_score(s[rt]), c, -kLead);
-        if (START) {
-            st.m[rt] = m[rt];
-            st.l[rt] = 0.0f;
-        } else {
-            grown |= m[rt] > st.m[rt] + kSlack;
-        }
-    }
-    if (START || !__any(grown)) return;
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const float to = m[rt] > st.m[rt] + kSlack ? m[rt] : st.m[rt];
-        const float f = __builtin_amdgcn_exp2f(st.m[rt] - to);       // 1 for the rows that keep theirs
-        st.l[rt] *= f;
-#pragma unroll
-        for (int t = 0; t < D / 16; ++t) st.o[rt][t] *= f;
-        st.m[rt] = to;
-    }
-}
-
-// The probabilities of half a block's keys (32 k .. 32 k + 31), times the values' share, as an operand of the second
-// product; their sum goes into the denominator.
-template <int D, int RT>
-__device__ __forceinline__ void take_half(Softmax<D, RT>& st, const v4f (&s)[RT][4], float c, float log_r, float inv_r,
-                                          int k, f16x8 (&p)[RT][2]) {
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const float base = log_r - st.m[rt];
-        float sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float e = __builtin_amdgcn_exp2f(fmaf(s[rt][2 * k + j / 4][j % 4], c, base));
-            sum += e;
-            p[rt][k][j] = (_Float16)e;
-        }
-        st.l[rt] = fmaf(sum, inv_r, st.l[rt]);
-    }
-}
-
-// Adds a block's product to the rows' accumulators (START: the accumulators begin with it).
-template <bool START, int D, int RT, typename T>
-__device__ __forceinline__ void add_values(Softmax<D, RT>& st, int t, const T& v, const T (&p)[RT][2], int k) {
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
-        st.o[rt][t] = mfma16(v, p[rt][k], START && k == 0 ? z : st.o[rt][t]);
-    }
-}
-
-// The same for 32 rows.
-template <bool START, int D>
-__device__ __forceinline__ void take_top(Wide<D>& st, const v16f (&s)[2], float c) {
-    const float m = fmaf(top_score(s), c, -kLead);
+// block of a span, whose state is empty (whatever the registers hold) and takes its maximum as it is.
+template <bool START, int D, int R>
+__device__ __forceinline__ void take_top(State<D, R>& st, const typename State<D, R>::Scores& s, float c) {
+    const float m = fmaf(State<D, R>::top_score(s), c, -kLead);
     if (START) {
         st.m = m;
-        st.l[0] = st.l[1] = 0.0f;
+        st.empty();
         return;
     }
     const bool grown = m > st.m + kSlack;
     if (!__any(grown)) return;
     const float to = grown ? m : st.m;
-    const float f = __builtin_amdgcn_exp2f(st.m - to);
-    st.l[0] *= f;
-    st.l[1] *= f;
+    const float f = __builtin_amdgcn_exp2f(st.m - to);       // 1 for the rows that keep theirs
 #pragma unroll
-    for (int t = 0; t < D / 32; ++t) st.o[t] *= f;
+    for (int g = 0; g < R / 16; ++g) st.l[g] *= f;
+#pragma unroll
+    for (int t = 0; t < D / R; ++t) st.o[t] *= f;
     st.m = to;
 }
-template <int D>
-__device__ __forceinline__ void take_half(Wide<D>& st, const v16f (&s)[2], float c, float log_r, float inv_r, int k,
-                                          f16x8 (&p)[2][2]) {
+
+// The probabilities of half a block's keys (32 h .. 32 h + 31), times the values' share, as operands of the second
+// product; their sum goes into the denominator.
+template <int D, int R>
+__device__ __forceinline__ void take_half(State<D, R>& st, const typename State<D, R>::Scores& s, float c, float log_r,
+                                          float inv_r, int h, f16x8 (&p)[2][R / 16]) {
     const float base = log_r - st.m;
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
+    for (int g = 0; g < R / 16; ++g) {
         float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const float e = __builtin_amdgcn_exp2f(fmaf(s[k][j / 4 * 8 + g * 4 + j % 4], c, base));
+            const float e = __builtin_amdgcn_exp2f(fmaf(st.score(s, h, g, j), c, base));
             sum += e;
-            p[k][g][j] = (_Float16)e;
+            p[h][g][j] = (_Float16)e;
         }
         st.l[g] = fmaf(sum, inv_r, st.l[g]);
     }
@@ -423,88 +377,73 @@ __device__ __forceinline__ bf16x8 part_odd(const uint4& v, bf16x8& mark) {
     return __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
 }
 
-// The unit's own block, bf16 with the causal mask, into an empty state (whatever the registers hold).  keys, values:
-// the block's operands, 64 lanes of 16 bytes each; the values are loaded before the scores are formed.  Keys behind the
-// last row's own come in halves of the block: the second is left out where no row reaches it (it would add zeros).
-template <int D, int RT>
-__device__ __forceinline__ void own_block(Softmax<D, RT>& st, const bf16x8 (&q)[RT][D / 32], float scale_log2,
-                                          int offset, int group, int row0, const bf16x8* keys, const uint4* values,
-                                          int lane) {
-    constexpr int NK = D / 32, NT = D / 16;
-    const bool both = offset + (row0 + 16 * RT - 1) / group >= 32;
-    uint4 value[NT][2];
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) value[t][k] = values[(t * 2 + k) * 64 + lane];
-    v4f s[RT][4];
+// The unit's own block, bf16 with the causal mask, into an empty state (whatever the registers hold).  key(tile, step),
+// value(tile, half, share): the block's operands; odd(): whether there are infinities or NaN among the values.  Keys
+// behind the last row's own come in halves of the block: the second is left out where no row reaches it (it would add
+// zeros).
+template <int D, int R, class Key, class Value, class Odd>
+__device__ __forceinline__ void own_block(State<D, R>& st, const bf16x8 (&q)[D / 32 * (R / 16)], float scale_log2, int offset,
+                                          int group, int row0, int lane, const Key& key, const Value& value,
+                                          const Odd& odd) {
+    typedef State<D, R> S;
+    typedef typename S::Acc Acc;
+    const bool both = offset + (row0 + R - 1) / group >= 32;
+    const int place = offset + (row0 + lane % R) / group;        // of the query in the block
+    typename S::Scores s;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        if (h && !both) break;
+        if (h && !both) {
 #pragma unroll
-        for (int t = 2 * h; t < 2 * h + 2; ++t)
+            for (int t = S::kTiles / 2; t < S::kTiles; ++t) s[t] = Acc{} - INFINITY;
+            break;
+        }
 #pragma unroll
-            for (int k = 0; k < NK; ++k) {
-                const bf16x8 x = keys[(t * NK + k) * 64 + lane];
+        for (int t = h * (S::kTiles / 2); t < (h + 1) * (S::kTiles / 2); ++t)
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
-                    s[rt][t] = mfma16(x, q[rt][k], k ? s[rt][t] : z);
-                }
-            }
+            for (int k = 0; k < S::kSteps; ++k) s[t] = mfma(key(t, k), q[k], k ? s[t] : Acc{});
+#pragma unroll
+        for (int g = 0; g < S::kShares; ++g)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (S::key(h, g, j, lane) > place) S::set_score(s, h, g, j, -INFINITY);
     }
+    st.m = S::top_score(s) * scale_log2;
+    st.empty();
     // The values are bf16 here, and so are the probabilities, each as a sum of two (16 significant bits).
-    bf16x8 p[RT][2], rest[RT][2];
-    int place[RT];                      // of the query in the block
+    bf16x8 p[2][S::kShares], rest[2][S::kShares];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        place[rt] = offset + (row0 + rt * 16 + lane % 16) / group;
-        auto mask = [&](int h) {
+    for (int h = 0; h < 2; ++h) {
+        if (h && !both) {
 #pragma unroll
-            for (int i = 8 * h; i < 8 * h + 8; ++i)
-                if (i / 4 * 16 + lane / 16 * 4 + i % 4 > place[rt]) s[rt][i / 4][i % 4] = -INFINITY;
-        };
-        auto take = [&](int h) {
+            for (int g = 0; g < S::kShares; ++g) p[h][g] = rest[h][g] = bf16x8{};
+            break;
+        }
 #pragma unroll
-            for (int i = 8 * h; i < 8 * h + 8; ++i) {
-                const float e = __builtin_amdgcn_exp2f(fmaf(s[rt][i / 4][i % 4], scale_log2, -st.m[rt]));
-                st.l[rt] += e;
-                p[rt][h][i % 8] = (__bf16)e;
-                rest[rt][h][i % 8] = (__bf16)(e - (float)(__bf16)e);
+        for (int g = 0; g < S::kShares; ++g)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float e = __builtin_amdgcn_exp2f(fmaf(S::score(s, h, g, j), scale_log2, -st.m));
+                st.l[g] += e;
+                p[h][g][j] = (__bf16)e;
+                rest[h][g][j] = (__bf16)(e - (float)(__bf16)e);
             }
-        };
-        mask(0);
-        if (both) {
-            mask(1);
-        } else {
-#pragma unroll
-            for (int i = 8; i < 16; ++i) s[rt][i / 4][i % 4] = -INFINITY;
-        }
-        st.m[rt] = top_score(s[rt]) * scale_log2;
-        st.l[rt] = 0.0f;
-        take(0);
-        if (both) {
-            take(1);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) p[rt][1][i] = rest[rt][1][i] = (__bf16)0.0f;
-        }
     }
-    uint32_t odd = 0;
+    auto add = [&](int t, int h, const bf16x8 (&x)[S::kShares]) {
 #pragma unroll
-    for (int t = 0; t < NT; ++t) odd |= all_ones(value[t][0]) | all_ones(value[t][1]);
-    if (__builtin_expect(!__any(odd != 0), 1)) {
+        for (int g = 0; g < S::kShares; ++g) st.o[t] = mfma(x[g], rest[h][g], h || g ? st.o[t] : Acc{});
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            if (k && !both) break;
+        for (int g = 0; g < S::kShares; ++g) st.o[t] = mfma(x[g], p[h][g], st.o[t]);
+    };
+    if (__builtin_expect(!odd(), 1)) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const bf16x8 x = __builtin_bit_cast(bf16x8, value[t][k]);
+        for (int h = 0; h < 2; ++h) {
+            if (h && !both) break;
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
-                    st.o[rt][t] = mfma16(x, p[rt][k], mfma16(x, rest[rt][k], k ? st.o[rt][t] : z));
-                }
+            for (int t = 0; t < S::kOut; ++t) {
+                bf16x8 x[S::kShares];
+#pragma unroll
+                for (int g = 0; g < S::kShares; ++g) x[g] = __builtin_bit_cast(bf16x8, value(t, h, g));
+                add(t, h, x);
             }
         }
         return;
@@ -512,141 +451,39 @@ __device__ __forceinline__ void own_block(Softmax<D, RT>& st, const bf16x8 (&q)[
     // 0 * infinity and 0 * NaN would carry a masked key's values into the rows before it: such values count as 0 in
     // the product, and the channels of the rows that see one become NaN.
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        v4f bad[RT];                  // above 0: the row sees such a value in this channel
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) bad[rt] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            bf16x8 mark;
-            const bf16x8 x = part_odd(value[t][k], mark);
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) {
-                bf16x8 seen;
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    seen[j] = (__bf16)(k * 32 + j / 4 * 16 + lane / 16 * 4 + j % 4 <= place[rt] ? 1.0f : 0.0f);
-                bad[rt] = mfma16(mark, seen, bad[rt]);
-                const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
-                st.o[rt][t] = mfma16(x, p[rt][k], mfma16(x, rest[rt][k], k ? st.o[rt][t] : z));
-            }
-        }
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) st.o[rt][t][i] = bad[rt][i] > 0.0f ? NAN : st.o[rt][t][i];
-    }
-}
-
-// The same for 32 rows whose operands are in LDS; odd: there are infinities or NaN among the values.
-template <int D>
-__device__ __forceinline__ void own_block(Wide<D>& st, const bf16x8 (&q)[D / 16], float scale_log2, int offset, int group,
-                                          int row0, const bf16x8 (*keys)[64], const f16x8 (*values)[64], bool odd, int lane) {
-    constexpr int NK = D / 16, NT = D / 32;
-    const bool both = offset + (row0 + 31) / group >= 32;
-    const int place = offset + (row0 + lane % 32) / group;
-    v16f s[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        if (h && !both) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) s[h][i] = -INFINITY;
-            break;
-        }
-#pragma unroll
-        for (int k = 0; k < NK; ++k) s[h] = mfma32(keys[h * NK + k][lane], q[k], k ? s[h] : v16f{});
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (h * 32 + i / 4 * 8 + lane / 32 * 4 + i % 4 > place) s[h][i] = -INFINITY;
-    }
-    st.m = top_score(s) * scale_log2;
-    st.l[0] = st.l[1] = 0.0f;
-    bf16x8 p[2][2], rest[2][2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        if (h && !both) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) p[h][i / 8][i % 8] = rest[h][i / 8][i % 8] = (__bf16)0.0f;
-            break;
-        }
-#pragma unroll
-        for (int g = 0; g < 2; ++g)
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float e = __builtin_amdgcn_exp2f(fmaf(s[h][j / 4 * 8 + g * 4 + j % 4], scale_log2, -st.m));
-                st.l[g] += e;
-                p[h][g][j] = (__bf16)e;
-                rest[h][g][j] = (__bf16)(e - (float)(__bf16)e);
-            }
-    }
-    if (__builtin_expect(!odd, 1)) {
+    for (int t = 0; t < S::kOut; ++t) {
+        Acc bad = {};                 // above 0: the row sees such a value in this channel
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            if (h && !both) break;
+            bf16x8 x[S::kShares];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                bf16x8 x[2];
-#pragma unroll
-                for (int g = 0; g < 2; ++g) x[g] = __builtin_bit_cast(bf16x8, values[t * 4 + h * 2 + g][lane]);
-#pragma unroll
-                for (int g = 0; g < 2; ++g) st.o[t] = mfma32(x[g], rest[h][g], h || g ? st.o[t] : v16f{});
-#pragma unroll
-                for (int g = 0; g < 2; ++g) st.o[t] = mfma32(x[g], p[h][g], st.o[t]);
-            }
-        }
-        return;
-    }
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        v16f bad = {};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            bf16x8 x[2];
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
+            for (int g = 0; g < S::kShares; ++g) {
                 bf16x8 mark, seen;
-                x[g] = part_odd(__builtin_bit_cast(uint4, values[t * 4 + h * 2 + g][lane]), mark);
+                x[g] = part_odd(value(t, h, g), mark);
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    seen[j] = (__bf16)(h * 32 + j / 4 * 16 + g * 8 + lane / 32 * 4 + j % 4 <= place ? 1.0f : 0.0f);
-                bad = mfma32(mark, seen, bad);
+                for (int j = 0; j < 8; ++j) seen[j] = (__bf16)(S::key(h, g, j, lane) <= place ? 1.0f : 0.0f);
+                bad = mfma(mark, seen, bad);
             }
-#pragma unroll
-            for (int g = 0; g < 2; ++g) st.o[t] = mfma32(x[g], rest[h][g], h || g ? st.o[t] : v16f{});
-#pragma unroll
-            for (int g = 0; g < 2; ++g) st.o[t] = mfma32(x[g], p[h][g], st.o[t]);
+            add(t, h, x);
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) st.o[t][i] = bad[i] > 0.0f ? NAN : st.o[t][i];
+        for (int i = 0; i < R * R / 64; ++i) st.o[t][i] = bad[i] > 0.0f ? NAN : st.o[t][i];
     }
 }
 
 // A state as one of the partial results of its rows (l summed over the column, o in units of ref).
-template <int D, int RT>
-__device__ __forceinline__ void store_part(const Softmax<D, RT>& st, float ref, const AttnArgs& a, int unit, int head,
-                                           int part, int row0, int rows, int lane) {
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-        const int row = row0 + rt * 16 + lane % 16;
-        if (row >= rows) continue;
-        const int64_t at = (((int64_t)unit * a.kv_heads + head) * a.parts + part) * a.max_rows + row;
-#pragma unroll
-        for (int t = 0; t < D / 16; ++t)
-            *reinterpret_cast<v4f*>(a.part_o + at * D + t * 16 + lane / 16 * 4) = st.o[rt][t] * ref;
-        if (lane < 16) a.part_ml[at] = make_float2(st.m[rt], st.l[rt]);
-    }
-}
-
-template <int D>
-__device__ __forceinline__ void store_part(float m, float l, const v16f (&o)[D / 32], const AttnArgs& a, int unit, int head,
-                                           int part, int row, int rows, int lane) {
+template <int D, int R>
+__device__ __forceinline__ void store_part(float m, float l, const typename State<D, R>::Acc (&o)[D / R], float ref,
+                                           const AttnArgs& a, int unit, int head, int part, int row, int rows, int lane) {
     if (row >= rows) return;
     const int64_t at = (((int64_t)unit * a.kv_heads + head) * a.parts + part) * a.max_rows + row;
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n)
-        *reinterpret_cast<v4f*>(a.part_o + at * D + n * 8 + lane / 32 * 4) =
-            v4f{o[n / 4][n % 4 * 4], o[n / 4][n % 4 * 4 + 1], o[n / 4][n % 4 * 4 + 2], o[n / 4][n % 4 * 4 + 3]};
-    if (lane < 32) a.part_ml[at] = make_float2(m, l);
+    for (int t = 0; t < D / R; ++t)
+#pragma unroll
+        for (int j = 0; j < R * R / 256; ++j)
+            *reinterpret_cast<v4f*>(a.part_o + at * D + t * R + j * 8 + lane / R * 4) =
+                v4f{o[t][4 * j], o[t][4 * j + 1], o[t][4 * j + 2], o[t][4 * j + 3]} * ref;
+    if (lane < R) a.part_ml[at] = make_float2(m, l);
 }
 
 // The operands of a recent block: its keys, and behind them (64 D elements on) its values.
@@ -655,12 +492,12 @@ __device__ __forceinline__ const uint4* recent_block(const AttnArgs& a, int rece
     return reinterpret_cast<const uint4*>(a.recent + ((int64_t)recent * a.kv_heads + head) * 2 * (kKvBlock * D));
 }
 
-// Attention of the query rows of one unit's kv head.  Rows are (new token, query head of the group), 16 RT of them to
-// a wave.  Scores are formed transposed, S^T = K Q^T, so that a lane holds 16 scores of one query per block: maximum
-// and sum need two exchanges between lanes, the factors of a row are plain lane values, and the probabilities
+// Attention of the query rows of one unit's kv head.  Rows are (new token, query head of the group), R = 16 or 32 of them
+// to a wave.  Scores are formed transposed, S^T = K Q^T, so that a lane holds R scores of one query per block: maximum
+// and sum need two exchanges between lanes, or one, the factors of a row are plain lane values, and the probabilities
 // are the second product's operand as they are (O^T = V^T P^T; the cache keeps the values in that key order).  Codes
 // are widened to the queries' bf16 and the probabilities' fp16 (both exact) and multiplied by
-// v_mfma_f32_16x16x32 (or the same in two halves, below); the scales enter in fp32, the keys' in the exponent's argument, the values' on the
+// v_mfma_f32_16x16x32 or 32x32x16; the scales enter in fp32, the keys' in the exponent's argument, the values' on the
 // probabilities.  Rounded below fp32 are only the probabilities (at most 2^-12 of each, an eighth of what bf16
 // would cost, whose error alone equals that of the results' own rounding), and the results.
 //
@@ -673,31 +510,47 @@ __device__ __forceinline__ const uint4* recent_block(const AttnArgs& a, int rece
 // attention_span_kernel gives every span of a row group a wave of its own and leaves the joining to
 // attention_join_kernel: for few rows, where the time is that of reading the cache and every wave must read.  Codes go
 // from memory to registers in whole lines (1 KB per load of a wave) and the next block's are loaded while this one's
-// are used; there is no LDS.  With RT = 1 all rows are one wave's and nobody else reads its codes: the loads are marked
+// are used; there is no LDS.  With R = 16 all rows are one wave's and nobody else reads its codes: the loads are marked
 // as not to be kept, which leaves the caches to the partial results (256 requests up to 8192 tokens: 477 -> 422 us).
-template <int D, int RT>
-__global__ __launch_bounds__(kWaves * 64, RT == 1 ? 3 : 2) void attention_span_kernel(AttnArgs a) {
-    constexpr int NT = D / 16;      // output tiles, and loads of a block's keys or values
-    constexpr int NK = D / 32;      // contraction steps of the score product
+template <int D, int R>
+__global__ __launch_bounds__(kWaves * 64, R == 16 ? 3 : 2) void attention_span_kernel(AttnArgs a) {
+    typedef State<D, R> S;
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int head = blockIdx.x % a.kv_heads;
     const int jobs = a.parts * a.row_groups, chunks = (jobs + kWaves - 1) / kWaves;
     const int unit = blockIdx.x / a.kv_heads / chunks, job = blockIdx.x / a.kv_heads % chunks * kWaves + wave;
     if (job >= jobs) return;
-    const int span = job / a.row_groups, row0 = job % a.row_groups * (16 * RT);
+    const int span = job / a.row_groups, row0 = job % a.row_groups * R;
     const KvUnit u = a.units[unit];
     if (!unit_fits(u, a.requests, a.tokens, a.recent_blocks, a.num_blocks)) return;
     const int rows = u.rows * a.group, own = (u.block + kSpan - 1) / kSpan;
     if (row0 >= rows || rows > a.max_rows || u.block > a.max_blocks || span > own) return;
 
-    bf16x8 q[RT][NK];
-    load_queries<D, RT>(q, a, u, head, row0, rows, lane);
-    Softmax<D, RT> st;
+    typename S::Queries q;
+    load_queries<D, R>(q, a, u, head, row0, rows, lane);
+    S st;
     float ref = 1.0f;
     if (span == own) {
         const uint4* mem = recent_block<D>(a, u.recent, head);
-        own_block<D, RT>(st, q, a.scale_log2, u.offset, a.group, row0, reinterpret_cast<const bf16x8*>(mem),
-                               mem + kKvBlock * D / 8, lane);
+        uint4 v[S::kOut][2][S::kShares];           // loaded before the scores are formed
+#pragma unroll
+        for (int t = 0; t < S::kOut; ++t)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int g = 0; g < S::kShares; ++g)
+                    v[t][h][g] = mem[kKvBlock * D / 8 + operand_at<R>(t, h * S::kShares + g, 2, lane)];
+        own_block<D, R>(
+            st, q, a.scale_log2, u.offset, a.group, row0, lane,
+            [&](int t, int k) { return __builtin_bit_cast(bf16x8, mem[operand_at<R>(t, k, D / 32, lane)]); },
+            [&](int t, int h, int g) { return v[t][h][g]; },
+            [&]() {
+                uint32_t odd = 0;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i)
+                    odd |= all_ones(v[i / 2 / S::kShares][i / S::kShares % 2][i % S::kShares]);
+                return __any(odd != 0);
+            });
     } else {
         const int first = span * kSpan, last = min(first + kSpan, u.block);
         const int64_t block_bytes = (int64_t)a.kv_heads * 2 * kKvBlock * D;
@@ -707,48 +560,47 @@ __global__ __launch_bounds__(kWaves * 64, RT == 1 ? 3 : 2) void attention_span_k
         if (!(run.use & 1)) st.clear();
         Raw<D> kr, vr;
         const uint8_t* here = codes + __builtin_amdgcn_readlane(run.at, 0) * block_bytes;
-        load_raw<RT == 1>(kr, here, lane);
-        load_raw<RT == 1>(vr, here + kKvBlock * D, lane);
+        load_raw<R, false>(kr, here, lane);
+        load_raw<R, true>(vr, here + kKvBlock * D, lane);
 #pragma unroll
         for (int i = 0; i < kSpan; ++i) {
             if (first + i >= last) break;
             const uint8_t* next = codes + __builtin_amdgcn_readlane(run.at, i + 1) * block_bytes;
-            v4f s[RT][4];
+            typename S::Scores s;
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
+            for (int t = 0; t < S::kTiles; ++t)
 #pragma unroll
-                for (int k = 0; k < NK; k += 2) {
-                    const uint4 w = kr.w[t * (NK / 2) + k / 2];
-                    const bf16x8 k0 = widen(w.x, w.y), k1 = widen(w.z, w.w);
-#pragma unroll
-                    for (int rt = 0; rt < RT; ++rt) {
-                        const v4f z = {0.0f, 0.0f, 0.0f, 0.0f};
-                        s[rt][t] = mfma16(k1, q[rt][k + 1], mfma16(k0, q[rt][k], k ? s[rt][t] : z));
-                    }
+                for (int k = 0; k < S::kSteps; ++k) {
+                    // a load holds two fragments' codes: halves of two times kShares steps
+                    const uint4 w = kr.w[(t * (D / 64) + k / (2 * S::kShares)) * S::kShares + k % S::kShares];
+                    const bool second = k / S::kShares % 2;
+                    const bf16x8 x = second ? widen(w.z, w.w) : widen(w.x, w.y);
+                    s[t] = mfma(x, q[k], k ? s[t] : typename S::Acc{});
                 }
             const bool more = i + 1 < kSpan && first + i + 1 < last;
-            if (more) load_raw<RT == 1>(kr, next, lane);
+            if (more) load_raw<R, false>(kr, next, lane);
             if (run.use >> i & 1) {
-                f16x8 p[RT][2];
+                f16x8 p[2][S::kShares];
                 const float c = lane_value(run.c, i), log_r = lane_value(run.log_r, i), inv_r = lane_value(run.inv_r, i);
                 if (i == 0) take_top<true>(st, s, c);
                 else take_top<false>(st, s, c);
                 take_half(st, s, c, log_r, inv_r, 0, p);
                 take_half(st, s, c, log_r, inv_r, 1, p);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const f16x8 v0 = widen_f16(vr.w[t].x, vr.w[t].y), v1 = widen_f16(vr.w[t].z, vr.w[t].w);
-                    if (i == 0) add_values<true>(st, t, v0, p, 0);
-                    else add_values<false>(st, t, v0, p, 0);
-                    add_values<false>(st, t, v1, p, 1);
-                }
+                for (int t = 0; t < S::kOut; ++t)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int g = 0; g < S::kShares; ++g) {
+                            const uint4 w = vr.w[t * S::kShares + g];
+                            const f16x8 x = h ? widen_f16(w.z, w.w) : widen_f16(w.x, w.y);
+                            st.o[t] = mfma(x, p[h][g], i == 0 && h + g == 0 ? typename S::Acc{} : st.o[t]);
+                        }
             }
-            if (more) load_raw<RT == 1>(vr, next + kKvBlock * D, lane);
+            if (more) load_raw<R, true>(vr, next + kKvBlock * D, lane);
         }
     }
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) st.l[rt] = column_sum(st.l[rt]);
-    store_part(st, ref, a, unit, head, span, row0, rows, lane);
+    store_part<D, R>(st.m, st.sum(), st.o, ref, a, unit, head, span, row0 + lane % R, rows, lane);
 }
 
 // The pair of units that stands at place x if all are ordered by the blocks that precede them, most first (64 classes;
@@ -875,8 +727,8 @@ __global__ __launch_bounds__(kWaves * 64, D == 64 ? 3 : 2) void attention_tile_k
     const int row0 = tile * 32, rows = busy ? u.rows * a.group : 0, last = busy ? min(u.block, end) : 0;
 
     bf16x8 q[NK];
-    load_queries<D>(q, a, u, head, row0, rows, lane);
-    Wide<D> st;
+    load_queries<D, 32>(q, a, u, head, row0, rows, lane);
+    State<D, 32> st;
     float all_m = -INFINITY, all_l = 0.0f;      // the units joined so far
     v16f all_o[NT] = {};
     auto join = [&](float ref) { join_state(all_m, all_l, all_o, st.m, st.sum(), st.o, ref); };
@@ -937,7 +789,7 @@ __global__ __launch_bounds__(kWaves * 64, D == 64 ? 3 : 2) void attention_tile_k
                     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                     for (int f = h * kGroup; f < (h + 1) * kGroup; ++f) {
-                        s[f % 2] = mfma32(kf[f % kAhead], q[f / 2], f / 2 ? s[f % 2] : v16f{});
+                        s[f % 2] = mfma(kf[f % kAhead], q[f / 2], f / 2 ? s[f % 2] : v16f{});
                         if (f + kAhead < NO) read_k(f + kAhead);
                     }
                     if (h < 2 * NL) store(buf ^ 1, h);          // block b + 1; nobody reads that buffer before the barrier
@@ -961,7 +813,7 @@ __global__ __launch_bounds__(kWaves * 64, D == 64 ? 3 : 2) void attention_tile_k
                         if (h == 0) take_half(st, s, c, log_r, inv_r, 1, p);
 #pragma unroll
                         for (int f = h * kGroup; f < (h + 1) * kGroup; ++f) {
-                            st.o[f % NT] = mfma32(vf[f % kAhead], p[f / NT / 2][f / NT % 2],
+                            st.o[f % NT] = mfma(vf[f % kAhead], p[f / NT / 2][f / NT % 2],
                                                   i == 0 && f / NT == 0 ? v16f{} : st.o[f % NT]);
                             if (f + kAhead < NO) read_v(f + kAhead);
                         }
@@ -1001,12 +853,15 @@ __global__ __launch_bounds__(kWaves * 64, D == 64 ? 3 : 2) void attention_tile_k
     if (!busy) return;
     const int unit = first_unit + which, own_part = (u.block + kRunBlocks - 1) / kRunBlocks;
     const int row = row0 + lane % 32;
-    if (a.parts && run < own_part) store_part<D>(all_m, all_l, all_o, a, unit, head, run, row, rows, lane);
+    if (a.parts && run < own_part) store_part<D, 32>(all_m, all_l, all_o, 1.0f, a, unit, head, run, row, rows, lane);
     if (run < own_run) return;
     const int buf = two ? which : 0;
-    own_block<D>(st, q, a.scale_log2, u.offset, a.group, row0, kt[buf], vt[buf], odd, lane);
+    own_block<D, 32>(
+        st, q, a.scale_log2, u.offset, a.group, row0, lane, [&](int t, int k) { return kt[buf][t * NK + k][lane]; },
+        [&](int t, int h, int g) { return __builtin_bit_cast(uint4, vt[buf][t * 4 + h * 2 + g][lane]); },
+        [&]() { return odd; });
     if (a.parts) {
-        store_part<D>(st.m, st.sum(), st.o, a, unit, head, own_part, row, rows, lane);
+        store_part<D, 32>(st.m, st.sum(), st.o, 1.0f, a, unit, head, own_part, row, rows, lane);
         return;
     }
     join(1.0f);
@@ -1150,7 +1005,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
 // The form of a call, from what the host knows of it.
 struct AttnShape {
     int64_t max_rows, row_groups, runs, parts, max_blocks;
-    int rt;
+    int rows;                       // of a wave
     bool split;
 };
 
@@ -1170,8 +1025,8 @@ AttnShape attn_shape(int64_t num_units, int64_t max_new, int64_t max_seq, int64_
     // tokens at 4096, 320 waves: 54 against 106 us), at 1072 and 1472 waves the two are within 5 %, above the
     // partial results cost more than they bring (16 times 64 tokens at 4096, 3008 waves: 157 against 109 us).
     s.split = spans > 0 && (s.max_rows <= 16 || attn_waves(s, num_units, kv_heads) < 1024);
-    s.rt = s.split && s.max_rows <= 16 ? 1 : 2;
-    s.row_groups = (s.max_rows + 16 * s.rt - 1) / (16 * s.rt);
+    s.rows = s.split && s.max_rows <= 16 ? 16 : 32;
+    s.row_groups = (s.max_rows + s.rows - 1) / s.rows;
     s.parts = s.split ? spans + 1 : s.runs > 1 ? s.runs + 1 : 0;
     if (s.runs < 1) s.runs = 1;
     return s;
@@ -1190,8 +1045,8 @@ double attn_blocks(const AttnShape& s, int64_t num_units, int64_t kv_heads) {
 template <int D>
 hipError_t launch(const AttnArgs& a, const AttnShape& s, unsigned grid, hipStream_t st) {
     if (!s.split) attention_tile_kernel<D><<<grid, kWaves * 64, 0, st>>>(a);
-    else if (s.rt == 1) attention_span_kernel<D, 1><<<grid, kWaves * 64, 0, st>>>(a);
-    else attention_span_kernel<D, 2><<<grid, kWaves * 64, 0, st>>>(a);
+    else if (s.rows == 16) attention_span_kernel<D, 16><<<grid, kWaves * 64, 0, st>>>(a);
+    else attention_span_kernel<D, 32><<<grid, kWaves * 64, 0, st>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || s.parts == 0) return e;
     const int64_t rows = (int64_t)a.num_units * a.kv_heads * a.max_rows;
