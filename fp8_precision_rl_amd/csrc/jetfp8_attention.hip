@@ -708,7 +708,7 @@ __global__ __launch_bounds__(kWaves * 64, D == 64 ? 3 : 2) void attention_tile_k
         if (chunk * kWaves >= tiles[0] + tiles[1]) return;
         which = tile >= tiles[0];
         two = chunk * kWaves < tiles[0] && chunk * kWaves + kWaves > tiles[0];
-        end = chunk * kWaves + kWaves > tiles[0] ? max(us[0].block, us[1].block) : us[0].block;
+        end = two ? max(us[0].block, us[1].block) : us[chunk * kWaves >= tiles[0]].block;      // units come in any order
         if (which) tile -= tiles[0];
     } else {
         which = chunk >= own_chunks;
