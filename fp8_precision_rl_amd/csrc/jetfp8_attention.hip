@@ -1,4 +1,5 @@
 // Causal grouped-query attention over the FP8 key/value cache.
+#include <float.h>
 #include <math.h>
 
 #include "jetfp8_common.h"
@@ -24,12 +25,18 @@ constexpr int kWaves = 4;          // waves of a thread block; they share nothin
 constexpr int kSpan = 8;
 constexpr int kRun = 8;
 constexpr int kRunBlocks = kRun * kSpan;
-// The cache's probabilities enter the second product as fp16, in which the values' codes are exact.  A row's reference m
-// follows its running maximum only when that has grown by more than 2^8 (in 16 rows of fresh spans some maximum grows
-// with nearly every block, and following each would rescale the whole accumulator each time), so probabilities reach
-// 2^8 of the reference, and the values' share (below 2) comes on top: a lead of 2^6 keeps the largest at 2^15, below
-// the type's 65504, and all above 2^-20 of the largest at 11 significant bits.
-constexpr float kLead = 6.0f, kSlack = 8.0f;
+// The cache's probabilities enter the second product as fp16, in which the values' codes are exact, each times its block's
+// scale and relative to a reference of its own, near the row's largest such product in the span: what a block adds to the
+// row decides about its bits, not its probability or its values alone.  The reference follows the running maximum only
+// when that has grown by more than 2^8 (in 16 rows of fresh spans some maximum grows with nearly every block, and
+// following each would rescale the whole accumulator each time).  A lead of 2^6 (up to 2^7 where the reference is rounded
+// down to a whole number) keeps the largest at 2^15, below the type's 65504, and all above 2^-20 of the largest at 11
+// significant bits; below that the error is 2^-31 of the largest.
+// Where a whole block lies so low that fp16 has only zeros for it (below 2^-25), its exponentials are raised to 2^-kDeep,
+// still zeros in fp16, so that in fp32 the denominator gets its terms however small the values are.  The reference is held
+// no further than 2^-kLow (and the slack) below the denominator's, so that the power of two between them is in fp32's
+// range: what is lost of values near 2^-126 and below is less than their own rounding to bf16.
+constexpr float kLead = 6.0f, kSlack = 8.0f, kDeep = 30.0f, kLow = 130.0f;
 
 struct AttnArgs {
     const uint16_t* q;
@@ -118,10 +125,11 @@ struct AccOf<32> {
 };
 
 // Running softmax state of R query rows: 16, for products of 16x16x32, or 32, for products of 32x32x16.  Lane l, with
-// g = l / R, holds query l % R: the reference m of its exponentials (in log2); of a block's keys and of each R channels
-// those at 8 j + 4 g .. + 3 (R = 32, j < 4; R = 16: j = 0); its shares l of the denominator.  With R = 32 these are two,
-// those that lanes g and g + 2 hold with R = 16, and two products in ascending order of the contraction give what one
-// of 16x16x32 gives, bit for bit: a row's results are the same in both.
+// g = l / R, holds query l % R: top, the reference of its denominator (its largest score, in log2), and m, that of the
+// cache's exponentials times the values' scales; of a block's keys and of each R channels those at 8 j + 4 g .. + 3
+// (R = 32, j < 4; R = 16: j = 0); its shares l of the denominator.  With R = 32 these are two, those that lanes g and
+// g + 2 hold with R = 16, and two products in ascending order of the contraction give what one of 16x16x32 gives, bit for
+// bit: a row's results are the same in both.
 template <int D, int R>
 struct State {
     typedef typename AccOf<R>::type Acc;
@@ -131,14 +139,14 @@ struct State {
     static constexpr int kSteps = D / 32 * kShares;    // of the score product
     typedef Acc Scores[kTiles];
     typedef bf16x8 Queries[kSteps];
-    float m, l[kShares];
+    float m, top, l[kShares];
     Acc o[kOut];
     __device__ __forceinline__ void empty() {
 #pragma unroll
         for (int g = 0; g < kShares; ++g) l[g] = 0.0f;
     }
     __device__ __forceinline__ void clear() {
-        m = -INFINITY;
+        m = top = -INFINITY;
         empty();
 #pragma unroll
         for (int t = 0; t < kOut; ++t) o[t] = Acc{};
@@ -146,6 +154,9 @@ struct State {
     __device__ __forceinline__ float sum() const {
         return R == 32 ? pair_sum(l[0] + l[kShares - 1]) : column_sum(l[0]);
     }
+    // What takes o from units of 2^m to those of 2^top, a power of two (exp2f: it may be subnormal; 0 where there were no
+    // keys).
+    __device__ __forceinline__ float factor() const { return exp2f(m - (top == -INFINITY ? 0.0f : top)); }
     // Score j of share g of half h of a block's keys, and the key that it belongs to.
     static __device__ __forceinline__ float score(const Scores& s, int h, int g, int j) {
         return R == 32 ? s[h][j / 4 * 8 + g * 4 + j % 4] : s[h * (kTiles / 2) + j / 4][j % 4];
@@ -206,14 +217,14 @@ __device__ __forceinline__ void load_raw(Raw<D>& r, const uint8_t* block, int la
     }
 }
 
-// Joins a state (m, l, o; l summed over the column, o in units of ref) to that of the units before it.
+// Joins a state (m, l, o; l summed over the column, o in units of factor) to that of the units before it.
 template <int NT>
 __device__ __forceinline__ void join_state(float& M, float& L, v16f (&O)[NT], float m, float l, const v16f (&o)[NT],
-                                           float ref) {
+                                           float factor) {
     float x, y;
     join_factors(M, m, x, y);
     L = fmaf(L, x, l * y);
-    y *= ref;
+    y *= factor;
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -263,15 +274,11 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, int token, int head
     }
 }
 
-// The scalars of a run, block i in lane i.  The values' scales are taken relative to ref, the power of two at or below
-// the largest of the block's span, so that a block's share (below 2) can be a factor of its probabilities and the
-// span's products stay in one accumulator; ref returns when the span ends.  The share enters the exponential's argument
-// as its log2, and the denominator is divided by it again.  (A block whose values are 2^-20 of another's of its span, or
-// less, loses bits: an absolute error below 2^-31 of that other block's values.  Shares are held at 2^-60 or more, so
-// that the denominator keeps its terms.)  A block id out of range has no keys: its bit of use is 0.
+// The scalars of a run, block i in lane i.  The values' scale enters the exponential's argument as its log2 (-infinity for
+// a block of zeros).  A block id out of range has no keys: its bit of use is 0.
 struct Run {
-    int at;                      // physical block
-    float c, log_r, inv_r, ref;  // the keys' scale * softmax scale * log2(e); the share's log2 and inverse
+    int at;            // physical block
+    float c, log_v;    // the keys' scale * softmax scale * log2(e); log2 of the values' scale
     uint64_t use;
 };
 
@@ -283,18 +290,10 @@ __device__ __forceinline__ Run load_run(const AttnArgs& a, int request, int head
     s.at = min(max(id, 0), a.num_blocks - 1);
     const float2 scale = *reinterpret_cast<const float2*>(a.scales + ((int64_t)s.at * a.kv_heads + head) * 2);
     const bool here = first + lane < last && id == s.at;
-    static_assert(kSpan == 8 && kRunBlocks == 64, "the maximum over a span is that of eight lanes, a run's blocks are the lanes");
+    static_assert(kRunBlocks == 64, "a run's blocks are the lanes");
     s.use = __ballot(here);
     s.c = scale.x * a.scale_log2;
-    const float v = here ? scale.y : 0.0f;
-    float top = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0xB1, 0xF, 0xF, false)));
-    top = fmaxf(top, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(top), 0x4E, 0xF, 0xF, false)));
-    top = fmaxf(top, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(top), 0x141, 0xF, 0xF, false)));
-    const uint32_t e = min(max(__float_as_uint(top) >> 23, 1u), 253u);      // scales are below 2^120
-    s.ref = __uint_as_float(e << 23);
-    const float r = fmaxf(v * __uint_as_float((254u - e) << 23), 0x1p-60f);
-    s.log_r = __builtin_amdgcn_logf(r);
-    s.inv_r = __builtin_amdgcn_rcpf(r);
+    s.log_v = log2f(scale.y);
     return s;
 }
 
@@ -316,33 +315,44 @@ __device__ __forceinline__ void load_queries(bf16x8 (&q)[D / 32 * (R / 16)], con
     }
 }
 
-// Takes the largest scores of a cache block's 64 keys (s, in units of c) into the rows' references.  START: the first
-// block of a span, whose state is empty (whatever the registers hold) and takes its maximum as it is.
+// Takes the largest scores of a cache block's 64 keys (s, in units of c; log_v: of its values' scale) into the rows'
+// references.  START: the first block of a span, whose state is empty (whatever the registers hold) and takes its maxima as
+// they are.  References are whole numbers, so that what they rescale keeps its bits, in whatever order a form of the call
+// does it.  base: what is added to a score in its exponential; den: takes such exponentials to the denominator's units.
 template <bool START, int D, int R>
-__device__ __forceinline__ void take_top(State<D, R>& st, const typename State<D, R>::Scores& s, float c) {
-    const float m = fmaf(State<D, R>::top_score(s), c, -kLead);
+__device__ __forceinline__ void take_top(State<D, R>& st, const typename State<D, R>::Scores& s, float c, float log_v,
+                                         float& base, float& den) {
+    const float most = max_of(State<D, R>::top_score(s) * c, -FLT_MAX);      // scores of -infinity: a block without weight
+    const float top = __builtin_ceilf(most);
+    const float m = max_of(__builtin_floorf(most + log_v) - kLead, top - kLow);
     if (START) {
         st.m = m;
+        st.top = top;
         st.empty();
-        return;
+    } else {
+        const float up = max_of(st.top, top);
+        const float less = __builtin_amdgcn_exp2f(st.top - up);
+#pragma unroll
+        for (int g = 0; g < R / 16; ++g) st.l[g] *= less;
+        st.top = up;
+        const bool grown = m > st.m + kSlack;
+        if (__any(grown)) {
+            const float to = grown ? m : st.m;
+            const float f = __builtin_amdgcn_exp2f(st.m - to);       // 1 for the rows that keep theirs
+#pragma unroll
+            for (int t = 0; t < D / R; ++t) st.o[t] *= f;
+            st.m = to;
+        }
     }
-    const bool grown = m > st.m + kSlack;
-    if (!__any(grown)) return;
-    const float to = grown ? m : st.m;
-    const float f = __builtin_amdgcn_exp2f(st.m - to);       // 1 for the rows that keep theirs
-#pragma unroll
-    for (int g = 0; g < R / 16; ++g) st.l[g] *= f;
-#pragma unroll
-    for (int t = 0; t < D / R; ++t) st.o[t] *= f;
-    st.m = to;
+    base = max_of(log_v - st.m, -kDeep - most);
+    den = __builtin_amdgcn_exp2f(-base - st.top);
 }
 
-// The probabilities of half a block's keys (32 h .. 32 h + 31), times the values' share, as operands of the second
+// The probabilities of half a block's keys (32 h .. 32 h + 31), times the values' scale, as operands of the second
 // product; their sum goes into the denominator.
 template <int D, int R>
-__device__ __forceinline__ void take_half(State<D, R>& st, const typename State<D, R>::Scores& s, float c, float log_r,
-                                          float inv_r, int h, f16x8 (&p)[2][R / 16]) {
-    const float base = log_r - st.m;
+__device__ __forceinline__ void take_half(State<D, R>& st, const typename State<D, R>::Scores& s, float c, float base,
+                                          float den, int h, f16x8 (&p)[2][R / 16]) {
 #pragma unroll
     for (int g = 0; g < R / 16; ++g) {
         float sum = 0.0f;
@@ -352,7 +362,7 @@ __device__ __forceinline__ void take_half(State<D, R>& st, const typename State<
             sum += e;
             p[h][g][j] = (_Float16)e;
         }
-        st.l[g] = fmaf(sum, inv_r, st.l[g]);
+        st.l[g] = fmaf(sum, den, st.l[g]);
     }
 }
 
@@ -407,7 +417,7 @@ __device__ __forceinline__ void own_block(State<D, R>& st, const bf16x8 (&q)[D /
             for (int j = 0; j < 8; ++j)
                 if (S::key(h, g, j, lane) > place) S::set_score(s, h, g, j, -INFINITY);
     }
-    st.m = S::top_score(s) * scale_log2;
+    st.top = S::top_score(s) * scale_log2;
     st.empty();
     // The values are bf16 here, and so are the probabilities, each as a sum of two (16 significant bits).
     bf16x8 p[2][S::kShares], rest[2][S::kShares];
@@ -422,7 +432,7 @@ __device__ __forceinline__ void own_block(State<D, R>& st, const bf16x8 (&q)[D /
         for (int g = 0; g < S::kShares; ++g)
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float e = __builtin_amdgcn_exp2f(fmaf(S::score(s, h, g, j), scale_log2, -st.m));
+                const float e = __builtin_amdgcn_exp2f(fmaf(S::score(s, h, g, j), scale_log2, -st.top));
                 st.l[g] += e;
                 p[h][g][j] = (__bf16)e;
                 rest[h][g][j] = (__bf16)(e - (float)(__bf16)e);
@@ -471,9 +481,9 @@ __device__ __forceinline__ void own_block(State<D, R>& st, const bf16x8 (&q)[D /
     }
 }
 
-// A state as one of the partial results of its rows (l summed over the column, o in units of ref).
+// A state as one of the partial results of its rows (l summed over the column, o in units of factor).
 template <int D, int R>
-__device__ __forceinline__ void store_part(float m, float l, const typename State<D, R>::Acc (&o)[D / R], float ref,
+__device__ __forceinline__ void store_part(float m, float l, const typename State<D, R>::Acc (&o)[D / R], float factor,
                                            const AttnArgs& a, int unit, int head, int part, int row, int rows, int lane) {
     if (row >= rows) return;
     const int64_t at = (((int64_t)unit * a.kv_heads + head) * a.parts + part) * a.max_rows + row;
@@ -482,7 +492,7 @@ __device__ __forceinline__ void store_part(float m, float l, const typename Stat
 #pragma unroll
         for (int j = 0; j < R * R / 256; ++j)
             *reinterpret_cast<v4f*>(a.part_o + at * D + t * R + j * 8 + lane / R * 4) =
-                v4f{o[t][4 * j], o[t][4 * j + 1], o[t][4 * j + 2], o[t][4 * j + 3]} * ref;
+                v4f{o[t][4 * j], o[t][4 * j + 1], o[t][4 * j + 2], o[t][4 * j + 3]} * factor;
     if (lane < R) a.part_ml[at] = make_float2(m, l);
 }
 
@@ -497,9 +507,10 @@ __device__ __forceinline__ const uint4* recent_block(const AttnArgs& a, int rece
 // and sum need two exchanges between lanes, or one, the factors of a row are plain lane values, and the probabilities
 // are the second product's operand as they are (O^T = V^T P^T; the cache keeps the values in that key order).  Codes
 // are widened to the queries' bf16 and the probabilities' fp16 (both exact) and multiplied by
-// v_mfma_f32_16x16x32 or 32x32x16; the scales enter in fp32, the keys' in the exponent's argument, the values' on the
-// probabilities.  Rounded below fp32 are only the probabilities (at most 2^-12 of each, an eighth of what bf16
-// would cost, whose error alone equals that of the results' own rounding), and the results.
+// v_mfma_f32_16x16x32 or 32x32x16; the scales enter in fp32, in the exponentials' arguments.  Rounded below fp32 are
+// only the probabilities (over the cache by at most 2^-12 of each whose product with its block's scale is above 2^-20 of
+// the row's largest in the span, and by 2^-31 of that largest otherwise; an eighth of what bf16 would cost, whose error
+// alone equals that of the results' own rounding), and the results.
 //
 // Blocks before the unit's own are complete and precede every query of the unit: no mask.  A row's sums have one order.
 // Its blocks are taken in spans of 8, each from an empty state; the spans are joined in ascending order in runs of 8,
@@ -529,7 +540,7 @@ __global__ __launch_bounds__(kWaves * 64, R == 16 ? 3 : 2) void attention_span_k
     typename S::Queries q;
     load_queries<D, R>(q, a, u, head, row0, rows, lane);
     S st;
-    float ref = 1.0f;
+    float factor = 1.0f;
     if (span == own) {
         const uint4* mem = recent_block<D>(a, u.recent, head);
         uint4 v[S::kOut][2][S::kShares];           // loaded before the scores are formed
@@ -556,7 +567,6 @@ __global__ __launch_bounds__(kWaves * 64, R == 16 ? 3 : 2) void attention_span_k
         const int64_t block_bytes = (int64_t)a.kv_heads * 2 * kKvBlock * D;
         const uint8_t* codes = a.codes + (int64_t)head * 2 * kKvBlock * D;
         const Run run = load_run(a, u.request, head, first, last, last, lane);
-        ref = lane_value(run.ref, 0);
         if (!(run.use & 1)) st.clear();
         Raw<D> kr, vr;
         const uint8_t* here = codes + __builtin_amdgcn_readlane(run.at, 0) * block_bytes;
@@ -581,11 +591,12 @@ __global__ __launch_bounds__(kWaves * 64, R == 16 ? 3 : 2) void attention_span_k
             if (more) load_raw<R, false>(kr, next, lane);
             if (run.use >> i & 1) {
                 f16x8 p[2][S::kShares];
-                const float c = lane_value(run.c, i), log_r = lane_value(run.log_r, i), inv_r = lane_value(run.inv_r, i);
-                if (i == 0) take_top<true>(st, s, c);
-                else take_top<false>(st, s, c);
-                take_half(st, s, c, log_r, inv_r, 0, p);
-                take_half(st, s, c, log_r, inv_r, 1, p);
+                const float c = lane_value(run.c, i), log_v = lane_value(run.log_v, i);
+                float base, den;
+                if (i == 0) take_top<true>(st, s, c, log_v, base, den);
+                else take_top<false>(st, s, c, log_v, base, den);
+                take_half(st, s, c, base, den, 0, p);
+                take_half(st, s, c, base, den, 1, p);
 #pragma unroll
                 for (int t = 0; t < S::kOut; ++t)
 #pragma unroll
@@ -599,8 +610,9 @@ __global__ __launch_bounds__(kWaves * 64, R == 16 ? 3 : 2) void attention_span_k
             }
             if (more) load_raw<R, true>(vr, next + kKvBlock * D, lane);
         }
+        factor = st.factor();
     }
-    store_part<D, R>(st.m, st.sum(), st.o, ref, a, unit, head, span, row0 + lane % R, rows, lane);
+    store_part<D, R>(st.top, st.sum(), st.o, factor, a, unit, head, span, row0 + lane % R, rows, lane);
 }
 
 // The pair of units that stands at place x if all are ordered by the blocks that precede them, most first (64 classes;
@@ -731,7 +743,7 @@ __global__ __launch_bounds__(kWaves * 64, D == 64 ? 3 : 2) void attention_tile_k
     State<D, 32> st;
     float all_m = -INFINITY, all_l = 0.0f;      // the units joined so far
     v16f all_o[NT] = {};
-    auto join = [&](float ref) { join_state(all_m, all_l, all_o, st.m, st.sum(), st.o, ref); };
+    auto join = [&](float factor) { join_state(all_m, all_l, all_o, st.top, st.sum(), st.o, factor); };
 
     const int64_t block_bytes = (int64_t)a.kv_heads * 2 * kKvBlock * D;
     const uint8_t* codes = a.codes + (int64_t)head * 2 * kKvBlock * D + lane * 16 + wave * (NL * 1024);
@@ -799,10 +811,11 @@ __global__ __launch_bounds__(kWaves * 64, D == 64 ? 3 : 2) void attention_tile_k
                 load(__builtin_amdgcn_readlane(sc.at, min(b + 2, 63)));
                 if (sc.use >> b & 1) {
                     f16x8 p[2][2], vf[kAhead];
-                    const float c = lane_value(sc.c, b), log_r = lane_value(sc.log_r, b), inv_r = lane_value(sc.inv_r, b);
-                    if (i == 0) take_top<true>(st, s, c);
-                    else take_top<false>(st, s, c);
-                    take_half(st, s, c, log_r, inv_r, 0, p);
+                    const float c = lane_value(sc.c, b), log_v = lane_value(sc.log_v, b);
+                    float base, den;
+                    if (i == 0) take_top<true>(st, s, c, log_v, base, den);
+                    else take_top<false>(st, s, c, log_v, base, den);
+                    take_half(st, s, c, base, den, 0, p);
                     auto read_v = [&](int f) { vf[f % kAhead] = vt[buf][f % NT * 4 + f / NT][lane]; };
 #pragma unroll
                     for (int f = 0; f < kAhead; ++f) read_v(f);
@@ -810,7 +823,7 @@ __global__ __launch_bounds__(kWaves * 64, D == 64 ? 3 : 2) void attention_tile_k
                     for (int h = 0; h < 4; ++h) {
                         // the second half's exponentials between the first half's products
                         if (h != 1) __builtin_amdgcn_sched_barrier(0);
-                        if (h == 0) take_half(st, s, c, log_r, inv_r, 1, p);
+                        if (h == 0) take_half(st, s, c, base, den, 1, p);
 #pragma unroll
                         for (int f = h * kGroup; f < (h + 1) * kGroup; ++f) {
                             st.o[f % NT] = mfma(vf[f % kAhead], p[f / NT / 2][f / NT % 2],
@@ -830,7 +843,7 @@ __global__ __launch_bounds__(kWaves * 64, D == 64 ? 3 : 2) void attention_tile_k
                 }
                 __syncthreads();
             }
-            if (begin + first < last) join(lane_value(sc.ref, first));
+            if (begin + first < last) join(st.factor());
         }
     }
     // The own blocks, as they are, through the same buffers: the first unit's (or the only one's) and the second's.
@@ -861,7 +874,7 @@ __global__ __launch_bounds__(kWaves * 64, D == 64 ? 3 : 2) void attention_tile_k
         [&](int t, int h, int g) { return __builtin_bit_cast(uint4, vt[buf][t * 4 + h * 2 + g][lane]); },
         [&]() { return odd; });
     if (a.parts) {
-        store_part<D, 32>(st.m, st.sum(), st.o, 1.0f, a, unit, head, own_part, row, rows, lane);
+        store_part<D, 32>(st.top, st.sum(), st.o, 1.0f, a, unit, head, own_part, row, rows, lane);
         return;
     }
     join(1.0f);

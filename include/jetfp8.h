@@ -267,9 +267,12 @@ int jetfp8_kv_append(const void* k_bf16, int64_t ldk, const void* v_bf16, int64_
  *   dst_codes, dst_scales (both or neither; head_dim 128 only): the JETFP8_ROWS_1x128 quantization of that bf16
  *   matrix [tokens][q_heads * 128], bit for bit: the activation of the output projection, quantized by the operator
  *   that produces it (Jet-RL explainers, "Schema de Quantification").
- * fp32 scores, softmax and sums; the probabilities are rounded to 11 bits or more for the second product.  A row's sums have one
- * fixed order (spans of 8 blocks, joined in ascending order, then its own block), so a token's result is bitwise the
- * same decoded alone, in a batch, or within a prompt.
+ * fp32 scores, softmax and sums.  For the second product the probabilities are rounded: over the own block to 16 bits; over
+ * the cache, each together with its block's value scale s_n, to 11 bits where p_n s_n is above 2^-20 of the row's largest
+ * such product, and by at most 2^-31 of that largest below (so a block of small values keeps its bits beside one of large
+ * values that has no weight).  Where values are near 2^-126 and below, an error of 2^-134 or less (half a bf16 there) is
+ * added.  A row's sums have one fixed order (spans of 8 blocks, joined in ascending order, then its own block), so a
+ * token's result is bitwise the same decoded alone, in a batch, or within a prompt.
  * max_new: no request has more new tokens; max_seq: nor more tokens after the step.  A unit beyond either, or whose
  * fields do not fit the buffers, is left out (its rows stay as they were); a block id outside 0 .. num_blocks - 1
  * reads as a block without keys.  Infinities and NaN reach only the rows that may see them.  Values below 2^90 (sums over

@@ -129,10 +129,11 @@ def bf16(bits):
 def attention(q, units, table, codes, scales, recent, softmax_scale):
     """q float64 [T, Hq, D] -> o [T, Hq, D] (NaN where no unit has the row), and per output a bound on the error of a
     computation in fp32 whose probabilities are rounded to 11 bits (before the rounding of the result):
-        |v| weighted by the probabilities * (2^-11 + 2 e + N 2^-22) + N 2^-31 max |v|,
+        |v| weighted by the probabilities * (2^-11 + 2 e + N 2^-22) + N 2^-31 * largest p_n * 448 s_n,
     2^-11 for the rounding of each probability; e for the relative error of an exponential, from the score's D products
-    and sums, its scaling and the exponential itself; N 2^-22 for the sums over N keys; 2^-31 for probabilities that are
-    subnormal in fp16 (below 2^-20 of the largest, or the less the smaller their block's values are)."""
+    and sums, its scaling and the exponential itself; N 2^-22 for the sums over N keys.  The last term is for cached keys
+    whose probability times their block's scale s_n is below 2^-20 of the largest such product of the row: those are
+    subnormal in fp16.  It goes by what a block contributes to the row, so one without weight costs the others nothing."""
     T, Hq, D = q.shape
     H = codes.shape[1]
     G = Hq // H
@@ -145,6 +146,7 @@ def attention(q, units, table, codes, scales, recent, softmax_scale):
         for h in range(H):
             K = [E4M3[codes[p, h, 0][k8]] * np.float64(scales[p, h, 0]) for p in ids]
             V = [E4M3[codes[p, h, 1][v8]] * np.float64(scales[p, h, 1]) for p in ids]
+            weight = np.repeat([448 * np.float64(scales[p, h, 1]) for p in ids], BLOCK)
             own_k, own_v = bf16(recent[place, h, 0][k16]), bf16(recent[place, h, 1][v16])
             for i in range(rows):
                 k = np.concatenate(K + [own_k[:offset + i + 1]])
@@ -156,6 +158,7 @@ def attention(q, units, table, codes, scales, recent, softmax_scale):
                 out[row + i, h * G:(h + 1) * G] = p @ v
                 size = (np.abs(qs) @ np.abs(k).T).max(axis=1, keepdims=True) * softmax_scale
                 e = (D + 8) * 2.0 ** -24 * size + 2.0 ** -21
+                most = (p[:, :len(weight)] * weight).max(axis=1, keepdims=True) if ids else 0.0
                 bound[row + i, h * G:(h + 1) * G] = (p @ np.abs(v)) * (2.0 ** -11 + 2 * e + len(k) * 2.0 ** -22) + \
-                    len(k) * 2.0 ** -31 * np.abs(v).max()
+                    len(k) * 2.0 ** -31 * most
     return out, bound

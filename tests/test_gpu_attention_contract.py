@@ -1,5 +1,5 @@
-"""What the header promises of the attention and its cache, in calls that a planner or a user may make: units in any order,
-values of any scale beside one another, steps in which requests are refused."""
+"""What the header promises of the attention and its cache, in calls that a user may make: units in any order, values of
+any scale beside one another, steps in which requests are refused."""
 import numpy as np
 import pytest
 
@@ -29,7 +29,8 @@ def test_units_of_a_request_in_descending_order(library, q_heads, kv_heads, head
     width = (past + new) // 64 + 1
     i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
     cache = jf.kv_cache(width, 1, past + new, kv_heads, head_dim)
-    state, head, free = torch.zeros((1, 2), dtype=torch.int32, device="cuda"), i32(0), torch.arange(width, dtype=torch.int32, device="cuda")
+    state, head = torch.zeros((1, 2), dtype=torch.int32, device="cuda"), i32(0)
+    free = torch.arange(width, dtype=torch.int32, device="cuda")
     table = torch.full((1, width), -1, dtype=torch.int32, device="cuda")
     g = torch.Generator(device="cuda")
     g.manual_seed(7)
@@ -41,10 +42,70 @@ def test_units_of_a_request_in_descending_order(library, q_heads, kv_heads, head
     units = p.units[p.units[:, 0] == 0].contiguous()
     waves = len(units) * kv_heads * (64 * (q_heads // kv_heads) // 32)
     assert waves >= 1024, "the kernel for prompts is meant"
-    run = lambda u: jf.attention(qkv[:, :q_heads], u.contiguous(), table, *cache, max_new=new, max_seq=past + new).view(torch.int16)
+    run = lambda u: jf.attention(qkv[:, :q_heads], u.contiguous(), table, *cache, max_new=new,
+                                 max_seq=past + new).view(torch.int16)
     want = run(units)
     back = units.flip(0)
     for order in (back, torch.cat([units[:1], back[:-1]])):
         wrong = (run(order) != want).flatten(1).any(1).nonzero().flatten()
         assert len(wrong) == 0, f"{len(wrong)} rows differ, the first {wrong[:4].tolist()}, of blocks " \
                                 f"{sorted(set(((past + wrong) // 64).tolist()))}"
+
+
+# ------------------------------------------------------------------------------------------------ values of any scale
+def spread(head_dim, q_heads, kv_heads, loud, quiet, new, seed, blocks=11):
+    """A request of `blocks` complete blocks of every finite code.  In block 3 (and block 9, of the next span) the keys'
+    scale is large, so the weight is there; its values' scale is 2^quiet, that of the others 2^loud."""
+    rng = np.random.default_rng(seed)
+    c = TwinCache(1, q_heads, kv_heads, head_dim, blocks + 4, blocks + 4, new, seed)
+    ids = c.free[:blocks]
+    codes = rng.integers(0, 254, c.codes[ids].shape).astype(np.uint8)
+    c.codes[ids] = np.where(codes >= 127, codes + 1, codes)              # without 0x7F and 0xFF
+    c.scales[ids, :, 0] = 2.0 ** -14
+    c.scales[ids, :, 1] = 2.0 ** loud
+    for b in (3, 9):
+        c.scales[ids[b], :, 0] = 2.0 ** -4
+        c.scales[ids[b], :, 1] = 2.0 ** quiet
+    c.table[0, :blocks] = ids
+    c.free = c.free[blocks:]
+    c.state[:] = [[64 * blocks, 0]]
+    for k in ("codes", "scales", "table", "state", "free"):
+        c.dev[k] = c.up(getattr(c, k))
+    return c
+
+
+@pytest.mark.parametrize("loud,quiet", [(0, 0), (0, -12), (0, -24), (0, -40), (60, -20), (-10, -126), (-120, -139),
+                                        (-126, 0)])
+@pytest.mark.parametrize("head_dim,q_heads,kv_heads,new", [(128, 4, 2, 1), (64, 4, 2, 1), (128, 4, 1, 20),
+                                                           (64, 6, 2, 70)])
+def test_weight_on_blocks_of_small_values(library, head_dim, q_heads, kv_heads, new, loud, quiet):
+    """What a row reads from a block does not suffer from another of its span whose values are larger but have little
+    weight, in any form of the call."""
+    import torch
+    jf = library
+    c = spread(head_dim, q_heads, kv_heads, loud, quiet, new, abs(40 + quiet))
+    ref, got = c.plan([new], new, new)
+    host, dev = c.qkv(new)
+    for x in host[:2]:
+        x &= 0xBFFF                        # magnitudes below 2: the own block's scores stay below the weighty ones'
+    host[2][:] = c.bits(2.0 ** min(quiet, 0) * np.ones(host[2].shape))
+    dev = tuple(c.up_bits(x) for x in host)
+    c.append(ref, got, host, dev)
+    out = c.attend(ref, got, host, dev, new, 64 * 11 + new)
+    # the same units often enough for the kernel for prompts: each writes the same
+    times = -(-1024 // (len(got.units) * kv_heads * max(1, min(new, 64) * (q_heads // kv_heads) // 32)))
+    o = jf.attention(dev[0], got.units.repeat(times, 1), c.dev["table"], c.dev["codes"], c.dev["scales"], c.dev["recent"],
+                     max_new=new, max_seq=64 * 11 + new)
+    assert np.array_equal(c.down_bits(o), out)
+
+
+@pytest.mark.parametrize("new", [1, 20])
+def test_blocks_of_zeros_have_weight(library, new):
+    """A block whose values are all zero (scale 0) counts in the denominator and adds nothing, whatever its codes; first,
+    last and alone in its span."""
+    for zero in ([0], [3], [7, 9], list(range(8)), list(range(11))):
+        c = spread(128, 4, 2, 0, -3, new, 9)
+        ids = c.table[0, zero]
+        c.scales[ids, :, 1] = 0.0
+        c.dev["scales"] = c.up(c.scales)
+        c.step([new])
