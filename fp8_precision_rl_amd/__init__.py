@@ -23,7 +23,7 @@ OK, ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_MODE, ERR_HIP, ERR_VALUE = 0, -1, -2, -3
 ROWS_1x128, COLS_128x1_T, BLOCKS_128x128, BLOCKS_128x128_FRAG = 0, 1, 2, 3
 EXPORTED = ("jetfp8_quantize", "jetfp8_quantize_dual", "jetfp8_requantize_cols_t", "jetfp8_rmsnorm_quantize",
             "jetfp8_swiglu_quantize", "jetfp8_gemm_fwd", "jetfp8_gemm_fwd_frag", "jetfp8_gemm_dgrad",
-            "jetfp8_gemm_wgrad", "jetfp8_kv_max_units", "jetfp8_kv_plan", "jetfp8_kv_append", "jetfp8_attention",
+            "jetfp8_gemm_wgrad", "jetfp8_kv_max_units", "jetfp8_kv_plan", "jetfp8_kv_plan_cache", "jetfp8_kv_append", "jetfp8_attention",
             "jetfp8_attention_workspace", "jetfp8_status_string", "jetfp8_version")
 KV_BLOCK, KV_UNIT_WORDS = 64, 8
 KV_OK, KV_BAD_LENGTH, KV_NO_ROWS, KV_NO_BLOCK = 0, 1, 2, 4
@@ -64,6 +64,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     L.jetfp8_kv_max_units.argtypes = [i64, i64]
     L.jetfp8_kv_plan.restype = c_int
     L.jetfp8_kv_plan.argtypes = [vp, vp, vp, i64, vp, vp, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp]
+    L.jetfp8_kv_plan_cache.restype = c_int
+    L.jetfp8_kv_plan_cache.argtypes = [vp, vp, vp, i64, vp, vp, i64, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp, vp]
     L.jetfp8_kv_append.restype = c_int
     L.jetfp8_kv_append.argtypes = [vp, i64, vp, i64, i64, vp, i64, i64, i64, vp, vp, i64, vp, i64, vp]
     L.jetfp8_attention.restype = c_int
@@ -345,12 +347,25 @@ def _plan_inputs(state, new_lens, free_blocks, F, free_head, block_table, R, W):
 
 def jetfp8_kv_plan(state, new_lens, free_blocks, num_free: int, free_head, block_table, max_blocks: int, requests: int,
                    tokens: int, max_new: int, next_state, next_free, status, units, slots=None, stream=None) -> None:
+    _plan("jetfp8_kv_plan", (), state, new_lens, free_blocks, num_free, free_head, block_table, max_blocks, requests,
+          tokens, max_new, next_state, next_free, status, units, slots, stream)
+
+
+def jetfp8_kv_plan_cache(state, new_lens, free_blocks, num_free: int, free_head, block_table, max_blocks: int,
+                         requests: int, tokens: int, max_new: int, num_blocks: int, recent_blocks: int, next_state,
+                         next_free, status, units, slots=None, stream=None) -> None:
+    _plan("jetfp8_kv_plan_cache", (int(num_blocks), int(recent_blocks)), state, new_lens, free_blocks, num_free, free_head,
+          block_table, max_blocks, requests, tokens, max_new, next_state, next_free, status, units, slots, stream)
+
+
+def _plan(name, sizes, state, new_lens, free_blocks, num_free, free_head, block_table, max_blocks, requests, tokens, max_new,
+          next_state, next_free, status, units, slots, stream) -> None:
     torch = _torch_mod()
     i32, R, T, F, W = torch.int32, int(requests), int(tokens), int(num_free), int(max_blocks)
     n = kv_max_units(T, R)
     inputs = _plan_inputs(state, new_lens, free_blocks, F, free_head, block_table, R, W)
     dev = state.get_device()
-    _call("jetfp8_kv_plan", dev, stream, *inputs, W, R, T, int(max_new), _use(next_state, (R, 2), i32, "next_state", dev),
+    _call(name, dev, stream, *inputs, W, R, T, int(max_new), *sizes, _use(next_state, (R, 2), i32, "next_state", dev),
           _use(next_free, (1,), i32, "next_free", dev), _use(status, (R,), i32, "status", dev),
           _use(units, (n, KV_UNIT_WORDS), i32, "units", dev),
           None if slots is None else _use(slots, (T,), torch.int64, "slots", dev))
@@ -599,10 +614,11 @@ def kv_cache(num_blocks: int, requests: int, tokens: int, kv_heads: int, head_di
 
 
 def kv_plan(state, new_lens, free_blocks, free_head, block_table, tokens: int, max_new: int, slot_map: bool = False,
-            stream=None) -> KVPlan:
+            stream=None, cache=None) -> KVPlan:
     """Plans a step of `tokens` rows: state int32 [R, 2], new_lens int32 [R] (none above max_new), free_blocks int32
     [F] with free_head int32 [1] of them handed out, block_table int32 [R, max_blocks] (entries of the blocks that
-    the step completes are written)."""
+    the step completes are written).  cache: a layer's (codes, scales, recent); with it a request whose status is KV_OK
+    is sure to fit (jetfp8_kv_plan_cache), without it ids of the free list beyond the cache are not noticed here."""
     R, W = block_table.shape
     n, F, T = kv_max_units(tokens, R), free_blocks.shape[0], int(tokens)
     inputs = _plan_inputs(state, new_lens, free_blocks, F, free_head, block_table, R, W)
@@ -610,8 +626,11 @@ def kv_plan(state, new_lens, free_blocks, free_head, block_table, tokens: int, m
         new, like = state.new_empty, _torch_mod().empty_like
         p = KVPlan(like(state), like(free_head), like(new_lens), new(n, KV_UNIT_WORDS),
                    new(T, dtype=_torch.int64) if slot_map else None)
-    _call("jetfp8_kv_plan", state.get_device(), stream, *inputs, W, R, T, int(max_new), p.next_state.data_ptr(), p.next_free.data_ptr(),
-          p.status.data_ptr(), p.units.data_ptr(), p.slots.data_ptr() if slot_map else None)
+    name, sizes = "jetfp8_kv_plan", ()
+    if cache is not None:
+        name, sizes = "jetfp8_kv_plan_cache", (cache[0].shape[0], cache[2].shape[0])
+    _call(name, state.get_device(), stream, *inputs, W, R, T, int(max_new), *sizes, p.next_state.data_ptr(),
+          p.next_free.data_ptr(), p.status.data_ptr(), p.units.data_ptr(), p.slots.data_ptr() if slot_map else None)
     return p
 
 

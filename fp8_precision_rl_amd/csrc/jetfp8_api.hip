@@ -55,7 +55,7 @@ bool attention_dims_ok(int64_t num_units, int64_t max_new, int64_t max_seq, int6
 
 extern "C" {
 
-int jetfp8_version(void) { return 400; }
+int jetfp8_version(void) { return 401; }
 
 const char* jetfp8_status_string(int status) {
     switch (status) {
@@ -198,12 +198,22 @@ int jetfp8_kv_plan(const int32_t* state, const int32_t* new_lens, const int32_t*
                    const int32_t* free_head, int32_t* block_table, int64_t max_blocks, int64_t requests, int64_t tokens,
                    int64_t max_new, int32_t* next_state, int32_t* next_free, int32_t* status, int32_t* units,
                    int64_t* slots, void* stream) {
+    // no size of a cache to go by: ids up to the type's largest, and as many recent blocks as the step may need
+    return jetfp8_kv_plan_cache(state, new_lens, free_blocks, num_free, free_head, block_table, max_blocks, requests, tokens,
+                                max_new, kMaxDim - 1, kMaxDim - 1, next_state, next_free, status, units, slots, stream);
+}
+
+int jetfp8_kv_plan_cache(const int32_t* state, const int32_t* new_lens, const int32_t* free_blocks, int64_t num_free,
+                         const int32_t* free_head, int32_t* block_table, int64_t max_blocks, int64_t requests,
+                         int64_t tokens, int64_t max_new, int64_t num_blocks, int64_t recent_blocks, int32_t* next_state,
+                         int32_t* next_free, int32_t* status, int32_t* units, int64_t* slots, void* stream) {
     if (!state || !new_lens || !free_head || !block_table || !next_state || !next_free || !status || !units ||
         (!free_blocks && num_free != 0))
         return JETFP8_ERR_NULL;
     if (requests < 1 || requests > jetfp8::kKvMaxRequests || tokens < 1 || tokens > jetfp8::kKvMaxTokens ||
         !dim_ok(max_new) || !dim_ok(max_blocks) || !dim_ok(JETFP8_KV_BLOCK * max_blocks) || num_free < 0 ||
-        num_free >= kMaxDim)
+        num_free >= kMaxDim || !dim_ok(num_blocks) || !dim_ok(recent_blocks) ||
+        recent_blocks < 2 * requests + tokens / JETFP8_KV_BLOCK)
         return JETFP8_ERR_SHAPE;
     if (!aligned16(state) || !aligned16(new_lens) || !aligned16(free_blocks) || !aligned16(free_head) ||
         !aligned16(block_table) || !aligned16(next_state) || !aligned16(next_free) || !aligned16(status) ||
@@ -211,7 +221,7 @@ int jetfp8_kv_plan(const int32_t* state, const int32_t* new_lens, const int32_t*
         return JETFP8_ERR_ALIGN;
     return hip_status(jetfp8::launch_kv_plan(state, new_lens, free_blocks, num_free, free_head, block_table, max_blocks,
                                              requests, tokens, max_new, next_state, next_free, status, units, slots,
-                                             static_cast<hipStream_t>(stream)));
+                                             num_blocks, static_cast<hipStream_t>(stream)));
 }
 
 int jetfp8_kv_append(const void* k_bf16, int64_t ldk, const void* v_bf16, int64_t ldv, int64_t tokens,

@@ -25,6 +25,7 @@ struct PlanArgs {
     int4* units;
     int64_t* slots;   // may be null
     int requests, tokens, max_new, width, num_free, num_units;
+    int num_blocks, max_ids;   // ids of the cache are below num_blocks; a step takes no more than max_ids
 };
 
 // Inclusive sums over the block of one 64-bit value per thread (two 32-bit sums side by side).
@@ -63,13 +64,25 @@ template <int PER>
 __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(PlanArgs a) {
     extern __shared__ uint32_t sums[];              // [3][requests]
     __shared__ uint64_t wave_sums[kPlanThreads / 64];
-    __shared__ int used;
+    __shared__ int used, avail;
     uint32_t* row_end = sums;
     uint32_t* unit_end = sums + a.requests;
     uint32_t* seal_mid = unit_end + a.requests;     // completed blocks before the request << 16 | middle blocks before it
     const int r0 = threadIdx.x * PER;
     const int head = min(max(*a.free_head, 0), a.num_free);
-    if (threadIdx.x == 0) used = 0;
+    if (threadIdx.x == 0) {
+        used = 0;
+        avail = a.num_free - head;
+    }
+    __syncthreads();
+    // The list ends at its first id that is no block of the cache: a unit with such an id would be left out later.
+    for (int i = threadIdx.x; i < min(a.num_free - head, a.max_ids); i += kPlanThreads) {
+        const int id = a.free_blocks[head + i];
+        if (id < 0 || id >= a.num_blocks) {
+            atomicMin(&avail, i);
+            break;
+        }
+    }
     int2 s[PER];
     int n[PER], st[PER];
 #pragma unroll
@@ -107,7 +120,7 @@ __global__ __launch_bounds__(kPlanThreads) void kv_plan_kernel(PlanArgs a) {
         } else if (n[i] > 0) {
             const uint32_t need = (s[i].x + n[i]) / kKvBlock - s[i].x / kKvBlock;
             seals += need;
-            if (need > 0 && seals > (uint32_t)(a.num_free - head)) {
+            if (need > 0 && seals > (uint32_t)avail) {
                 st[i] = JETFP8_KV_NO_BLOCK;
             } else {
                 const int units = (s[i].x + n[i] - 1) / kKvBlock - s[i].x / kKvBlock + 1;
@@ -317,7 +330,7 @@ int64_t kv_max_units(int64_t tokens, int64_t requests) {
 hipError_t launch_kv_plan(const int32_t* state, const int32_t* new_lens, const int32_t* free_blocks, int64_t num_free,
                           const int32_t* free_head, int32_t* table, int64_t width, int64_t requests, int64_t tokens,
                           int64_t max_new, int32_t* next_state, int32_t* next_free, int32_t* status, int32_t* units,
-                          int64_t* slots, hipStream_t st) {
+                          int64_t* slots, int64_t num_blocks, hipStream_t st) {
     PlanArgs a;
     a.state = reinterpret_cast<const int2*>(state);
     a.new_lens = new_lens;
@@ -335,6 +348,8 @@ hipError_t launch_kv_plan(const int32_t* state, const int32_t* new_lens, const i
     a.width = (int)width;
     a.num_free = (int)num_free;
     a.num_units = (int)kv_max_units(tokens, requests);
+    a.num_blocks = (int)num_blocks;
+    a.max_ids = (int)((tokens + (kKvBlock - 1) * requests) / kKvBlock);
     const int items = slots ? a.tokens : a.num_units;    // never fewer rows than units
     const unsigned grid = (unsigned)((items + kPlanItems - 1) / kPlanItems), lds = (unsigned)(3 * requests * sizeof(uint32_t));
     if (requests <= kPlanThreads) kv_plan_kernel<1><<<grid, kPlanThreads, lds, st>>>(a);

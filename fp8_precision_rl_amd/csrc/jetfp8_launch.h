@@ -57,7 +57,7 @@ int64_t kv_max_units(int64_t tokens, int64_t requests);
 hipError_t launch_kv_plan(const int32_t* state, const int32_t* new_lens, const int32_t* free_blocks, int64_t num_free,
                           const int32_t* free_head, int32_t* table, int64_t width, int64_t requests, int64_t tokens,
                           int64_t max_new, int32_t* next_state, int32_t* next_free, int32_t* status, int32_t* units,
-                          int64_t* slots, hipStream_t st);
+                          int64_t* slots, int64_t num_blocks, hipStream_t st);
 hipError_t launch_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, int64_t ldv, int64_t tokens,
                             const int32_t* units, int64_t num_units, int64_t heads, int64_t D, uint8_t* codes,
                             float* scales, int64_t num_blocks, uint16_t* recent, int64_t recent_blocks, hipStream_t st);

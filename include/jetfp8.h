@@ -219,7 +219,7 @@ typedef enum {                  /* per-request outcome of jetfp8_kv_plan */
     JETFP8_KV_BAD_LENGTH = 1,   /* a negative length, more new tokens than max_new, more tokens than the table's row
                                  * holds, or a recent block other than 0 or 1 */
     JETFP8_KV_NO_ROWS = 2,      /* its new tokens end behind the call's rows */
-    JETFP8_KV_NO_BLOCK = 4      /* the free list is used up */
+    JETFP8_KV_NO_BLOCK = 4      /* the free list is used up, or its next id is no block of the cache */
 } jetfp8_kv_status;
 
 /* Units that a plan of this many rows and requests may have: min(tokens, (tokens + 62 requests) / 64 + requests). */
@@ -232,7 +232,7 @@ int64_t jetfp8_kv_max_units(int64_t tokens, int64_t requests);
  *                              follow one another in the call's q, k, v ([tokens] rows; rows behind the last
  *                              request's are padding and stay untouched);
  *   free_blocks [num_free] int32 (may be NULL if num_free is 0), free_head [1] int32: ids of unused physical blocks, of
- *                              which the first *free_head have been handed out.
+ *                              which the first *free_head have been handed out.  A negative id ends the list;
  * Writes
  *   block_table [requests][max_blocks] int32: only the entries of blocks that the step completes, taken from the free
  *                              list in request order;
@@ -251,10 +251,22 @@ int jetfp8_kv_plan(const int32_t* state, const int32_t* new_lens, const int32_t*
                    int64_t tokens, int64_t max_new, int32_t* next_state, int32_t* next_free, int32_t* status,
                    int32_t* units, int64_t* slots, void* stream);
 
+/* The same for a cache of num_blocks blocks and recent_blocks recent blocks (every layer's, as given to append and
+ * attention).  The free list ends at its first id that is not in 0 .. num_blocks - 1, and recent_blocks
+ * < 2 requests + tokens / 64 is refused (JETFP8_ERR_SHAPE), so that the units of every request with status
+ * JETFP8_KV_OK fit the cache and none of its tokens is left out.  jetfp8_kv_plan cannot see ids that are too large:
+ * append and attention leave out units that have one. */
+int jetfp8_kv_plan_cache(const int32_t* state, const int32_t* new_lens, const int32_t* free_blocks, int64_t num_free,
+                         const int32_t* free_head, int32_t* block_table, int64_t max_blocks, int64_t requests,
+                         int64_t tokens, int64_t max_new, int64_t num_blocks, int64_t recent_blocks,
+                         int32_t* next_state, int32_t* next_free, int32_t* status, int32_t* units, int64_t* slots,
+                         void* stream);
+
 /* New keys and values into a layer's cache: into the recent blocks, and for each block that the step completes its
  * codes and scales.  k, v: bf16, row t at k + t * ldk elements, [kv_heads][head_dim] contiguous within a row (so they
  * may be columns of a fused projection); ldk, ldv >= kv_heads * head_dim and multiples of 8.  Repeating the call
- * writes the same values again.  Finite inputs (others give unspecified codes of their block and head). */
+ * writes the same values again.  A unit whose fields do not fit the buffers is left out (units of
+ * jetfp8_kv_plan_cache fit).  Finite inputs (others give unspecified codes of their block and head). */
 int jetfp8_kv_append(const void* k_bf16, int64_t ldk, const void* v_bf16, int64_t ldv, int64_t tokens,
                      const int32_t* units, int64_t num_units, int64_t kv_heads, int64_t head_dim, uint8_t* codes,
                      float* scales, int64_t num_blocks, void* recent_bf16, int64_t recent_blocks, void* stream);

@@ -54,7 +54,7 @@ def max_units(tokens, requests):
     return min(tokens, (tokens + 62 * requests) // BLOCK + requests)
 
 
-def plan(state, new_lens, free_blocks, free_head, table, tokens, max_new):
+def plan(state, new_lens, free_blocks, free_head, table, tokens, max_new, num_blocks=2 ** 31 - 1):
     """One request after the other.  Returns next_state, next_free, status, units, slots and the new table."""
     R, width = table.shape
     table, next_state = table.copy(), state.copy()
@@ -62,6 +62,7 @@ def plan(state, new_lens, free_blocks, free_head, table, tokens, max_new):
     slots = np.full(tokens, -1, dtype=np.int64)
     units, row, middle, stopped = [], 0, 0, False
     head = start = min(max(int(free_head), 0), len(free_blocks))
+    end = next((i for i in range(head, len(free_blocks)) if not 0 <= free_blocks[i] < num_blocks), len(free_blocks))
     for r in range(R):
         ctx, slot, n = int(state[r, 0]), int(state[r, 1]), int(new_lens[r])
         row += min(max(n, 0), tokens + 1)
@@ -74,7 +75,7 @@ def plan(state, new_lens, free_blocks, free_head, table, tokens, max_new):
         if n == 0:
             continue
         done = range(ctx // BLOCK, (ctx + n) // BLOCK)       # blocks that this step completes
-        if len(done) and (stopped or head + len(done) > len(free_blocks)):
+        if len(done) and (stopped or head + len(done) > end):
             status[r], stopped = NO_BLOCK, True
             continue
         taken = {j: int(free_blocks[head + i]) for i, j in enumerate(done)}

@@ -1,0 +1,47 @@
+"""Refusals of the key/value cache's calls that need no GPU (nothing is launched), and pins of the oracle for them."""
+import os
+
+import numpy as np
+import pytest
+
+from oracle import kvcache as kc
+
+P = 0x10000        # a 16-byte aligned fake address: validation rejects every call below before any use
+BAD = 0x10008
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import fp8_precision_rl_amd as jf
+    if not os.path.exists(jf.LIB_PATH):
+        from fp8_precision_rl_amd import build
+        build.build()
+    return jf.load_library()
+
+
+def _plan_cache(lib, state=P, new=P, free=P, num_free=8, head=P, table=P, width=8, R=4, T=16, max_new=4, blocks=8,
+                recent=8, ns=2 * P, nf=2 * P, st=P, units=P, slots=P):
+    return lib.jetfp8_kv_plan_cache(state, new, free, num_free, head, table, width, R, T, max_new, blocks, recent, ns, nf,
+                                    st, units, slots, None)
+
+
+def test_plan_for_a_cache_refusals(lib):
+    for k in ("state", "new", "free", "head", "table", "ns", "nf", "st", "units"):
+        assert _plan_cache(lib, **{k: None}) == -1, k
+        assert _plan_cache(lib, **{k: BAD}) == -3, k
+    assert _plan_cache(lib, slots=BAD) == -3
+    for kw in (dict(R=0), dict(R=4097), dict(T=0), dict(T=(1 << 19) + 1), dict(max_new=0), dict(max_new=1 << 31),
+               dict(width=0), dict(width=1 << 25), dict(num_free=-1), dict(num_free=1 << 31), dict(blocks=0),
+               dict(blocks=1 << 31), dict(recent=0), dict(recent=1 << 31), dict(recent=7), dict(T=64, recent=8),
+               dict(R=4096, T=1 << 19, recent=8192 + 8191)):
+        assert _plan_cache(lib, **kw) == -2, kw
+
+
+def test_oracle_free_list_ends_at_an_id_of_no_block():
+    state, table = np.zeros((3, 2), np.int32), np.full((3, 4), -1, np.int32)
+    plan = lambda free, **kw: kc.plan(state, [64, 64, 64], np.array(free, np.int32), 1, table, 192, 64, **kw)
+    assert plan([-1, 4, 2, 3])["status"].tolist() == [0, 0, 0]                  # what is handed out is not looked at
+    p = plan([0, 4, -1, 3])
+    assert p["status"].tolist() == [0, 4, 4] and p["next_free"][0] == 2 and p["table"][:, 0].tolist() == [4, -1, -1]
+    assert plan([0, 4, 5, 3])["status"].tolist() == [0, 0, 0]
+    assert plan([0, 4, 5, 3], num_blocks=5)["status"].tolist() == [0, 4, 4]

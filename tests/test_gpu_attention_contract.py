@@ -109,3 +109,41 @@ def test_blocks_of_zeros_have_weight(library, new):
         c.scales[ids, :, 1] = 0.0
         c.dev["scales"] = c.up(c.scales)
         c.step([new])
+
+
+# ------------------------------------------------------------------------------------------------ plans that hold
+@pytest.mark.parametrize("bad", [(0, -1), (3, -2 ** 31), (2, 9), (4, 2 ** 31 - 2), (300, 700), (511, 700)])
+def test_a_plan_hands_out_blocks_of_the_cache_only(library, bad):
+    """A free list with an id that is no block of the cache: it ends there, and every request with status 0 is stored."""
+    at, wrong = bad
+    blocks, tokens = (700, 64 * 520) if at > 5 else (9, 64 * 8)
+    c = TwinCache(3, 1, 1, 64, blocks, blocks, tokens, 3)
+    c.free[at] = wrong
+    c.dev["free"] = c.up(c.free)
+    lens = [64 * at - 64, 64, 64] if at > 1 else [64, 3, 64]
+    ref = c.orc.plan(c.state, np.array(lens, np.int32), c.free, 0, c.table, tokens, tokens, blocks)
+    got = library.kv_plan(c.dev["state"], c.up(np.array(lens, np.int32)), c.dev["free"], c.dev["head"], c.dev["table"],
+                          tokens, tokens, slot_map=True, cache=(c.dev["codes"], c.dev["scales"], c.dev["recent"]))
+    for k, want in ref.items():
+        assert np.array_equal(dict(table=c.dev["table"], **got._asdict())[k].cpu().numpy(), want), k
+    assert ref["status"].tolist() == ([0, 0, 4] if at > 1 else [4, 0, 4]) and ref["next_free"][0] == (at if at > 1 else 0)
+    assert ref["units"][:, 6].max() < blocks
+    # without a cache's size only negative ids are seen
+    plain = library.kv_plan(c.dev["state"], c.up(np.array(lens, np.int32)), c.dev["free"], c.dev["head"],
+                            c.dev["table"], tokens, tokens)
+    assert plain.status.tolist() == (ref["status"].tolist() if wrong < 0 else [0, 0, 0])
+
+
+def test_plan_for_a_cache_equals_the_plan(library):
+    import torch
+    rng = np.random.default_rng(1)
+    R, tokens = 700, 30000
+    c = TwinCache(R, 1, 1, 64, 900, 40, tokens, 3)
+    c.state = np.stack([rng.integers(0, 2000, R), rng.integers(0, 2, R)], 1).astype(np.int32)
+    c.dev["state"] = c.up(c.state)
+    lens = rng.integers(0, 80, R)
+    ref, got = c.plan(lens, tokens, 80)
+    again = library.kv_plan(c.dev["state"], c.up(lens.astype(np.int32)), c.dev["free"], c.dev["head"], c.dev["table"], tokens,
+                            80, slot_map=True, cache=(c.dev["codes"], c.dev["scales"], c.dev["recent"]))
+    for a, b in zip(got, again):
+        assert torch.equal(a, b)
