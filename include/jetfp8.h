@@ -219,7 +219,10 @@ typedef enum {                  /* per-request outcome of jetfp8_kv_plan */
     JETFP8_KV_BAD_LENGTH = 1,   /* a negative length, more new tokens than max_new, more tokens than the table's row
                                  * holds, or a recent block other than 0 or 1 */
     JETFP8_KV_NO_ROWS = 2,      /* its new tokens end behind the call's rows */
-    JETFP8_KV_NO_BLOCK = 4      /* the free list is used up, or its next id is no block of the cache */
+    JETFP8_KV_NO_BLOCK = 4      /* it completes more blocks than the free list has left, or one whose id is no block of
+                                 * the cache.  Blocks are handed out in request order: after a request that is refused
+                                 * for them no later one gets any in this step, so that a request that needs many is not
+                                 * passed by for ever.  Who would rather let them pass plans it without new tokens */
 } jetfp8_kv_status;
 
 /* Units that a plan of this many rows and requests may have: min(tokens, (tokens + 62 requests) / 64 + requests). */
@@ -239,7 +242,8 @@ int64_t jetfp8_kv_max_units(int64_t tokens, int64_t requests);
  *   next_state, next_free:     state and free_head after the step (other buffers than the inputs, so that a step can
  *                              be planned again);
  *   status [requests] int32:   jetfp8_kv_status.  A request that is refused has no units, its rows stay untouched in
- *                              later calls, and its state does not change; the others go ahead;
+ *                              later calls, and its state does not change; the others go ahead (but for
+ *                              those that complete a block, after one with JETFP8_KV_NO_BLOCK);
  *   units [jetfp8_kv_max_units(tokens, requests)][JETFP8_KV_UNIT_WORDS] int32, in request and block order: request,
  *                              block index, recent block, first row, rows, place of the first row in the block,
  *                              physical block (-1: not complete after this step), 0; unused records are all -1;

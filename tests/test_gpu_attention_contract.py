@@ -147,3 +147,32 @@ def test_plan_for_a_cache_equals_the_plan(library):
                             80, slot_map=True, cache=(c.dev["codes"], c.dev["scales"], c.dev["recent"]))
     for a, b in zip(got, again):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("new", [9, 70])
+def test_refused_requests_keep_what_they_have(library, new):
+    """Steps in which requests are refused for blocks and for rows, through append and attention: their rows, recent
+    blocks, table and state stay; the refused are taken in later, and the results are those of the oracle throughout."""
+    c = TwinCache(4, 4, 2, 64, 12, 6, 400, 5)
+    every = c.free
+    c.free = every[:1]
+    c.dev["free"] = c.up(c.free)
+    c.step([100, 60, 0, 30])
+    lens = [5, 4 + new, 40, new]                # request 1 completes a block or two; with 70 request 3 would, too
+    before = c.state.copy()
+    ref, _ = c.step(lens, pad=6)
+    assert ref["status"].tolist() == [0, 4, 0, 4 if new == 70 else 0]
+    assert (c.state[1] == before[1]).all() and ref["next_free"][0] == 1
+    # the same tokens again, with blocks, but three rows too few: the last request with tokens is refused
+    c.free = every
+    c.dev["free"] = c.up(c.free)
+    lens = [0, 4 + new, 1, 8]
+    tokens = sum(lens) - 3
+    ref, got = c.plan(lens, tokens, 74)
+    assert ref["status"].tolist() == [0, 0, 0, 2]
+    host, dev = c.qkv(tokens)
+    c.append(ref, got, host, dev)
+    c.attend(ref, got, host, dev, 74, int(ref["next_state"][:, 0].max()))
+    c.advance(ref, got)
+    ref, _ = c.step([1, 1, 30, 40])
+    assert not ref["status"].any()
