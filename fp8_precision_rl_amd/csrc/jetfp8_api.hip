@@ -37,7 +37,7 @@ int check_gemm_extent(int64_t I, int64_t J, int64_t Kc) {
 bool kv_dims_ok(int64_t tokens, int64_t num_units, int64_t kv_heads, int64_t head_dim, int64_t num_blocks,
                 int64_t recent_blocks) {
     return dim_ok(tokens) && dim_ok(num_units) && dim_ok(kv_heads) && (head_dim == 64 || head_dim == 128) &&
-           dim_ok(num_blocks) && dim_ok(recent_blocks) && dim_ok(2 * kv_heads * num_units);
+           dim_ok(num_blocks) && dim_ok(recent_blocks) && 2 * kv_heads * num_units < jetfp8::kKvMaxGrid;
 }
 
 bool row_pitch_ok(int64_t ld, int64_t heads, int64_t head_dim) {

@@ -1082,7 +1082,9 @@ int64_t attention_workspace(int64_t num_units, int64_t max_new, int64_t max_seq,
 
 bool attention_fits(int64_t num_units, int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads) {
     const AttnShape s = attn_shape(num_units, max_new, max_seq, q_heads, kv_heads);
-    return attn_blocks(s, num_units, kv_heads) <= INT32_MAX && (double)num_units * kv_heads * s.max_rows <= INT32_MAX;
+    const double join = s.parts ? (double)num_units * kv_heads * s.max_rows / 4 : 0.0;      // its thread blocks, nearly
+    return attn_blocks(s, num_units, kv_heads) < kKvMaxGrid && join < kKvMaxGrid - 1 &&
+           (double)num_units * kv_heads * s.max_rows <= INT32_MAX;
 }
 
 hipError_t launch_attention(const uint16_t* q, int64_t ldq, int64_t tokens, const int32_t* units, int64_t num_units,

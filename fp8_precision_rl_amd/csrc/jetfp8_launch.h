@@ -52,6 +52,7 @@ hipError_t launch_gemm_fwd_frag(const uint8_t* xq, const float* xs, const uint8_
                                 int64_t M, int64_t N, int64_t K, hipStream_t st);
 // The FP8 key/value cache: a step's plan, the append of its keys and values, and the attention over the cache.
 constexpr int64_t kKvMaxRequests = 4096;            // three prefix sums of a request are kept in LDS
+constexpr int64_t kKvMaxGrid = (int64_t)1 << 24;    // a launch holds fewer than 2^32 threads, 256 to a thread block
 constexpr int64_t kKvMaxTokens = (int64_t)1 << 19;  // sums over 4096 requests stay below 2^32
 int64_t kv_max_units(int64_t tokens, int64_t requests);
 hipError_t launch_kv_plan(const int32_t* state, const int32_t* new_lens, const int32_t* free_blocks, int64_t num_free,

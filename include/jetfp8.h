@@ -45,7 +45,9 @@
  *       requantize_cols_t ... (cols / 128) * (rows / 128) > 2^31 - 1, 32 * cols + 128 >= 2^31, or
  *                             128 * rows + 128 >= 2^31;
  *       swiglu_quantize ..... ceil(cols / 512) * ceil(rows / 32) >= 2^31, or 128 * cols >= 2^31 (32 rows of
- *                             gate_up in bytes).
+ *                             gate_up in bytes);
+ *       kv_append, attention  2 * kv_heads * num_units >= 2^24, and attention also grids of its own kernels of
+ *                             2^24 thread blocks or more (a launch holds fewer than 2^32 threads).
  *   - Thread safety: calls are independent; concurrent calls on different streams are allowed.
  */
 #ifndef JETFP8_H

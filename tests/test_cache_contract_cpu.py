@@ -45,3 +45,15 @@ def test_oracle_free_list_ends_at_an_id_of_no_block():
     assert p["status"].tolist() == [0, 4, 4] and p["next_free"][0] == 2 and p["table"][:, 0].tolist() == [4, -1, -1]
     assert plan([0, 4, 5, 3])["status"].tolist() == [0, 0, 0]
     assert plan([0, 4, 5, 3], num_blocks=5)["status"].tolist() == [0, 4, 4]
+
+
+def test_grids_that_a_launch_does_not_hold(lib):
+    """A launch has fewer than 2^32 threads, so fewer than 2^24 thread blocks of 256: such calls are refused before
+    anything is enqueued, also where only the second kernel's grid is too large."""
+    append = lambda n, H: lib.jetfp8_kv_append(BAD, 128 * H, P, 128 * H, 16, P, n, H, 128, P, P, 8, P, 8, None)
+    assert append((1 << 20) - 1, 8) == -3 and append(1 << 20, 8) == -2
+    f = lib.jetfp8_attention_workspace
+    # units, max_new, max_seq, q_heads, kv_heads, head_dim
+    assert f(1 << 20, 64, 64, 8, 8, 128) == 0 and f(1 << 20, 64, 64, 16, 16, 128) == -2
+    # 128 rows a unit to join, four to a thread block; the first kernel has two thread blocks a unit
+    assert f(1 << 18, 64, 8192, 2, 1, 128) > 0 and f(1 << 19, 64, 8192, 2, 1, 128) == -2
