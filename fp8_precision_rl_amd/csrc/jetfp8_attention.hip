@@ -27,9 +27,9 @@ constexpr int kRun = 8;
 constexpr int kRunBlocks = kRun * kSpan;
 // The cache's probabilities enter the second product as fp16, in which the values' codes are exact, each times its block's
 // scale and relative to a reference of its own, near the row's largest such product in the span: what a block adds to the
-// row decides about its bits, not its probability or its values alone.  The reference follows the running maximum only
-// when that has grown by more than 2^8 (in 16 rows of fresh spans some maximum grows with nearly every block, and
-// following each would rescale the whole accumulator each time).  A lead of 2^6 (up to 2^7 where the reference is rounded
+// row decides about its bits, not its probability or its values alone.  This reference, and the denominator's, follow the
+// running maxima only when those have grown by more than 2^8 (in 16 rows of fresh spans some maximum grows with nearly
+// every block, and following each would rescale the whole accumulator each time).  A lead of 2^6 (up to 2^7 where the reference is rounded
 // down to a whole number) keeps the largest at 2^15, below the type's 65504, and all above 2^-20 of the largest at 11
 // significant bits; below that the error is 2^-31 of the largest.
 // Where a whole block lies so low that fp16 has only zeros for it (below 2^-25), its exponentials are raised to 2^-kDeep,
@@ -125,8 +125,8 @@ struct AccOf<32> {
 };
 
 // Running softmax state of R query rows: 16, for products of 16x16x32, or 32, for products of 32x32x16.  Lane l, with
-// g = l / R, holds query l % R: top, the reference of its denominator (its largest score, in log2), and m, that of the
-// cache's exponentials times the values' scales; of a block's keys and of each R channels those at 8 j + 4 g .. + 3
+// g = l / R, holds query l % R: top, the reference of its denominator (near its largest score, in log2), and m, that of
+// the cache's exponentials times the values' scales; of a block's keys and of each R channels those at 8 j + 4 g .. + 3
 // (R = 32, j < 4; R = 16: j = 0); its shares l of the denominator.  With R = 32 these are two, those that lanes g and
 // g + 2 hold with R = 16, and two products in ascending order of the contraction give what one of 16x16x32 gives, bit for
 // bit: a row's results are the same in both.
@@ -330,18 +330,16 @@ __device__ __forceinline__ void take_top(State<D, R>& st, const typename State<D
         st.top = top;
         st.empty();
     } else {
-        const float up = max_of(st.top, top);
-        const float less = __builtin_amdgcn_exp2f(st.top - up);
+        const bool grown = m > st.m + kSlack, ahead = top > st.top + kSlack;
+        if (__any(grown || ahead)) {
+            const float to = grown ? m : st.m, up = ahead ? top : st.top;
+            const float f = __builtin_amdgcn_exp2f(st.m - to), less = __builtin_amdgcn_exp2f(st.top - up);   // 1 if kept
 #pragma unroll
-        for (int g = 0; g < R / 16; ++g) st.l[g] *= less;
-        st.top = up;
-        const bool grown = m > st.m + kSlack;
-        if (__any(grown)) {
-            const float to = grown ? m : st.m;
-            const float f = __builtin_amdgcn_exp2f(st.m - to);       // 1 for the rows that keep theirs
+            for (int g = 0; g < R / 16; ++g) st.l[g] *= less;
 #pragma unroll
             for (int t = 0; t < D / R; ++t) st.o[t] *= f;
             st.m = to;
+            st.top = up;
         }
     }
     base = max_of(log_v - st.m, -kDeep - most);
