@@ -294,7 +294,8 @@ int jetfp8_kv_append(const void* k_bf16, int64_t ldk, const void* v_bf16, int64_
  * max_new: no request has more new tokens; max_seq: nor more tokens after the step.  A unit beyond either, or whose
  * fields do not fit the buffers, is left out (its rows stay as they were); a block id outside 0 .. num_blocks - 1
  * reads as a block without keys.  Infinities and NaN reach only the rows that may see them.  Values below 2^90 (sums over
- * the keys are taken before they are divided by the denominator).
+ * the keys are taken before they are divided by the denominator), queries below 2^104 (scores over the cache are those of
+ * its codes until their scale comes in; at -infinity a key has no weight, at infinity the row is NaN).
  * 0 < softmax_scale <= FLT_MAX / 2 (JETFP8_ERR_VALUE otherwise).
  * workspace: jetfp8_attention_workspace() bytes (its content is not kept between calls; calls that may run at the same
  * time need one each); JETFP8_ERR_SHAPE if workspace_bytes is less. */

@@ -111,6 +111,34 @@ def test_blocks_of_zeros_have_weight(library, new):
         c.step([new])
 
 
+@pytest.mark.parametrize("new", [1, 20, 70])
+@pytest.mark.parametrize("out", [[0], [3], [7, 8, 9], list(range(8)), list(range(11))])
+def test_scores_of_minus_infinity(library, out, new):
+    """Blocks whose scores overflow to -infinity have no weight, wherever in a span they are: the rows are those of a table
+    without them."""
+    import torch
+    jf = library
+    c = spread(128, 4, 2, 0, -3, new, 9)
+    k8 = c.orc.places(128)[0]
+    channel = c.codes[c.table[0, :11], :, 0]
+    channel[:, :, k8[:, 5]] = 0
+    channel[out] = np.where(np.isin(np.arange(64 * 128), k8[:, 5]), 0x7E, channel[out])          # 448 in channel 5
+    c.codes[c.table[0, :11], :, 0] = channel
+    c.dev["codes"] = c.up(c.codes)
+    ref, got = c.plan([new], new, new)
+    host, dev = c.qkv(new)
+    host[0][..., 5], host[1][..., 5] = 0xFB80, 0                                                  # queries -2^120
+    dev = tuple(c.up_bits(x) for x in host)
+    c.append(ref, got, host, dev)
+    without = c.table.copy()
+    without[0, out] = -1
+    tables = c.dev["table"], c.up(without)
+    for units in (got.units, got.units.repeat(1500, 1)):          # the forms for few rows and for prompts
+        a, b = (jf.attention(dev[0], units, t, c.dev["codes"], c.dev["scales"], c.dev["recent"], max_new=new,
+                             max_seq=64 * 11 + new).float() for t in tables)
+        assert bool(torch.isfinite(a).all()) and torch.equal(a, b)
+
+
 # ------------------------------------------------------------------------------------------------ plans that hold
 @pytest.mark.parametrize("bad", [(0, -1), (3, -2 ** 31), (2, 9), (4, 2 ** 31 - 2), (300, 700), (511, 700)])
 def test_a_plan_hands_out_blocks_of_the_cache_only(library, bad):
