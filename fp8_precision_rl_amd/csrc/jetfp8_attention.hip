@@ -1065,7 +1065,10 @@ hipError_t launch(const AttnArgs& a, const AttnShape& s, unsigned grid, hipStrea
     if (e != hipSuccess || s.parts == 0) return e;
     const int64_t rows = (int64_t)a.num_units * a.kv_heads * a.max_rows;
     if (!s.split) attention_join_kernel<D, false, 1><<<(unsigned)((rows + 3) / 4), 256, 0, st>>>(a);
-    else if (s.runs == 1 || rows >= 8192) attention_join_kernel<D, true, 1><<<(unsigned)((rows + 3) / 4), 256, 0, st>>>(a);
+    // Four waves form a row's runs at once where there are several and rows are too few to fill the chip (one wave a row
+    // against four, us: 4 runs 6.3 / 4.6 for 128 rows, 7.4 / 7.2 for 1024, 8.7 / 10.5 for 2048; 16 runs 17.5 / 8.8,
+    // 20.8 / 16.2 and 23.2 / 25.9; 2 runs 4.0 / 4.5, 4.7 / 5.5, 5.4 / 8.7).
+    else if (s.runs <= 2 || rows >= 2048) attention_join_kernel<D, true, 1><<<(unsigned)((rows + 3) / 4), 256, 0, st>>>(a);
     else attention_join_kernel<D, true, 4><<<(unsigned)rows, 256, 0, st>>>(a);
     return hipGetLastError();
 }
