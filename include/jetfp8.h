@@ -306,7 +306,10 @@ int jetfp8_attention(const void* q_bf16, int64_t ldq, int64_t tokens, const int3
                      float softmax_scale, void* dst_o_bf16, uint8_t* dst_codes, float* dst_scales, void* workspace,
                      int64_t workspace_bytes, void* stream);
 
-/* Bytes of workspace that jetfp8_attention needs for these sizes (0: none); JETFP8_ERR_SHAPE if it would refuse them. */
+/* Bytes of workspace that jetfp8_attention needs for these sizes (0: none); JETFP8_ERR_SHAPE if it would refuse them.
+ * A call lays its work and workspace out by max_new and max_seq for every unit alike (the rows of up to 64 new tokens,
+ * the partial results of a request of max_seq tokens).  So a step with a prompt's chunk beside many single tokens takes
+ * less of both as two calls, each with a part of the plan's units (any part, in any order) and its own max_new. */
 int64_t jetfp8_attention_workspace(int64_t num_units, int64_t max_new, int64_t max_seq, int64_t q_heads,
                                    int64_t kv_heads, int64_t head_dim);
 
