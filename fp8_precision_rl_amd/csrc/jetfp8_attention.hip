@@ -415,7 +415,7 @@ __device__ __forceinline__ void own_block(State<D, R>& st, const bf16x8 (&q)[D /
             for (int j = 0; j < 8; ++j)
                 if (S::key(h, g, j, lane) > place) S::set_score(s, h, g, j, -INFINITY);
     }
-    st.top = S::top_score(s) * scale_log2;
+    st.top = max_of(S::top_score(s) * scale_log2, -FLT_MAX);     // scores of -infinity: no weight
     st.empty();
     // The values are bf16 here, and so are the probabilities, each as a sum of two (16 significant bits).
     bf16x8 p[2][S::kShares], rest[2][S::kShares];

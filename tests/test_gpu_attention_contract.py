@@ -139,6 +139,31 @@ def test_scores_of_minus_infinity(library, out, new):
         assert bool(torch.isfinite(a).all()) and torch.equal(a, b)
 
 
+@pytest.mark.parametrize("new", [1, 20, 64])
+def test_own_scores_of_minus_infinity(library, new):
+    """The same where all scores of the own block overflow to -infinity: as with scores so low that their exponentials are 0.
+    (The request ends at a block's end, so that with 64 new tokens every row has cached blocks before it.)"""
+    import torch
+    jf = library
+    c = spread(128, 4, 2, 0, -3, new, 9)
+    k8 = c.orc.places(128)[0]
+    c.codes[c.table[0, :11][:, None], :, 0, k8[:, 5]] = 0
+    c.dev["codes"] = c.up(c.codes)
+    ref, got = c.plan([new], new, new)
+    host, dev = c.qkv(new)
+    host[0][..., 5] = 0xFB80                                                                      # queries -2^120
+    outs = []
+    for key in (0x4480, 0x0B00):                                    # keys 2^10: scores -2^130; 2^-105: -2^15
+        host[1][..., 5] = key
+        dev = tuple(c.up_bits(x) for x in host)
+        cache = [c.dev[k].clone() for k in ("codes", "scales", "recent")]
+        jf.kv_append(dev[1], dev[2], got.units, *cache)
+        outs.append([jf.attention(dev[0], u, c.dev["table"], *cache, max_new=new, max_seq=64 * 11 + new).float()
+                     for u in (got.units, got.units.repeat(1500, 1))])
+    for a, b in zip(*outs):
+        assert bool(torch.isfinite(a).all()) and torch.equal(a, b)
+
+
 # ------------------------------------------------------------------------------------------------ plans that hold
 @pytest.mark.parametrize("bad", [(0, -1), (3, -2 ** 31), (2, 9), (4, 2 ** 31 - 2), (300, 700), (511, 700)])
 def test_a_plan_hands_out_blocks_of_the_cache_only(library, bad):
