@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import math
 import os
 from typing import Any, NamedTuple, Optional, Tuple
 
@@ -24,7 +25,11 @@ ROWS_1x128, COLS_128x1_T, BLOCKS_128x128, BLOCKS_128x128_FRAG = 0, 1, 2, 3
 EXPORTED = ("jetfp8_quantize", "jetfp8_quantize_dual", "jetfp8_requantize_cols_t", "jetfp8_rmsnorm_quantize",
             "jetfp8_swiglu_quantize", "jetfp8_gemm_fwd", "jetfp8_gemm_fwd_frag", "jetfp8_gemm_dgrad",
             "jetfp8_gemm_wgrad", "jetfp8_kv_max_units", "jetfp8_kv_plan", "jetfp8_kv_plan_cache", "jetfp8_kv_append", "jetfp8_attention",
-            "jetfp8_attention_workspace", "jetfp8_status_string", "jetfp8_version")
+            "jetfp8_attention_workspace", "jetfp8_rmsnorm_add_quantize", "jetfp8_rmsnorm_backward",
+            "jetfp8_rmsnorm_backward_workspace", "jetfp8_rotary", "jetfp8_kv_positions", "jetfp8_kv_prefix",
+            "jetfp8_attention_prefix", "jetfp8_attention_prefix_workspace", "jetfp8_kv_fork", "jetfp8_kv_fork_recent",
+            "jetfp8_kv_sweep", "jetfp8_kv_sweep_workspace", "jetfp8_kv_move", "jetfp8_status_string", "jetfp8_version")
+ROTARY_HALVES, ROTARY_INTERLEAVED = 0, 1
 KV_BLOCK, KV_UNIT_WORDS = 64, 8
 KV_OK, KV_BAD_LENGTH, KV_NO_ROWS, KV_NO_BLOCK = 0, 1, 2, 4
 
@@ -73,6 +78,33 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                    ctypes.c_float, vp, vp, vp, vp, i64, vp]
     L.jetfp8_attention_workspace.restype = i64
     L.jetfp8_attention_workspace.argtypes = [i64] * 6
+    L.jetfp8_attention_prefix.restype = c_int
+    L.jetfp8_attention_prefix.argtypes = [vp, i64, i64, vp, i64, vp, vp, i64, i64, vp, vp, i64, vp, i64, i64, i64, i64, i64,
+                                          i64, ctypes.c_float, vp, vp, vp, vp, i64, vp]
+    L.jetfp8_attention_prefix_workspace.restype = i64
+    L.jetfp8_attention_prefix_workspace.argtypes = [i64] * 6
+    L.jetfp8_kv_prefix.restype = c_int
+    L.jetfp8_kv_prefix.argtypes = [vp, i64, vp, i64, i64, vp, vp, vp]
+    L.jetfp8_kv_positions.restype = c_int
+    L.jetfp8_kv_positions.argtypes = [vp, i64, i64, vp, vp]
+    L.jetfp8_kv_fork.restype = c_int
+    L.jetfp8_kv_fork.argtypes = [vp, vp, i64, i64, vp, vp, vp, vp]
+    L.jetfp8_kv_fork_recent.restype = c_int
+    L.jetfp8_kv_fork_recent.argtypes = [vp, vp, i64, i64, i64, vp, i64, vp]
+    L.jetfp8_kv_sweep.restype = c_int
+    L.jetfp8_kv_sweep.argtypes = [vp, vp, i64, i64, i64, vp, vp, vp, vp, vp, vp, i64, vp]
+    L.jetfp8_kv_sweep_workspace.restype = i64
+    L.jetfp8_kv_sweep_workspace.argtypes = [i64] * 3
+    L.jetfp8_kv_move.restype = c_int
+    L.jetfp8_kv_move.argtypes = [vp, i64, i64, i64, vp, vp, i64, vp]
+    L.jetfp8_rotary.restype = c_int
+    L.jetfp8_rotary.argtypes = [vp, i64, i64, i64, i64, vp, vp, i64, c_int, ctypes.c_float, c_int, vp, i64, vp]
+    L.jetfp8_rmsnorm_add_quantize.restype = c_int
+    L.jetfp8_rmsnorm_add_quantize.argtypes = [vp, vp, vp, i64, i64, ctypes.c_float, vp, vp, vp, vp, vp, vp]
+    L.jetfp8_rmsnorm_backward.restype = c_int
+    L.jetfp8_rmsnorm_backward.argtypes = [vp, vp, vp, vp, vp, i64, i64, vp, vp, vp, i64, vp]
+    L.jetfp8_rmsnorm_backward_workspace.restype = i64
+    L.jetfp8_rmsnorm_backward_workspace.argtypes = [i64] * 2
     L.jetfp8_status_string.restype = ctypes.c_char_p
     L.jetfp8_status_string.argtypes = [c_int]
     L.jetfp8_version.restype = c_int
@@ -391,39 +423,179 @@ def jetfp8_kv_append(k_bf16, v_bf16, units, codes, scales, recent_bf16, tokens: 
           *work, H, D, *cache)
 
 
-def attention_workspace(num_units: int, max_new: int, max_seq: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
-    """Bytes of workspace that jetfp8_attention needs for these sizes."""
-    n = load_library().jetfp8_attention_workspace(int(num_units), int(max_new), int(max_seq), int(q_heads),
-                                                  int(kv_heads), int(head_dim))
+def attention_workspace(num_units: int, max_new: int, max_seq: int, q_heads: int, kv_heads: int, head_dim: int,
+                        prefix: bool = False) -> int:
+    """Bytes of workspace that jetfp8_attention needs for these sizes; with prefix, jetfp8_attention_prefix."""
+    name = "jetfp8_attention_prefix_workspace" if prefix else "jetfp8_attention_workspace"
+    n = getattr(load_library(), name)(int(num_units), int(max_new), int(max_seq), int(q_heads), int(kv_heads),
+                                      int(head_dim))
     if n < 0:
-        _check("jetfp8_attention_workspace", n)
+        _check(name, n)
     return n
 
 
-def _attention_inputs(q, units, block_table, codes, scales, recent, T, Hq, H, D, max_new, max_seq, softmax_scale):
-    """The device and the arguments of jetfp8_attention up to its outputs."""
+def _attention_inputs(q, units, block_table, codes, scales, recent, T, Hq, H, D, max_new, max_seq, softmax_scale,
+                      prefix=None):
+    """The device, the name of the entry point and its arguments up to its outputs."""
     dev, work, cache = _kv_buffers(units, codes, scales, recent, H, D)
     requests, width = block_table.shape if getattr(block_table, "ndim", 0) == 2 else (0, 0)
-    return dev, (*_rows(q, (T, Hq, D), "q", dev), T, *work,
-                 _use(block_table, (requests, width), _torch.int32, "block_table", dev), requests, width, *cache,
-                 int(max_new), int(max_seq), Hq, H, D, float(softmax_scale))
+    i32 = _torch.int32
+    name, shared = "jetfp8_attention", ()
+    if prefix is not None:
+        name, shared = "jetfp8_attention_prefix", (_use(prefix, (work[1], 4), i32, "prefix", dev),)
+    return dev, name, (*_rows(q, (T, Hq, D), "q", dev), T, *work, *shared,
+                       _use(block_table, (requests, width), i32, "block_table", dev), requests, width, *cache,
+                       int(max_new), int(max_seq), Hq, H, D, float(softmax_scale))
+
+
+def _space(workspace, device):
+    """A caller's workspace: its pointer and bytes."""
+    if workspace is None:
+        return None, 0
+    return _use(workspace, workspace.shape, None, "workspace", device), workspace.numel() * workspace.element_size()
 
 
 def jetfp8_attention(q_bf16, units, block_table, codes, scales, recent_bf16, tokens: int, max_new: int, max_seq: int,
                      q_heads: int, kv_heads: int, head_dim: int, softmax_scale: float, dst_o_bf16=None, dst_codes=None,
                      dst_scales=None, workspace=None, stream=None) -> None:
+    _attention(q_bf16, units, None, block_table, codes, scales, recent_bf16, tokens, max_new, max_seq, q_heads, kv_heads,
+               head_dim, softmax_scale, dst_o_bf16, dst_codes, dst_scales, workspace, stream)
+
+
+def jetfp8_attention_prefix(q_bf16, units, prefix, block_table, codes, scales, recent_bf16, tokens: int, max_new: int,
+                            max_seq: int, q_heads: int, kv_heads: int, head_dim: int, softmax_scale: float,
+                            dst_o_bf16=None, dst_codes=None, dst_scales=None, workspace=None, stream=None) -> None:
+    if prefix is None:
+        raise ValueError("prefix: required")
+    _attention(q_bf16, units, prefix, block_table, codes, scales, recent_bf16, tokens, max_new, max_seq, q_heads, kv_heads,
+               head_dim, softmax_scale, dst_o_bf16, dst_codes, dst_scales, workspace, stream)
+
+
+def _attention(q, units, prefix, block_table, codes, scales, recent, tokens, max_new, max_seq, q_heads, kv_heads, head_dim,
+               softmax_scale, dst_o_bf16, dst_codes, dst_scales, workspace, stream) -> None:
     bf, u8, f32 = _bf16_u8_f32()
     T, Hq, H, D = int(tokens), int(q_heads), int(kv_heads), int(head_dim)
-    dev, inputs = _attention_inputs(q_bf16, units, block_table, codes, scales, recent_bf16, T, Hq, H, D, max_new, max_seq,
-                                    softmax_scale)
+    dev, name, inputs = _attention_inputs(q, units, block_table, codes, scales, recent, T, Hq, H, D, max_new, max_seq,
+                                          softmax_scale, prefix)
     out = (None if dst_o_bf16 is None else _use(dst_o_bf16, (T, Hq, D), bf, "dst_o_bf16", dev),
            None if dst_codes is None else _use(dst_codes, (T, Hq * D), u8, "dst_codes", dev),
            None if dst_scales is None else _use(dst_scales, (Hq * D // 128, T), f32, "dst_scales", dev))
-    space = (None, 0)
-    if workspace is not None:
-        space = (_use(workspace, workspace.shape, None, "workspace", dev),
-                 workspace.numel() * workspace.element_size())
-    _call("jetfp8_attention", dev, stream, *inputs, *out, *space)
+    _call(name, dev, stream, *inputs, *out, *_space(workspace, dev))
+
+
+def jetfp8_kv_prefix(units, block_table, groups, prefix, stream=None) -> None:
+    i32 = _torch_mod().int32
+    n = units.shape[0] if getattr(units, "ndim", 0) else 0
+    R, W = block_table.shape if getattr(block_table, "ndim", 0) == 2 else (0, 0)
+    p_units = _use(units, (n, KV_UNIT_WORDS), i32, "units")
+    dev = units.get_device()
+    _call("jetfp8_kv_prefix", dev, stream, p_units, n, _use(block_table, (R, W), i32, "block_table", dev), R, W,
+          _use(groups, (R,), i32, "groups", dev), _use(prefix, (n, 4), i32, "prefix", dev))
+
+
+def jetfp8_kv_positions(units, tokens: int, positions, stream=None) -> None:
+    i32, T = _torch_mod().int32, int(tokens)
+    n = units.shape[0] if getattr(units, "ndim", 0) else 0
+    p_units = _use(units, (n, KV_UNIT_WORDS), i32, "units")
+    dev = units.get_device()
+    _call("jetfp8_kv_positions", dev, stream, p_units, n, T, _use(positions, (T,), i32, "positions", dev))
+
+
+def jetfp8_kv_fork(state, block_table, max_blocks: int, requests: int, parents, next_state, next_table,
+                   stream=None) -> None:
+    i32, R, W = _torch_mod().int32, int(requests), int(max_blocks)
+    p_state = _use(state, (R, 2), i32, "state")
+    dev = state.get_device()
+    _call("jetfp8_kv_fork", dev, stream, p_state, _use(block_table, (R, W), i32, "block_table", dev), W, R,
+          _use(parents, (R,), i32, "parents", dev), _use(next_state, (R, 2), i32, "next_state", dev),
+          _use(next_table, (R, W), i32, "next_table", dev))
+
+
+def jetfp8_kv_fork_recent(parents, state, requests: int, kv_heads: int, head_dim: int, recent_bf16, stream=None) -> None:
+    bf, _, _ = _bf16_u8_f32()
+    i32, R, H, D = _torch.int32, int(requests), int(kv_heads), int(head_dim)
+    n = recent_bf16.shape[0] if getattr(recent_bf16, "ndim", 0) else 0
+    p_parents = _use(parents, (R,), i32, "parents")
+    dev = parents.get_device()
+    _call("jetfp8_kv_fork_recent", dev, stream, p_parents, _use(state, (R, 2), i32, "state", dev), R, H, D,
+          _use(recent_bf16, (n, H, 2, KV_BLOCK * D), bf, "recent", dev), n)
+
+
+def kv_sweep_workspace(requests: int, max_blocks: int, num_blocks: int) -> int:
+    """Bytes of workspace that jetfp8_kv_sweep needs for these sizes."""
+    n = load_library().jetfp8_kv_sweep_workspace(int(requests), int(max_blocks), int(num_blocks))
+    if n < 0:
+        _check("jetfp8_kv_sweep_workspace", n)
+    return n
+
+
+def jetfp8_kv_sweep(state, block_table, max_blocks: int, requests: int, num_blocks: int, free_blocks, free_head, live,
+                    next_table=None, moves=None, workspace=None, stream=None) -> None:
+    i32, R, W, n = _torch_mod().int32, int(requests), int(max_blocks), int(num_blocks)
+    p_state = _use(state, (R, 2), i32, "state")
+    dev = state.get_device()
+    _call("jetfp8_kv_sweep", dev, stream, p_state, _use(block_table, (R, W), i32, "block_table", dev), W, R, n,
+          _use(free_blocks, (n,), i32, "free_blocks", dev), _use(free_head, (1,), i32, "free_head", dev),
+          _use(live, (1,), i32, "live", dev),
+          None if next_table is None else _use(next_table, (R, W), i32, "next_table", dev),
+          None if moves is None else _use(moves, (max(1, n // 2), 2), i32, "moves", dev), *_space(workspace, dev))
+
+
+def jetfp8_kv_move(moves, kv_heads: int, head_dim: int, codes, scales, stream=None) -> None:
+    _, u8, f32 = _bf16_u8_f32()
+    H, D = int(kv_heads), int(head_dim)
+    n, blocks = (t.shape[0] if getattr(t, "ndim", 0) else 0 for t in (moves, codes))
+    p_moves = _use(moves, (n, 2), _torch.int32, "moves")
+    dev = moves.get_device()
+    _call("jetfp8_kv_move", dev, stream, p_moves, n, H, D, _use(codes, (blocks, H, 2, KV_BLOCK * D), u8, "codes", dev),
+          _use(scales, (blocks, H, 2), f32, "scales", dev), blocks)
+
+
+def jetfp8_rotary(x_bf16, tokens: int, heads: int, head_dim: int, positions, freqs, layout: int, amplitude: float,
+                  inverse: int, dst_bf16, stream=None) -> None:
+    torch = _torch_mod()
+    T, H, D = int(tokens), int(heads), int(head_dim)
+    dev = x_bf16.get_device()
+    P = freqs.shape[0] if getattr(freqs, "ndim", 0) else 0
+    x, ldx = _rows(x_bf16, (T, H, D), "x", dev)
+    dst, ldd = _rows(dst_bf16, (T, H, D), "dst", dev)
+    _call("jetfp8_rotary", dev, stream, x, ldx, T, H, D, _use(positions, (T,), torch.int32, "positions", dev),
+          _use(freqs, (P,), torch.float64, "freqs", dev), P, int(layout), float(amplitude), int(inverse), dst, ldd)
+
+
+def jetfp8_rmsnorm_add_quantize(x_bf16, residual_bf16, weight_bf16, rows: int, cols: int, eps: float, dst_h_bf16,
+                                dst_codes, dst_scales, dst_rstd=None, dst_y_bf16=None, stream=None) -> None:
+    bf, u8, f32 = _bf16_u8_f32()
+    R, C = int(rows), int(cols)
+    p_x = _use(x_bf16, (R, C), bf, "x_bf16")
+    dev = x_bf16.get_device()
+    _call("jetfp8_rmsnorm_add_quantize", dev, stream, p_x, _use(residual_bf16, (R, C), bf, "residual_bf16", dev),
+          _use(weight_bf16, (C,), bf, "weight_bf16", dev), R, C, float(eps),
+          _use(dst_h_bf16, (R, C), bf, "dst_h_bf16", dev), _use(dst_codes, (R, C), u8, "dst_codes", dev),
+          _use(dst_scales, (C // 128, R), f32, "dst_scales", dev),
+          None if dst_rstd is None else _use(dst_rstd, (R,), f32, "dst_rstd", dev),
+          None if dst_y_bf16 is None else _use(dst_y_bf16, (R, C), bf, "dst_y_bf16", dev))
+
+
+def rmsnorm_backward_workspace(rows: int, cols: int) -> int:
+    """Bytes of workspace that jetfp8_rmsnorm_backward needs for the weight's gradient."""
+    n = load_library().jetfp8_rmsnorm_backward_workspace(int(rows), int(cols))
+    if n < 0:
+        _check("jetfp8_rmsnorm_backward_workspace", n)
+    return n
+
+
+def jetfp8_rmsnorm_backward(dy_bf16, h_bf16, weight_bf16, rstd, dres_bf16, rows: int, cols: int, dst_dx_bf16, dst_dw=None,
+                            workspace=None, stream=None) -> None:
+    bf, _, f32 = _bf16_u8_f32()
+    R, C = int(rows), int(cols)
+    p_dy = _use(dy_bf16, (R, C), bf, "dy_bf16")
+    dev = dy_bf16.get_device()
+    _call("jetfp8_rmsnorm_backward", dev, stream, p_dy, _use(h_bf16, (R, C), bf, "h_bf16", dev),
+          _use(weight_bf16, (C,), bf, "weight_bf16", dev), _use(rstd, (R,), f32, "rstd", dev),
+          None if dres_bf16 is None else _use(dres_bf16, (R, C), bf, "dres_bf16", dev), R, C,
+          _use(dst_dx_bf16, (R, C), bf, "dst_dx_bf16", dev),
+          None if dst_dw is None else _use(dst_dw, (C,), f32, "dst_dw", dev), *_space(workspace, dev))
 
 
 # ------------------------------------------------------------------------------------------------
@@ -489,6 +661,85 @@ def rmsnorm_quantize(x, weight, eps: float, return_y: bool = False, stream=None)
     y = torch.empty((R, C), dtype=torch.bfloat16, device=x.device) if return_y else None
     jetfp8_rmsnorm_quantize(x, weight, R, C, eps, q, s, r, y, stream)
     return (q, s, r, y) if return_y else (q, s, r)
+
+
+def rmsnorm_add_quantize(x, residual, weight, eps: float, return_y: bool = False, out=None, stream=None):
+    """rmsnorm_quantize behind a residual connection: x, residual bf16 [R, C] -> (codes [R, C], scales [C/128, R],
+    rstd [R], h [R, C]) of h = bf16(x + residual) and, with return_y, the normalized activation as well.  out: where h
+    goes (x or residual for an update in place)."""
+    torch = _torch_mod()
+    _need(x, x.shape, torch.bfloat16, "x")
+    R, C = x.shape
+    with _memory_of(stream, x.device):
+        new = x.new_empty
+        q, s, r = new((R, C), dtype=torch.uint8), new((C // 128, R), dtype=torch.float32), new((R,), dtype=torch.float32)
+        h = new((R, C)) if out is None else out
+        y = new((R, C)) if return_y else None
+    jetfp8_rmsnorm_add_quantize(x, residual, weight, R, C, eps, h, q, s, r, y, stream)
+    return (q, s, r, h, y) if return_y else (q, s, r, h)
+
+
+def rmsnorm_backward(dy, h, weight, rstd, dres=None, weight_grad: bool = True, out=None, workspace=None, stream=None):
+    """Backward pass of rmsnorm_quantize (h = x) and rmsnorm_add_quantize: dy, h bf16 [R, C], weight bf16 [C], rstd fp32
+    [R], dres the gradient of h by way of the residual stream -> (dx bf16 [R, C], dw fp32 [C], or None without
+    weight_grad).  out: where dx goes (it may be dy or dres)."""
+    torch = _torch_mod()
+    _need(dy, dy.shape, torch.bfloat16, "dy")
+    R, C = dy.shape
+    dw = None
+    with _memory_of(stream, dy.device):
+        dx = dy.new_empty((R, C)) if out is None else out
+        if weight_grad:
+            dw = dy.new_empty((C,), dtype=torch.float32)
+            if workspace is None:
+                workspace = dy.new_empty(rmsnorm_backward_workspace(R, C), dtype=torch.uint8)
+    jetfp8_rmsnorm_backward(dy, h, weight, rstd, dres, R, C, dx, dw, workspace, stream)
+    return dx, dw
+
+
+def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional[str] = None, factor: float = 1.0,
+                       original: int = 0, low: float = 1.0, high: float = 32.0, device="cuda"):
+    """The frequencies [rotary_dim / 2] fp64 of jetfp8_rotary, base^(-2 i / rotary_dim), for a context longer by `factor`
+    than the one trained on:
+      None       as they are;
+      "linear"   divided by factor (positions closer together);
+      "base"     with base * factor^(rotary_dim / (rotary_dim - 2)): the last pair's is divided by factor, the first stays;
+      "bands"    those that make more than `high` turns in the `original` context stay, those that make less than `low`
+                 are divided by factor, and the ones between are blended linearly in the number of turns."""
+    torch = _torch_mod()
+    P = rotary_dim // 2
+    if rotary_dim < 2 or rotary_dim % 2 or not base > 0 or not factor > 0:
+        raise ValueError("rotary_frequencies: rotary_dim even, base and factor above 0")
+    if scaling == "base":
+        if rotary_dim < 4:
+            raise ValueError("rotary_frequencies: scaling 'base' needs two pairs")
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    i = torch.arange(P, dtype=torch.float64)
+    f = torch.pow(torch.tensor(float(base), dtype=torch.float64), -2 * i / rotary_dim)
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "bands":
+        if not 0 <= low < high or original < 1:
+            raise ValueError("rotary_frequencies: scaling 'bands' needs original and 0 <= low < high")
+        keep = ((original * f / (2 * math.pi) - low) / (high - low)).clamp(0, 1)
+        f = f * (keep + (1 - keep) / factor)
+    elif scaling not in (None, "base"):
+        raise ValueError(f"rotary_frequencies: unknown scaling {scaling!r}")
+    return f.to(device)
+
+
+def rotary(x, positions, freqs, interleaved: bool = False, amplitude: float = 1.0, inverse: bool = False, out=None,
+           stream=None):
+    """Rotary positions of queries and keys: x bf16 [T, heads, D] (rows may be columns of a wider matrix), positions int32
+    [T], freqs fp64 [pairs] (rotary_frequencies) -> bf16 [T, heads, D], or `out` (x itself for an update in place; rows
+    with a negative position are not written).  inverse: the backward pass."""
+    T, H, D = x.shape
+    if out is None:
+        with _memory_of(stream, x.device):
+            out = x.new_empty((T, H, D))
+    jetfp8_rotary(x, T, H, D, positions, freqs, ROTARY_INTERLEAVED if interleaved else ROTARY_HALVES, amplitude,
+                  1 if inverse else 0, out, stream)
+    return out
 
 
 def swiglu_quantize(gate_up, return_h: bool = False, stream=None):
@@ -640,20 +891,90 @@ def kv_append(k, v, units, codes, scales, recent, stream=None) -> None:
     jetfp8_kv_append(k, v, units, codes, scales, recent, T, H, D, stream)
 
 
+def kv_positions(units, tokens: int, stream=None):
+    """Positions int32 [tokens] of a planned step's rows (for rotary), -1 for rows of no unit."""
+    _need(units, units.shape, _torch_mod().int32, "units")
+    with _memory_of(stream, units.device):
+        positions = units.new_empty(int(tokens))
+    jetfp8_kv_positions(units, tokens, positions, stream)
+    return positions
+
+
+def kv_prefix(units, block_table, groups, stream=None):
+    """Which of a planned step's units share blocks: groups int32 [R] (consecutive requests with the same id, 0 or above)
+    -> prefix int32 [units, 4] for attention, the same for every layer."""
+    _need(units, units.shape, _torch_mod().int32, "units")
+    with _memory_of(stream, units.device):
+        prefix = units.new_empty(units.shape[0], 4)
+    jetfp8_kv_prefix(units, block_table, groups, prefix, stream)
+    return prefix
+
+
+class KVFork(NamedTuple):
+    next_state: Any     # int32 [R, 2]
+    next_table: Any     # int32 [R, max_blocks]
+
+
+def kv_fork(state, block_table, parents, stream=None) -> KVFork:
+    """Request r becomes a copy of request parents[r] (int32 [R]; -1 or r: it stays): the state and block table after it.
+    kv_fork_recent copies the unfinished blocks of each layer."""
+    _need(state, state.shape, _torch_mod().int32, "state")
+    R, W = block_table.shape
+    with _memory_of(stream, state.device):
+        f = KVFork(state.new_empty(R, 2), state.new_empty(R, W))
+    jetfp8_kv_fork(state, block_table, W, R, parents, f.next_state, f.next_table, stream)
+    return f
+
+
+def kv_fork_recent(parents, state, recent, stream=None) -> None:
+    """The unfinished blocks of one layer for kv_fork's parents and state (that before the fork)."""
+    n, H, _, size = recent.shape
+    jetfp8_kv_fork_recent(parents, state, parents.shape[0], H, size // KV_BLOCK, recent, stream)
+
+
+class KVSweep(NamedTuple):
+    """What a cache holds: see jetfp8_kv_sweep in include/jetfp8.h."""
+    free_blocks: Any    # int32 [num_blocks], for kv_plan
+    free_head: Any      # int32 [1], 0
+    live: Any           # int32 [1]: blocks that requests hold
+    next_table: Any     # int32 [R, max_blocks], or None
+    moves: Any          # int32 [max(1, num_blocks / 2), 2] for kv_move, or None
+
+
+def kv_sweep(state, block_table, num_blocks: int, compact: bool = False, workspace=None, stream=None) -> KVSweep:
+    """The free list of a cache of num_blocks blocks from what the requests hold; with compact also the tables and moves
+    that bring the held blocks to the ids below `live`."""
+    _need(state, state.shape, _torch_mod().int32, "state")
+    R, W = block_table.shape
+    n = int(num_blocks)
+    size = kv_sweep_workspace(R, W, n)
+    with _memory_of(stream, state.device):
+        new = state.new_empty
+        p = KVSweep(new(n), new(1), new(1), new(R, W) if compact else None, new(max(1, n // 2), 2) if compact else None)
+        if size and workspace is None:
+            workspace = new(size, dtype=_torch.uint8)
+    jetfp8_kv_sweep(state, block_table, W, R, n, p.free_blocks, p.free_head, p.live, p.next_table, p.moves, workspace, stream)
+    return p
+
+
+def kv_move(moves, codes, scales, stream=None) -> None:
+    """Carries kv_sweep's moves out in one layer's cache."""
+    n, H, _, size = codes.shape
+    jetfp8_kv_move(moves, H, size // KV_BLOCK, codes, scales, stream)
+
+
 def attention(q, units, block_table, codes, scales, recent, max_new: int, max_seq: int, softmax_scale=None,
-              quantize: bool = False, return_o: bool = True, workspace=None, stream=None):
+              quantize: bool = False, return_o: bool = True, workspace=None, stream=None, prefix=None):
     """Causal attention of a step's new tokens, after kv_append: q bf16 [T, Hq, D] -> bf16 [T, Hq, D]; with quantize
     (D = 128) -> (codes [T, Hq * D], scales [Hq, T]) and, with return_o, the bf16 matrix as well.  softmax_scale:
-    1 / sqrt(D) unless given.  Rows that belong to no unit are left unwritten."""
+    1 / sqrt(D) unless given.  Rows that belong to no unit are left unwritten.  prefix: kv_prefix's records; blocks that
+    requests share are then read once for all of them (the same results)."""
     T, Hq, D = q.shape
     H = codes.shape[1]
-    dev, inputs = _attention_inputs(q, units, block_table, codes, scales, recent, T, Hq, H, D, max_new, max_seq,
-                                    D ** -0.5 if softmax_scale is None else softmax_scale)
-    size = attention_workspace(units.shape[0], max_new, max_seq, Hq, H, D)
-    space = (None, 0)
-    if workspace is not None:
-        space = (_use(workspace, workspace.shape, None, "workspace", dev),
-                 workspace.numel() * workspace.element_size())
+    dev, name, inputs = _attention_inputs(q, units, block_table, codes, scales, recent, T, Hq, H, D, max_new, max_seq,
+                                          D ** -0.5 if softmax_scale is None else softmax_scale, prefix)
+    size = attention_workspace(units.shape[0], max_new, max_seq, Hq, H, D, prefix is not None)
+    space = _space(workspace, dev)
     o = c = s = None
     with _memory_of(stream, q.device):
         if size and workspace is None:
@@ -663,7 +984,7 @@ def attention(q, units, block_table, codes, scales, recent, max_new: int, max_se
             o = q.new_empty(T, Hq, D)
         if quantize:
             c, s = codes.new_empty(T, Hq * D), scales.new_empty(Hq * D // 128, T)
-    _call("jetfp8_attention", dev, stream, *inputs, None if o is None else o.data_ptr(),
+    _call(name, dev, stream, *inputs, None if o is None else o.data_ptr(),
           None if c is None else c.data_ptr(), None if s is None else s.data_ptr(), *space)
     if not quantize:
         return o

@@ -14,7 +14,8 @@ SRC_DIR = os.path.join(HERE, "csrc")
 LIB_DIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIB_DIR, "libjetfp8.so")
 SOURCES = ["jetfp8_api.hip", "jetfp8_quant.hip", "jetfp8_gemm.hip", "jetfp8_decode.hip", "jetfp8_producers.hip",
-           "jetfp8_cache.hip", "jetfp8_attention.hip"]
+           "jetfp8_norm_backward.hip", "jetfp8_rotary.hip", "jetfp8_cache.hip", "jetfp8_pages.hip",
+           "jetfp8_attention.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",

@@ -45,17 +45,56 @@ bool row_pitch_ok(int64_t ld, int64_t heads, int64_t head_dim) {
 }
 
 bool attention_dims_ok(int64_t num_units, int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads,
-                       int64_t head_dim) {
+                       int64_t head_dim, bool prefix) {
     return dim_ok(num_units) && dim_ok(max_new) && dim_ok(max_seq) && dim_ok(q_heads) && dim_ok(kv_heads) &&
            q_heads % kv_heads == 0 && q_heads <= 65536 && (head_dim == 64 || head_dim == 128) &&
-           jetfp8::attention_fits(num_units, max_new, max_seq, q_heads, kv_heads);
+           jetfp8::attention_fits(num_units, max_new, max_seq, q_heads, kv_heads, prefix);
+}
+
+bool table_ok(int64_t requests, int64_t max_blocks) {
+    return requests >= 1 && requests <= jetfp8::kKvMaxRequests && dim_ok(max_blocks) &&
+           dim_ok(JETFP8_KV_BLOCK * max_blocks) && dim_ok(requests * max_blocks);
+}
+
+bool sweep_ok(int64_t requests, int64_t max_blocks, int64_t num_blocks) {
+    return table_ok(requests, max_blocks) && num_blocks >= 1 && num_blocks <= jetfp8::kKvMaxSweepBlocks;
+}
+
+int attention_call(const void* q_bf16, int64_t ldq, int64_t tokens, const int32_t* units, int64_t num_units,
+                   const int32_t* prefix, const int32_t* block_table, int64_t requests, int64_t max_blocks,
+                   const uint8_t* codes, const float* scales, int64_t num_blocks, const void* recent_bf16,
+                   int64_t recent_blocks, int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads,
+                   int64_t head_dim, float softmax_scale, void* dst_o_bf16, uint8_t* dst_codes, float* dst_scales,
+                   void* workspace, int64_t workspace_bytes, void* stream) {
+    if (!q_bf16 || !units || !block_table || !codes || !scales || !recent_bf16 || (!dst_o_bf16 && !dst_codes) ||
+        !dst_codes != !dst_scales)
+        return JETFP8_ERR_NULL;
+    if (!attention_dims_ok(num_units, max_new, max_seq, q_heads, kv_heads, head_dim, prefix != nullptr) ||
+        !kv_dims_ok(tokens, num_units, kv_heads, head_dim, num_blocks, recent_blocks) || !dim_ok(requests) ||
+        !dim_ok(max_blocks) || !row_pitch_ok(ldq, q_heads, head_dim) || (dst_codes && head_dim != 128) ||
+        recent_blocks < 2 * requests + tokens / JETFP8_KV_BLOCK)
+        return JETFP8_ERR_SHAPE;
+    if (!(softmax_scale > 0.0f && softmax_scale <= FLT_MAX / 2)) return JETFP8_ERR_VALUE;
+    const int64_t need =
+        jetfp8::attention_workspace(num_units, max_new, max_seq, q_heads, kv_heads, head_dim, prefix != nullptr);
+    if (need > 0 && !workspace) return JETFP8_ERR_NULL;
+    if (need > workspace_bytes) return JETFP8_ERR_SHAPE;
+    if (!aligned16(q_bf16) || !aligned16(units) || !aligned16(prefix) || !aligned16(block_table) || !aligned16(codes) ||
+        !aligned16(scales) || !aligned16(recent_bf16) || !aligned16(dst_o_bf16) || !aligned16(dst_codes) ||
+        !aligned16(dst_scales) || !aligned16(workspace))
+        return JETFP8_ERR_ALIGN;
+    return hip_status(jetfp8::launch_attention(
+        static_cast<const uint16_t*>(q_bf16), ldq, tokens, units, num_units, prefix, block_table, requests, max_blocks,
+        codes, scales, num_blocks, static_cast<const uint16_t*>(recent_bf16), recent_blocks, max_new, max_seq, q_heads,
+        kv_heads, head_dim, softmax_scale, static_cast<uint16_t*>(dst_o_bf16), dst_codes, dst_scales,
+        static_cast<float*>(workspace), static_cast<hipStream_t>(stream)));
 }
 
 }  // namespace
 
 extern "C" {
 
-int jetfp8_version(void) { return 401; }
+int jetfp8_version(void) { return 500; }
 
 const char* jetfp8_status_string(int status) {
     switch (status) {
@@ -136,6 +175,41 @@ int jetfp8_rmsnorm_quantize(const void* x_bf16, const void* weight_bf16, int64_t
                                                    static_cast<const uint16_t*>(weight_bf16), rows, cols, eps,
                                                    dst_codes, dst_scales, dst_rstd, static_cast<uint16_t*>(dst_y_bf16),
                                                    static_cast<hipStream_t>(stream)));
+}
+
+int jetfp8_rmsnorm_add_quantize(const void* x_bf16, const void* residual_bf16, const void* weight_bf16, int64_t rows,
+                                int64_t cols, float eps, void* dst_h_bf16, uint8_t* dst_codes, float* dst_scales,
+                                float* dst_rstd, void* dst_y_bf16, void* stream) {
+    if (!x_bf16 || !residual_bf16 || !weight_bf16 || !dst_h_bf16 || !dst_codes || !dst_scales) return JETFP8_ERR_NULL;
+    if (!dim_ok(rows) || !dim_ok(cols) || cols % 128 || cols > jetfp8::kRmsNormMaxCols) return JETFP8_ERR_SHAPE;
+    if (!(eps > 0.0f && eps <= FLT_MAX)) return JETFP8_ERR_VALUE;
+    if (!aligned16(x_bf16) || !aligned16(residual_bf16) || !aligned16(weight_bf16) || !aligned16(dst_h_bf16) ||
+        !aligned16(dst_codes) || !aligned16(dst_scales) || !aligned16(dst_rstd) || !aligned16(dst_y_bf16))
+        return JETFP8_ERR_ALIGN;
+    return hip_status(jetfp8::launch_rmsnorm_add_quant(
+        static_cast<const uint16_t*>(x_bf16), static_cast<const uint16_t*>(residual_bf16),
+        static_cast<const uint16_t*>(weight_bf16), rows, cols, eps, static_cast<uint16_t*>(dst_h_bf16), dst_codes,
+        dst_scales, dst_rstd, static_cast<uint16_t*>(dst_y_bf16), static_cast<hipStream_t>(stream)));
+}
+
+int64_t jetfp8_rmsnorm_backward_workspace(int64_t rows, int64_t cols) {
+    if (!dim_ok(rows) || !dim_ok(cols) || cols % 128 || cols > jetfp8::kRmsNormMaxCols) return JETFP8_ERR_SHAPE;
+    return jetfp8::rmsnorm_backward_workspace(rows, cols);
+}
+
+int jetfp8_rmsnorm_backward(const void* dy_bf16, const void* h_bf16, const void* weight_bf16, const float* rstd,
+                            const void* dres_bf16, int64_t rows, int64_t cols, void* dst_dx_bf16, float* dst_dw,
+                            void* workspace, int64_t workspace_bytes, void* stream) {
+    if (!dy_bf16 || !h_bf16 || !weight_bf16 || !rstd || !dst_dx_bf16 || (dst_dw && !workspace)) return JETFP8_ERR_NULL;
+    if (!dim_ok(rows) || !dim_ok(cols) || cols % 128 || cols > jetfp8::kRmsNormMaxCols) return JETFP8_ERR_SHAPE;
+    if (dst_dw && workspace_bytes < jetfp8::rmsnorm_backward_workspace(rows, cols)) return JETFP8_ERR_SHAPE;
+    if (!aligned16(dy_bf16) || !aligned16(h_bf16) || !aligned16(weight_bf16) || !aligned16(rstd) ||
+        !aligned16(dres_bf16) || !aligned16(dst_dx_bf16) || !aligned16(dst_dw) || !aligned16(workspace))
+        return JETFP8_ERR_ALIGN;
+    return hip_status(jetfp8::launch_rmsnorm_backward(
+        static_cast<const uint16_t*>(dy_bf16), static_cast<const uint16_t*>(h_bf16),
+        static_cast<const uint16_t*>(weight_bf16), rstd, static_cast<const uint16_t*>(dres_bf16), rows, cols,
+        static_cast<uint16_t*>(dst_dx_bf16), dst_dw, static_cast<float*>(workspace), static_cast<hipStream_t>(stream)));
 }
 
 int jetfp8_swiglu_quantize(const void* gate_up_bf16, int64_t rows, int64_t cols, uint8_t* dst_codes,
@@ -243,8 +317,14 @@ int jetfp8_kv_append(const void* k_bf16, int64_t ldk, const void* v_bf16, int64_
 
 int64_t jetfp8_attention_workspace(int64_t num_units, int64_t max_new, int64_t max_seq, int64_t q_heads,
                                    int64_t kv_heads, int64_t head_dim) {
-    if (!attention_dims_ok(num_units, max_new, max_seq, q_heads, kv_heads, head_dim)) return JETFP8_ERR_SHAPE;
-    return jetfp8::attention_workspace(num_units, max_new, max_seq, q_heads, kv_heads, head_dim);
+    if (!attention_dims_ok(num_units, max_new, max_seq, q_heads, kv_heads, head_dim, false)) return JETFP8_ERR_SHAPE;
+    return jetfp8::attention_workspace(num_units, max_new, max_seq, q_heads, kv_heads, head_dim, false);
+}
+
+int64_t jetfp8_attention_prefix_workspace(int64_t num_units, int64_t max_new, int64_t max_seq, int64_t q_heads,
+                                          int64_t kv_heads, int64_t head_dim) {
+    if (!attention_dims_ok(num_units, max_new, max_seq, q_heads, kv_heads, head_dim, true)) return JETFP8_ERR_SHAPE;
+    return jetfp8::attention_workspace(num_units, max_new, max_seq, q_heads, kv_heads, head_dim, true);
 }
 
 int jetfp8_attention(const void* q_bf16, int64_t ldq, int64_t tokens, const int32_t* units, int64_t num_units,
@@ -253,27 +333,107 @@ int jetfp8_attention(const void* q_bf16, int64_t ldq, int64_t tokens, const int3
                      int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads, int64_t head_dim,
                      float softmax_scale, void* dst_o_bf16, uint8_t* dst_codes, float* dst_scales, void* workspace,
                      int64_t workspace_bytes, void* stream) {
-    if (!q_bf16 || !units || !block_table || !codes || !scales || !recent_bf16 || (!dst_o_bf16 && !dst_codes) ||
-        !dst_codes != !dst_scales)
-        return JETFP8_ERR_NULL;
-    if (!attention_dims_ok(num_units, max_new, max_seq, q_heads, kv_heads, head_dim) ||
-        !kv_dims_ok(tokens, num_units, kv_heads, head_dim, num_blocks, recent_blocks) || !dim_ok(requests) ||
-        !dim_ok(max_blocks) || !row_pitch_ok(ldq, q_heads, head_dim) || (dst_codes && head_dim != 128) ||
-        recent_blocks < 2 * requests + tokens / JETFP8_KV_BLOCK)
+    return attention_call(q_bf16, ldq, tokens, units, num_units, nullptr, block_table, requests, max_blocks, codes, scales,
+                          num_blocks, recent_bf16, recent_blocks, max_new, max_seq, q_heads, kv_heads, head_dim,
+                          softmax_scale, dst_o_bf16, dst_codes, dst_scales, workspace, workspace_bytes, stream);
+}
+
+int jetfp8_attention_prefix(const void* q_bf16, int64_t ldq, int64_t tokens, const int32_t* units, int64_t num_units,
+                            const int32_t* prefix, const int32_t* block_table, int64_t requests, int64_t max_blocks,
+                            const uint8_t* codes, const float* scales, int64_t num_blocks, const void* recent_bf16,
+                            int64_t recent_blocks, int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads,
+                            int64_t head_dim, float softmax_scale, void* dst_o_bf16, uint8_t* dst_codes, float* dst_scales,
+                            void* workspace, int64_t workspace_bytes, void* stream) {
+    if (!prefix) return JETFP8_ERR_NULL;
+    return attention_call(q_bf16, ldq, tokens, units, num_units, prefix, block_table, requests, max_blocks, codes, scales,
+                          num_blocks, recent_bf16, recent_blocks, max_new, max_seq, q_heads, kv_heads, head_dim,
+                          softmax_scale, dst_o_bf16, dst_codes, dst_scales, workspace, workspace_bytes, stream);
+}
+
+int jetfp8_kv_positions(const int32_t* units, int64_t num_units, int64_t tokens, int32_t* positions, void* stream) {
+    if (!units || !positions) return JETFP8_ERR_NULL;
+    if (!dim_ok(num_units) || tokens < 1 || tokens > jetfp8::kKvMaxTokens) return JETFP8_ERR_SHAPE;
+    if (!aligned16(units) || !aligned16(positions)) return JETFP8_ERR_ALIGN;
+    return hip_status(jetfp8::launch_kv_positions(units, num_units, tokens, positions, static_cast<hipStream_t>(stream)));
+}
+
+int jetfp8_kv_prefix(const int32_t* units, int64_t num_units, const int32_t* block_table, int64_t requests,
+                     int64_t max_blocks, const int32_t* groups, int32_t* prefix, void* stream) {
+    if (!units || !block_table || !groups || !prefix) return JETFP8_ERR_NULL;
+    if (!dim_ok(num_units) || !table_ok(requests, max_blocks)) return JETFP8_ERR_SHAPE;
+    if (!aligned16(units) || !aligned16(block_table) || !aligned16(groups) || !aligned16(prefix)) return JETFP8_ERR_ALIGN;
+    return hip_status(jetfp8::launch_kv_prefix(units, num_units, block_table, requests, max_blocks, groups, prefix,
+                                               static_cast<hipStream_t>(stream)));
+}
+
+int jetfp8_kv_fork(const int32_t* state, const int32_t* block_table, int64_t max_blocks, int64_t requests,
+                   const int32_t* parents, int32_t* next_state, int32_t* next_table, void* stream) {
+    if (!state || !block_table || !parents || !next_state || !next_table) return JETFP8_ERR_NULL;
+    if (!table_ok(requests, max_blocks)) return JETFP8_ERR_SHAPE;
+    if (!aligned16(state) || !aligned16(block_table) || !aligned16(parents) || !aligned16(next_state) ||
+        !aligned16(next_table))
+        return JETFP8_ERR_ALIGN;
+    return hip_status(jetfp8::launch_kv_fork(state, block_table, max_blocks, requests, parents, next_state, next_table,
+                                             static_cast<hipStream_t>(stream)));
+}
+
+int jetfp8_kv_fork_recent(const int32_t* parents, const int32_t* state, int64_t requests, int64_t kv_heads,
+                          int64_t head_dim, void* recent_bf16, int64_t recent_blocks, void* stream) {
+    if (!parents || !state || !recent_bf16) return JETFP8_ERR_NULL;
+    if (requests < 1 || requests > jetfp8::kKvMaxRequests || !dim_ok(kv_heads) || (head_dim != 64 && head_dim != 128) ||
+        !dim_ok(recent_blocks) || recent_blocks < 2 * requests || requests * kv_heads >= jetfp8::kKvMaxGrid)
         return JETFP8_ERR_SHAPE;
-    if (!(softmax_scale > 0.0f && softmax_scale <= FLT_MAX / 2)) return JETFP8_ERR_VALUE;
-    const int64_t need = jetfp8::attention_workspace(num_units, max_new, max_seq, q_heads, kv_heads, head_dim);
+    if (!aligned16(parents) || !aligned16(state) || !aligned16(recent_bf16)) return JETFP8_ERR_ALIGN;
+    return hip_status(jetfp8::launch_kv_fork_recent(parents, state, requests, kv_heads, head_dim,
+                                                    static_cast<uint16_t*>(recent_bf16), static_cast<hipStream_t>(stream)));
+}
+
+int64_t jetfp8_kv_sweep_workspace(int64_t requests, int64_t max_blocks, int64_t num_blocks) {
+    if (!sweep_ok(requests, max_blocks, num_blocks)) return JETFP8_ERR_SHAPE;
+    return jetfp8::kv_sweep_workspace(requests, max_blocks, num_blocks);
+}
+
+int jetfp8_kv_sweep(const int32_t* state, const int32_t* block_table, int64_t max_blocks, int64_t requests,
+                    int64_t num_blocks, int32_t* free_blocks, int32_t* free_head, int32_t* live, int32_t* next_table,
+                    int32_t* moves, void* workspace, int64_t workspace_bytes, void* stream) {
+    if (!state || !block_table || !free_blocks || !free_head || !live || !next_table != !moves) return JETFP8_ERR_NULL;
+    if (!sweep_ok(requests, max_blocks, num_blocks)) return JETFP8_ERR_SHAPE;
+    const int64_t need = jetfp8::kv_sweep_workspace(requests, max_blocks, num_blocks);
     if (need > 0 && !workspace) return JETFP8_ERR_NULL;
     if (need > workspace_bytes) return JETFP8_ERR_SHAPE;
-    if (!aligned16(q_bf16) || !aligned16(units) || !aligned16(block_table) || !aligned16(codes) || !aligned16(scales) ||
-        !aligned16(recent_bf16) || !aligned16(dst_o_bf16) || !aligned16(dst_codes) || !aligned16(dst_scales) ||
-        !aligned16(workspace))
+    if (!aligned16(state) || !aligned16(block_table) || !aligned16(free_blocks) || !aligned16(free_head) ||
+        !aligned16(live) || !aligned16(next_table) || !aligned16(moves) || !aligned16(workspace))
         return JETFP8_ERR_ALIGN;
-    return hip_status(jetfp8::launch_attention(
-        static_cast<const uint16_t*>(q_bf16), ldq, tokens, units, num_units, block_table, requests, max_blocks, codes,
-        scales, num_blocks, static_cast<const uint16_t*>(recent_bf16), recent_blocks, max_new, max_seq, q_heads,
-        kv_heads, head_dim, softmax_scale, static_cast<uint16_t*>(dst_o_bf16), dst_codes, dst_scales,
-        static_cast<float*>(workspace), static_cast<hipStream_t>(stream)));
+    return hip_status(jetfp8::launch_kv_sweep(state, block_table, max_blocks, requests, num_blocks, free_blocks, free_head,
+                                              live, next_table, moves, static_cast<uint64_t*>(workspace),
+                                              static_cast<hipStream_t>(stream)));
+}
+
+int jetfp8_kv_move(const int32_t* moves, int64_t num_moves, int64_t kv_heads, int64_t head_dim, uint8_t* codes,
+                   float* scales, int64_t num_blocks, void* stream) {
+    if (!moves || !codes || !scales) return JETFP8_ERR_NULL;
+    if (!dim_ok(num_moves) || !dim_ok(kv_heads) || (head_dim != 64 && head_dim != 128) || !dim_ok(num_blocks) ||
+        num_moves >= jetfp8::kKvMaxGrid || kv_heads >= jetfp8::kKvMaxGrid || num_moves * kv_heads >= jetfp8::kKvMaxGrid)
+        return JETFP8_ERR_SHAPE;
+    if (!aligned16(moves) || !aligned16(codes) || !aligned16(scales)) return JETFP8_ERR_ALIGN;
+    return hip_status(jetfp8::launch_kv_move(moves, num_moves, kv_heads, head_dim, codes, scales, num_blocks,
+                                             static_cast<hipStream_t>(stream)));
+}
+
+int jetfp8_rotary(const void* x_bf16, int64_t ldx, int64_t tokens, int64_t heads, int64_t head_dim,
+                  const int32_t* positions, const double* freqs, int64_t pairs, int layout, float amplitude, int inverse,
+                  void* dst_bf16, int64_t ldd, void* stream) {
+    if (layout != JETFP8_ROTARY_HALVES && layout != JETFP8_ROTARY_INTERLEAVED) return JETFP8_ERR_MODE;
+    if (!x_bf16 || !positions || !freqs || !dst_bf16) return JETFP8_ERR_NULL;
+    if (!dim_ok(tokens) || !dim_ok(heads) || head_dim < 16 || head_dim % 16 || head_dim > jetfp8::kRotaryMaxDim ||
+        pairs < 8 || pairs % 8 || 2 * pairs > head_dim || !row_pitch_ok(ldx, heads, head_dim) ||
+        !row_pitch_ok(ldd, heads, head_dim) || (x_bf16 == dst_bf16 && ldx != ldd) || !jetfp8::rotary_fits(tokens, heads))
+        return JETFP8_ERR_SHAPE;
+    if (!(amplitude > 0.0f && amplitude <= FLT_MAX) || (inverse != 0 && inverse != 1)) return JETFP8_ERR_VALUE;
+    if (!aligned16(x_bf16) || !aligned16(positions) || !aligned16(freqs) || !aligned16(dst_bf16)) return JETFP8_ERR_ALIGN;
+    return hip_status(jetfp8::launch_rotary(static_cast<const uint16_t*>(x_bf16), ldx, tokens, heads, head_dim, positions,
+                                            freqs, pairs, layout == JETFP8_ROTARY_INTERLEAVED, amplitude, inverse != 0,
+                                            static_cast<uint16_t*>(dst_bf16), ldd, static_cast<hipStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -22,7 +22,7 @@ constexpr int kWaves = 4;          // waves of a thread block; they share nothin
 // Cache blocks of a span, the unit of summation, and spans of a run, the unit of joining.  Spans of 4 blocks measured
 // 4 % slower where the cache is long (256 requests up to 8192 tokens 421 against 405 us: twice the partial results)
 // and 6 % in the tile kernel (twice the joining), and 4 % faster for 32 requests up to 4096 tokens.
-constexpr int kSpan = 8;
+constexpr int kSpan = kKvSpan;
 constexpr int kRun = 8;
 constexpr int kRunBlocks = kRun * kSpan;
 // The cache's probabilities enter the second product as fp16, in which the values' codes are exact, each times its block's
@@ -41,6 +41,7 @@ constexpr float kLead = 6.0f, kSlack = 8.0f, kDeep = 30.0f, kLow = 130.0f;
 struct AttnArgs {
     const uint16_t* q;
     const KvUnit* units;
+    const int4* prefix;            // of attention_prefix: each unit's group and the blocks that it shares
     const int* table;
     const uint8_t* codes;
     const float* scales;
@@ -500,6 +501,60 @@ __device__ __forceinline__ const uint4* recent_block(const AttnArgs& a, int rece
     return reinterpret_cast<const uint4*>(a.recent + ((int64_t)recent * a.kv_heads + head) * 2 * (kKvBlock * D));
 }
 
+// Takes cache blocks first .. last - 1 of a request, at most a span and at least one, into the rows' state, which is empty
+// before the first (whatever the registers hold).
+template <int D, int R>
+__device__ __forceinline__ void walk_span(State<D, R>& st, const typename State<D, R>::Queries& q, const AttnArgs& a,
+                                          int request, int head, int first, int last, int lane) {
+    typedef State<D, R> S;
+    const int64_t block_bytes = (int64_t)a.kv_heads * 2 * kKvBlock * D;
+    const uint8_t* codes = a.codes + (int64_t)head * 2 * kKvBlock * D;
+    const Run run = load_run(a, request, head, first, last, last, lane);
+    if (!(run.use & 1)) st.clear();
+    Raw<D> kr, vr;
+    const uint8_t* here = codes + __builtin_amdgcn_readlane(run.at, 0) * block_bytes;
+    load_raw<R, false>(kr, here, lane);
+    load_raw<R, true>(vr, here + kKvBlock * D, lane);
+#pragma unroll
+    for (int i = 0; i < kSpan; ++i) {
+        if (first + i >= last) break;
+        const uint8_t* next = codes + __builtin_amdgcn_readlane(run.at, i + 1) * block_bytes;
+        typename S::Scores s;
+#pragma unroll
+        for (int t = 0; t < S::kTiles; ++t)
+#pragma unroll
+            for (int k = 0; k < S::kSteps; ++k) {
+                // a load holds two fragments' codes: halves of two times kShares steps
+                const uint4 w = kr.w[(t * (D / 64) + k / (2 * S::kShares)) * S::kShares + k % S::kShares];
+                const bool second = k / S::kShares % 2;
+                const bf16x8 x = second ? widen(w.z, w.w) : widen(w.x, w.y);
+                s[t] = mfma(x, q[k], k ? s[t] : typename S::Acc{});
+            }
+        const bool more = i + 1 < kSpan && first + i + 1 < last;
+        if (more) load_raw<R, false>(kr, next, lane);
+        if (run.use >> i & 1) {
+            f16x8 p[2][S::kShares];
+            const float c = lane_value(run.c, i), log_v = lane_value(run.log_v, i);
+            float base, den;
+            if (i == 0) take_top<true>(st, s, c, log_v, base, den);
+            else take_top<false>(st, s, c, log_v, base, den);
+            take_half(st, s, c, base, den, 0, p);
+            take_half(st, s, c, base, den, 1, p);
+#pragma unroll
+            for (int t = 0; t < S::kOut; ++t)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int g = 0; g < S::kShares; ++g) {
+                        const uint4 w = vr.w[t * S::kShares + g];
+                        const f16x8 x = h ? widen_f16(w.z, w.w) : widen_f16(w.x, w.y);
+                        st.o[t] = mfma(x, p[h][g], i == 0 && h + g == 0 ? typename S::Acc{} : st.o[t]);
+                    }
+        }
+        if (more) load_raw<R, true>(vr, next + kKvBlock * D, lane);
+    }
+}
+
 // Attention of the query rows of one unit's kv head.  Rows are (new token, query head of the group), R = 16 or 32 of them
 // to a wave.  Scores are formed transposed, S^T = K Q^T, so that a lane holds R scores of one query per block: maximum
 // and sum need two exchanges between lanes, or one, the factors of a row are plain lane values, and the probabilities
@@ -521,7 +576,10 @@ __device__ __forceinline__ const uint4* recent_block(const AttnArgs& a, int rece
 // from memory to registers in whole lines (1 KB per load of a wave) and the next block's are loaded while this one's
 // are used; there is no LDS.  With R = 16 all rows are one wave's and nobody else reads its codes: the loads are marked
 // as not to be kept, which leaves the caches to the partial results (256 requests up to 8192 tokens: 477 -> 422 us).
-template <int D, int R>
+//
+// PREFIX: the spans that the unit's group shares are attention_prefix_kernel's, and the others are taken from the last on,
+// so that the thread blocks without work are whole.
+template <int D, int R, bool PREFIX>
 __global__ __launch_bounds__(kWaves * 64, R == 16 ? 3 : 2) void attention_span_kernel(AttnArgs a) {
     typedef State<D, R> S;
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -529,11 +587,13 @@ __global__ __launch_bounds__(kWaves * 64, R == 16 ? 3 : 2) void attention_span_k
     const int jobs = a.parts * a.row_groups, chunks = (jobs + kWaves - 1) / kWaves;
     const int unit = blockIdx.x / a.kv_heads / chunks, job = blockIdx.x / a.kv_heads % chunks * kWaves + wave;
     if (job >= jobs) return;
-    const int span = job / a.row_groups, row0 = job % a.row_groups * R;
+    const int row0 = job % a.row_groups * R;
     const KvUnit u = a.units[unit];
     if (!unit_fits(u, a.requests, a.tokens, a.recent_blocks, a.num_blocks)) return;
     const int rows = u.rows * a.group, own = (u.block + kSpan - 1) / kSpan;
-    if (row0 >= rows || rows > a.max_rows || u.block > a.max_blocks || span > own) return;
+    const int span = PREFIX ? own - job / a.row_groups : job / a.row_groups;
+    if (row0 >= rows || rows > a.max_rows || u.block > a.max_blocks) return;
+    if (PREFIX ? span < a.prefix[unit].z / kSpan || span < 0 : span > own) return;
 
     typename S::Queries q;
     load_queries<D, R>(q, a, u, head, row0, rows, lane);
@@ -561,56 +621,98 @@ __global__ __launch_bounds__(kWaves * 64, R == 16 ? 3 : 2) void attention_span_k
                 return __any(odd != 0);
             });
     } else {
-        const int first = span * kSpan, last = min(first + kSpan, u.block);
-        const int64_t block_bytes = (int64_t)a.kv_heads * 2 * kKvBlock * D;
-        const uint8_t* codes = a.codes + (int64_t)head * 2 * kKvBlock * D;
-        const Run run = load_run(a, u.request, head, first, last, last, lane);
-        if (!(run.use & 1)) st.clear();
-        Raw<D> kr, vr;
-        const uint8_t* here = codes + __builtin_amdgcn_readlane(run.at, 0) * block_bytes;
-        load_raw<R, false>(kr, here, lane);
-        load_raw<R, true>(vr, here + kKvBlock * D, lane);
-#pragma unroll
-        for (int i = 0; i < kSpan; ++i) {
-            if (first + i >= last) break;
-            const uint8_t* next = codes + __builtin_amdgcn_readlane(run.at, i + 1) * block_bytes;
-            typename S::Scores s;
-#pragma unroll
-            for (int t = 0; t < S::kTiles; ++t)
-#pragma unroll
-                for (int k = 0; k < S::kSteps; ++k) {
-                    // a load holds two fragments' codes: halves of two times kShares steps
-                    const uint4 w = kr.w[(t * (D / 64) + k / (2 * S::kShares)) * S::kShares + k % S::kShares];
-                    const bool second = k / S::kShares % 2;
-                    const bf16x8 x = second ? widen(w.z, w.w) : widen(w.x, w.y);
-                    s[t] = mfma(x, q[k], k ? s[t] : typename S::Acc{});
-                }
-            const bool more = i + 1 < kSpan && first + i + 1 < last;
-            if (more) load_raw<R, false>(kr, next, lane);
-            if (run.use >> i & 1) {
-                f16x8 p[2][S::kShares];
-                const float c = lane_value(run.c, i), log_v = lane_value(run.log_v, i);
-                float base, den;
-                if (i == 0) take_top<true>(st, s, c, log_v, base, den);
-                else take_top<false>(st, s, c, log_v, base, den);
-                take_half(st, s, c, base, den, 0, p);
-                take_half(st, s, c, base, den, 1, p);
-#pragma unroll
-                for (int t = 0; t < S::kOut; ++t)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int g = 0; g < S::kShares; ++g) {
-                            const uint4 w = vr.w[t * S::kShares + g];
-                            const f16x8 x = h ? widen_f16(w.z, w.w) : widen_f16(w.x, w.y);
-                            st.o[t] = mfma(x, p[h][g], i == 0 && h + g == 0 ? typename S::Acc{} : st.o[t]);
-                        }
-            }
-            if (more) load_raw<R, true>(vr, next + kKvBlock * D, lane);
-        }
+        const int first = span * kSpan;
+        walk_span<D, R>(st, q, a, u.request, head, first, min(first + kSpan, u.block), lane);
         factor = st.factor();
     }
     store_part<D, R>(st.top, st.sum(), st.o, factor, a, unit, head, span, row0 + lane % R, rows, lane);
+}
+
+// attention_prefix_kernel takes the blocks that the requests of a group share, in the rows of all its units at once: row g
+// of the group is row g % max_rows of its unit g / max_rows, and 32 of them are a wave's, whatever units they belong to.
+// The units' own records say which group; a thread block is that of the unit whose rows the tile of 32 begins with.
+// It takes a run of 8 spans, two of them by each wave, and joins them in order as the other kernels do, so that one
+// partial result of a run is written instead of eight: in the place of the run's last shared span.
+template <int D>
+__global__ __launch_bounds__(kWaves * 64, 2) void attention_prefix_kernel(AttnArgs a) {
+    typedef State<D, 32> S;
+    constexpr int kQuads = D / 4, kMine = kQuads / 2 / kWaves;       // 4 channels each: of a row, and of a lane to join
+    __shared__ v4f part_o[kWaves][kQuads][32];
+    __shared__ float2 part_ml[kWaves][32];
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int head = blockIdx.x % a.kv_heads;
+    int job = blockIdx.x / a.kv_heads;
+    const int run = job % a.runs;
+    job /= a.runs;
+    const int unit = job / a.row_groups;
+    const int4 group = a.prefix[unit];
+    const int rank = unit - group.x, shared = group.z / kSpan;       // spans
+    if (group.x < 0 || rank < 0 || rank >= group.y || group.y > a.num_units - group.x || shared <= run * kRun ||
+        group.z > a.max_blocks)
+        return;
+    const int row0 = ((rank * a.max_rows + 31) / 32 + job % a.row_groups) * 32;
+    if (row0 >= (rank + 1) * a.max_rows) return;
+    const int request = a.units[group.x].request;
+    if (request < 0 || request >= a.requests) return;
+    const int spans = min(shared - run * kRun, kRun);                // of this run
+
+    // this lane's row
+    const int row = row0 + lane % 32, member = row / a.max_rows, local = row % a.max_rows;
+    const int mine = group.x + min(member, group.y - 1);
+    const KvUnit u = a.units[mine];
+    const int rows = u.rows * a.group;
+    const bool live = member < group.y && unit_fits(u, a.requests, a.tokens, a.recent_blocks, a.num_blocks) && local < rows &&
+                      rows <= a.max_rows && u.block <= a.max_blocks && u.block >= group.z;
+    typename S::Queries q;
+    const uint16_t* p = a.q + (live ? (u.row + local / a.group) * a.ldq + ((int64_t)head * a.group + local % a.group) * D : 0) +
+                        lane / 32 * 8;
+#pragma unroll
+    for (int k = 0; k < S::kSteps; ++k) {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (live) x = *reinterpret_cast<const uint4*>(p + k * 16);
+        q[k] = __builtin_bit_cast(bf16x8, x);
+    }
+
+    float M = -INFINITY, L = 0.0f;
+    v4f o[kMine];
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) o[i] = v4f{};
+    for (int s0 = 0; s0 < spans; s0 += kWaves) {
+        if (s0) __syncthreads();
+        if (s0 + wave < spans) {
+            S st;
+            const int first = (run * kRun + s0 + wave) * kSpan;
+            walk_span<D, 32>(st, q, a, request, head, first, first + kSpan, lane);
+            const float factor = st.factor(), l = st.sum();
+#pragma unroll
+            for (int t = 0; t < S::kOut; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    part_o[wave][t * 8 + j * 2 + lane / 32][lane % 32] =
+                        v4f{st.o[t][4 * j], st.o[t][4 * j + 1], st.o[t][4 * j + 2], st.o[t][4 * j + 3]} * factor;
+            if (lane < 32) part_ml[wave][lane] = make_float2(st.top, l);
+        }
+        __syncthreads();
+        const int n = min(spans - s0, kWaves);
+        for (int s = 0; s < n; ++s) {
+            const float2 ml = part_ml[s][lane % 32];
+            float x, y;
+            join_factors(M, ml.x, x, y);
+            L = fmaf(L, x, ml.y * y);
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) {
+                const v4f v = part_o[s][(wave * kMine + i) * 2 + lane / 32][lane % 32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) o[i][c] = fmaf(o[i][c], x, v[c] * y);
+            }
+        }
+    }
+    if (!live) return;
+    const int64_t at = (((int64_t)mine * a.kv_heads + head) * a.parts + run * kRun + spans - 1) * a.max_rows + local;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+        *reinterpret_cast<v4f*>(a.part_o + at * D + (wave * kMine + i) * 8 + lane / 32 * 4) = o[i];
+    if (wave == 0 && lane < 32) a.part_ml[at] = make_float2(M, L);
 }
 
 // The pair of units that stands at place x if all are ordered by the blocks that precede them, most first (64 classes;
@@ -920,7 +1022,9 @@ __device__ __forceinline__ void join_parts(const float2& ml, const float* from, 
 // latency of a few dependent loads, so all of a run's parts are loaded at once and, where rows are few and may have
 // several runs, WAVES waves form them at the same time.  (Loads of parts that are not there, of the last one again, cost
 // 1 % of a chunk of 2048 at 14336 and 2 % of 16 chunks up to 12000.)
-template <int D, bool SPANS, int WAVES>
+//
+// PREFIX: a run's shared spans are one partial result, that of the last of them.
+template <int D, bool SPANS, int WAVES, bool PREFIX>
 __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
     constexpr int W = D / 64;       // channels of a lane
     __shared__ float run_o[WAVES > 1 ? kRun : 1][D];
@@ -944,12 +1048,15 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
     auto load_ml = [&](int first, int n) {
         return lane < n ? pml[(int64_t)(first + lane) * a.max_rows] : make_float2(-INFINITY, 0.0f);
     };
+    const int shared = PREFIX ? a.prefix[unit].z / kSpan : 0;
+    // First partial result of the run that begins at span s.
+    auto run_begin = [&](int s) { return PREFIX && shared > s ? min(shared, s + kRun) - 1 : s; };
     float M = -INFINITY, L = 0.0f, o[W];
 #pragma unroll
     for (int i = 0; i < W; ++i) o[i] = 0.0f;
     if (!SPANS || runs <= 1) {
         if (WAVES > 1 && wave) return;
-        for (int s0 = 0; s0 <= parts; s0 += kJoin) {
+        for (int s0 = run_begin(0); s0 <= parts; s0 += kJoin) {
             const int n = min(kJoin, parts + 1 - s0);
             join_parts<W>(load_ml(s0, n), po + s0 * step, step, n, lane, M, L, o);
         }
@@ -957,7 +1064,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
         for (int r0 = 0; r0 < runs; r0 += kRun) {
             const int n = min(kRun, runs - r0);
             for (int r = wave % WAVES; r < n; r += WAVES) {
-                const int s0 = (r0 + r) * kRun, m = min(kRun, parts - s0);
+                const int s0 = run_begin((r0 + r) * kRun), m = min((r0 + r + 1) * kRun, parts) - s0;
                 float rm = -INFINITY, rl = 0.0f, ro[W];
 #pragma unroll
                 for (int i = 0; i < W; ++i) ro[i] = 0.0f;
@@ -1028,7 +1135,7 @@ double attn_waves(const AttnShape& s, int64_t num_units, int64_t kv_heads) {
     return (double)num_units * kv_heads * ((s.max_rows + 31) / 32);
 }
 
-AttnShape attn_shape(int64_t num_units, int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads) {
+AttnShape attn_shape(int64_t num_units, int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads, bool prefix) {
     AttnShape s;
     s.max_rows = (max_new < kKvBlock ? max_new : kKvBlock) * (q_heads / kv_heads);
     s.max_blocks = (max_seq - 1) / kKvBlock;
@@ -1038,7 +1145,7 @@ AttnShape attn_shape(int64_t num_units, int64_t max_new, int64_t max_seq, int64_
     // the tile kernel if that has enough waves (32 rows each) for the chip's 1024 SIMDs: below, spans in parallel win (256
     // tokens at 4096, 320 waves: 54 against 106 us), at 1072 and 1472 waves the two are within 5 %, above the
     // partial results cost more than they bring (16 times 64 tokens at 4096, 3008 waves: 157 against 109 us).
-    s.split = spans > 0 && (s.max_rows <= 16 || attn_waves(s, num_units, kv_heads) < 1024);
+    s.split = spans > 0 && (prefix || s.max_rows <= 16 || attn_waves(s, num_units, kv_heads) < 1024);
     s.rows = s.split && s.max_rows <= 16 ? 16 : 32;
     s.row_groups = (s.max_rows + s.rows - 1) / s.rows;
     s.parts = s.split ? spans + 1 : s.runs > 1 ? s.runs + 1 : 0;
@@ -1056,48 +1163,56 @@ double attn_blocks(const AttnShape& s, int64_t num_units, int64_t kv_heads) {
     return (double)((num_units + 1) / 2 * 2) * kv_heads * ((s.row_groups + kWaves - 1) / kWaves) * s.runs;
 }
 
-template <int D>
+template <int D, bool PREFIX>
 hipError_t launch(const AttnArgs& a, const AttnShape& s, unsigned grid, hipStream_t st) {
+    if (PREFIX) {
+        // (no more thread blocks than the grid that attention_fits looks at)
+        const int64_t blocks = (int64_t)a.num_units * a.kv_heads * s.runs * s.row_groups;
+        attention_prefix_kernel<D><<<(unsigned)blocks, kWaves * 64, 0, st>>>(a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
     if (!s.split) attention_tile_kernel<D><<<grid, kWaves * 64, 0, st>>>(a);
-    else if (s.rows == 16) attention_span_kernel<D, 16><<<grid, kWaves * 64, 0, st>>>(a);
-    else attention_span_kernel<D, 32><<<grid, kWaves * 64, 0, st>>>(a);
+    else if (s.rows == 16) attention_span_kernel<D, 16, PREFIX><<<grid, kWaves * 64, 0, st>>>(a);
+    else attention_span_kernel<D, 32, PREFIX><<<grid, kWaves * 64, 0, st>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || s.parts == 0) return e;
     const int64_t rows = (int64_t)a.num_units * a.kv_heads * a.max_rows;
-    if (!s.split) attention_join_kernel<D, false, 1><<<(unsigned)((rows + 3) / 4), 256, 0, st>>>(a);
+    if (!s.split) attention_join_kernel<D, false, 1, false><<<(unsigned)((rows + 3) / 4), 256, 0, st>>>(a);
     // Four waves form a row's runs at once where there are several and rows are too few to fill the chip (one wave a row
     // against four, us: 4 runs 6.3 / 4.6 for 128 rows, 7.4 / 7.2 for 1024, 8.7 / 10.5 for 2048; 16 runs 17.5 / 8.8,
     // 20.8 / 16.2 and 23.2 / 25.9; 2 runs 4.0 / 4.5, 4.7 / 5.5, 5.4 / 8.7).
-    else if (s.runs <= 2 || rows >= 2048) attention_join_kernel<D, true, 1><<<(unsigned)((rows + 3) / 4), 256, 0, st>>>(a);
-    else attention_join_kernel<D, true, 4><<<(unsigned)rows, 256, 0, st>>>(a);
+    else if (s.runs <= 2 || rows >= 2048) attention_join_kernel<D, true, 1, PREFIX><<<(unsigned)((rows + 3) / 4), 256, 0, st>>>(a);
+    else attention_join_kernel<D, true, 4, PREFIX><<<(unsigned)rows, 256, 0, st>>>(a);
     return hipGetLastError();
 }
 
 }  // namespace
 
 int64_t attention_workspace(int64_t num_units, int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads,
-                            int64_t D) {
-    return partial_rows(attn_shape(num_units, max_new, max_seq, q_heads, kv_heads), num_units, kv_heads) * (D + 2) *
+                            int64_t D, bool prefix) {
+    return partial_rows(attn_shape(num_units, max_new, max_seq, q_heads, kv_heads, prefix), num_units, kv_heads) * (D + 2) *
            (int64_t)sizeof(float);
 }
 
-bool attention_fits(int64_t num_units, int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads) {
-    const AttnShape s = attn_shape(num_units, max_new, max_seq, q_heads, kv_heads);
+bool attention_fits(int64_t num_units, int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads, bool prefix) {
+    const AttnShape s = attn_shape(num_units, max_new, max_seq, q_heads, kv_heads, prefix);
     const double join = s.parts ? (double)num_units * kv_heads * s.max_rows / 4 : 0.0;      // its thread blocks, nearly
     return attn_blocks(s, num_units, kv_heads) < kKvMaxGrid && join < kKvMaxGrid - 1 &&
            (double)num_units * kv_heads * s.max_rows <= INT32_MAX;
 }
 
 hipError_t launch_attention(const uint16_t* q, int64_t ldq, int64_t tokens, const int32_t* units, int64_t num_units,
-                            const int32_t* table, int64_t requests, int64_t width, const uint8_t* codes,
-                            const float* scales, int64_t num_blocks, const uint16_t* recent, int64_t recent_blocks,
-                            int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads, int64_t D,
-                            float softmax_scale, uint16_t* o, uint8_t* oq, float* os, float* workspace,
+                            const int32_t* prefix, const int32_t* table, int64_t requests, int64_t width,
+                            const uint8_t* codes, const float* scales, int64_t num_blocks, const uint16_t* recent,
+                            int64_t recent_blocks, int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads,
+                            int64_t D, float softmax_scale, uint16_t* o, uint8_t* oq, float* os, float* workspace,
                             hipStream_t st) {
-    const AttnShape s = attn_shape(num_units, max_new, max_seq, q_heads, kv_heads);
+    const AttnShape s = attn_shape(num_units, max_new, max_seq, q_heads, kv_heads, prefix != nullptr);
     AttnArgs a;
     a.q = q;
     a.units = reinterpret_cast<const KvUnit*>(units);
+    a.prefix = reinterpret_cast<const int4*>(prefix);
     a.table = table;
     a.codes = codes;
     a.scales = scales;
@@ -1128,7 +1243,8 @@ hipError_t launch_attention(const uint16_t* q, int64_t ldq, int64_t tokens, cons
     // at 17344 344 -> 360, at 31840 405 -> 428.
     a.ordered = requests > 1 && s.max_blocks > 0 && num_units <= 2 * 256 * kOrder && attn_waves(s, num_units, kv_heads) < 12288;
     const unsigned grid = (unsigned)attn_blocks(s, num_units, kv_heads);
-    return D == 64 ? launch<64>(a, s, grid, st) : launch<128>(a, s, grid, st);
+    if (prefix && s.split) return D == 64 ? launch<64, true>(a, s, grid, st) : launch<128, true>(a, s, grid, st);
+    return D == 64 ? launch<64, false>(a, s, grid, st) : launch<128, false>(a, s, grid, st);
 }
 
 }  // namespace jetfp8

@@ -130,12 +130,15 @@ __device__ __forceinline__ float swiglu_fast(float g, float u, bool& exact) {
 // 268.9 -> 242.3 us at 65536 x 5120, bitwise the same codes, scales and rstd.  The group scales of the block's
 // rows are staged in LDS and written as runs per group.  (Four rows per wave, with or without the next row's loads
 // issued ahead, measured slower than one: all blocks loaded, then all computed, in step.)
+//
+// ADD: the row is h = bf16(x + residual) instead of x, and is written out as the residual stream's next value.  A
+// lane adds, keeps and writes the same 8 columns, so h may lie where x or the residual does.
 constexpr int RN_WAVES = 8;
 
-template <int NCH, int WPR>
+template <int NCH, int WPR, bool ADD>
 __global__ __launch_bounds__(RN_WAVES * 64) void rmsnorm_quant_kernel(
-    const uint16_t* __restrict__ x, const uint16_t* __restrict__ w, int64_t R, int64_t C, float eps,
-    uint8_t* __restrict__ q, float* __restrict__ s, float* __restrict__ rstd, uint16_t* __restrict__ y) {
+    const uint16_t* x, const uint16_t* residual, const uint16_t* __restrict__ w, int64_t R, int64_t C, float eps,
+    uint16_t* h, uint8_t* __restrict__ q, float* __restrict__ s, float* __restrict__ rstd, uint16_t* __restrict__ y) {
     constexpr int ROWS = RN_WAVES / WPR, HCH = NCH / WPR;
     __shared__ float sc[NCH * 4][ROWS];
     __shared__ double pss[ROWS][WPR];
@@ -151,6 +154,25 @@ __global__ __launch_bounds__(RN_WAVES * 64) void rmsnorm_quant_kernel(
     for (int k = 0; k < HCH; ++k) {
         const int64_t col = (int64_t)(part * HCH + k) * 512 + lane * 8;
         v[k] = ld16(x + rowc * C + (col < C ? col : 0));         // in-bounds stand-in past C: not used
+    }
+    if (ADD) {
+        uint4 b[HCH];
+#pragma unroll
+        for (int k = 0; k < HCH; ++k) {
+            const int64_t col = (int64_t)(part * HCH + k) * 512 + lane * 8;
+            b[k] = ld16(residual + rowc * C + (col < C ? col : 0));
+        }
+#pragma unroll
+        for (int k = 0; k < HCH; ++k) {
+            const int64_t col = (int64_t)(part * HCH + k) * 512 + lane * 8;
+            uint32_t sum[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                sum[i] = bf16x2_rne(elem_of(v[k], 2 * i) + elem_of(b[k], 2 * i),
+                                    elem_of(v[k], 2 * i + 1) + elem_of(b[k], 2 * i + 1));
+            v[k] = make_uint4(sum[0], sum[1], sum[2], sum[3]);
+            if (live && col < C) *reinterpret_cast<uint4*>(h + row * C + col) = v[k];
+        }
     }
     double pa[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
@@ -295,19 +317,35 @@ __global__ __launch_bounds__(SG_WAVES * 64) void swiglu_quant_kernel(const uint1
     }
 }
 
-hipError_t launch_rmsnorm_quant(const uint16_t* x, const uint16_t* w, int64_t R, int64_t C, float eps, uint8_t* q,
-                                float* s, float* rstd, uint16_t* y, hipStream_t st) {
+namespace {
+
+template <bool ADD>
+hipError_t launch_norm(const uint16_t* x, const uint16_t* res, const uint16_t* w, int64_t R, int64_t C, float eps,
+                       uint16_t* h, uint8_t* q, float* s, float* rstd, uint16_t* y, hipStream_t st) {
     if (C > kRmsNormMaxCols) return hipErrorInvalidValue;
     const dim3 block(RN_WAVES * 64);
     const dim3 grid1((unsigned)((R + RN_WAVES - 1) / RN_WAVES)), grid2((unsigned)((R + RN_WAVES / 2 - 1) / (RN_WAVES / 2)));
     const int nch = (int)((C + 511) / 512);
-    if (nch <= 2) hipLaunchKernelGGL((rmsnorm_quant_kernel<2, 1>), grid1, block, 0, st, x, w, R, C, eps, q, s, rstd, y);
-    else if (nch <= 4) hipLaunchKernelGGL((rmsnorm_quant_kernel<4, 1>), grid1, block, 0, st, x, w, R, C, eps, q, s, rstd, y);
-    else if (nch <= 8) hipLaunchKernelGGL((rmsnorm_quant_kernel<8, 2>), grid2, block, 0, st, x, w, R, C, eps, q, s, rstd, y);
-    else if (nch <= 10) hipLaunchKernelGGL((rmsnorm_quant_kernel<10, 2>), grid2, block, 0, st, x, w, R, C, eps, q, s, rstd, y);
-    else if (nch <= 12) hipLaunchKernelGGL((rmsnorm_quant_kernel<12, 2>), grid2, block, 0, st, x, w, R, C, eps, q, s, rstd, y);
-    else hipLaunchKernelGGL((rmsnorm_quant_kernel<16, 2>), grid2, block, 0, st, x, w, R, C, eps, q, s, rstd, y);
+    if (nch <= 2) rmsnorm_quant_kernel<2, 1, ADD><<<grid1, block, 0, st>>>(x, res, w, R, C, eps, h, q, s, rstd, y);
+    else if (nch <= 4) rmsnorm_quant_kernel<4, 1, ADD><<<grid1, block, 0, st>>>(x, res, w, R, C, eps, h, q, s, rstd, y);
+    else if (nch <= 8) rmsnorm_quant_kernel<8, 2, ADD><<<grid2, block, 0, st>>>(x, res, w, R, C, eps, h, q, s, rstd, y);
+    else if (nch <= 10) rmsnorm_quant_kernel<10, 2, ADD><<<grid2, block, 0, st>>>(x, res, w, R, C, eps, h, q, s, rstd, y);
+    else if (nch <= 12) rmsnorm_quant_kernel<12, 2, ADD><<<grid2, block, 0, st>>>(x, res, w, R, C, eps, h, q, s, rstd, y);
+    else rmsnorm_quant_kernel<16, 2, ADD><<<grid2, block, 0, st>>>(x, res, w, R, C, eps, h, q, s, rstd, y);
     return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_rmsnorm_quant(const uint16_t* x, const uint16_t* w, int64_t R, int64_t C, float eps, uint8_t* q,
+                                float* s, float* rstd, uint16_t* y, hipStream_t st) {
+    return launch_norm<false>(x, nullptr, w, R, C, eps, nullptr, q, s, rstd, y, st);
+}
+
+hipError_t launch_rmsnorm_add_quant(const uint16_t* x, const uint16_t* res, const uint16_t* w, int64_t R, int64_t C,
+                                    float eps, uint16_t* h, uint8_t* q, float* s, float* rstd, uint16_t* y,
+                                    hipStream_t st) {
+    return launch_norm<true>(x, res, w, R, C, eps, h, q, s, rstd, y, st);
 }
 
 bool swiglu_quant_fits(int64_t R, int64_t F) {

@@ -22,7 +22,7 @@
  * Conventions for every entry point:
  *   - Matrices are dense, row-major, last index contiguous; bf16 tensors are passed as raw 16-bit
  *     patterns (void*), FP8 codes as uint8_t, scales as float.  No strides, but for the row pitches (ldq, ldk, ldv) of
- *     the key/value cache's calls.
+ *     the key/value cache's calls and those (ldx, ldd) of the rotary positions.
  *   - Every pointer is a DEVICE pointer owned by the caller; the library never allocates, frees or
  *     synchronizes.  Work is enqueued on `stream` (a hipStream_t; NULL = the default stream) and runs
  *     asynchronously; outputs are valid once the stream has reached that point.
@@ -30,7 +30,8 @@
  *     negative jetfp8_status; on error nothing has been enqueued and outputs are untouched
  *     (JETFP8_ERR_HIP: a launch was rejected by the runtime; earlier kernels of the same call may have
  *     been enqueued).  No exception ever crosses this interface.
- *   - All pointers must be 16-byte aligned (JETFP8_ERR_ALIGN otherwise).  Buffers must not overlap.
+ *   - All pointers must be 16-byte aligned (JETFP8_ERR_ALIGN otherwise).  Buffers must not overlap, but where a call
+ *     says that an output may be one of its inputs.
  *   - Sizes: every dimension >= 1; every grouped or contraction axis a multiple of 128, plus the
  *     per-mode rules below (JETFP8_ERR_SHAPE otherwise); every dimension < 2^31.  Kernels address their
  *     tiles with 32-bit offsets and launch one-dimensional grids, so each call also rejects, with
@@ -47,7 +48,12 @@
  *       swiglu_quantize ..... ceil(cols / 512) * ceil(rows / 32) >= 2^31, or 128 * cols >= 2^31 (32 rows of
  *                             gate_up in bytes);
  *       kv_append, attention  2 * kv_heads * num_units >= 2^24, and attention also grids of its own kernels of
- *                             2^24 thread blocks or more (a launch holds fewer than 2^32 threads).
+ *                             2^24 thread blocks or more (a launch holds fewer than 2^32 threads);
+ *       rotary .............. tokens >= 2^24 - 1024, or heads >= 2^20;
+ *       kv_prefix, kv_fork,
+ *       kv_sweep ............ requests > 4096, 64 * max_blocks >= 2^31, or requests * max_blocks >= 2^31;
+ *       kv_fork_recent,
+ *       kv_move ............. requests (moves) * kv_heads >= 2^24.
  *   - Thread safety: calls are independent; concurrent calls on different streams are allowed.
  */
 #ifndef JETFP8_H
@@ -131,6 +137,31 @@ int jetfp8_requantize_cols_t(const uint8_t* codes, const float* scales, int64_t 
  * Finite inputs whose y overflows bf16 give unspecified codes for that group. */
 int jetfp8_rmsnorm_quantize(const void* x_bf16, const void* weight_bf16, int64_t rows, int64_t cols, float eps,
                             uint8_t* dst_codes, float* dst_scales, float* dst_rstd, void* dst_y_bf16, void* stream);
+
+/* The same behind a residual connection: h = bf16(fl32(x + residual)), the residual stream's next value, is written to
+ * dst_h_bf16 [rows][cols], and codes, scales, rstd and y are those of jetfp8_rmsnorm_quantize of h, bit for bit.  dst_h_bf16
+ * may be x_bf16 or residual_bf16 (an update in place).  x + residual must not overflow bf16. */
+int jetfp8_rmsnorm_add_quantize(const void* x_bf16, const void* residual_bf16, const void* weight_bf16, int64_t rows,
+                                int64_t cols, float eps, void* dst_h_bf16, uint8_t* dst_codes, float* dst_scales,
+                                float* dst_rstd, void* dst_y_bf16, void* stream);
+
+/* Backward pass of both.  Gradients between operators stay in bf16 (Jet-RL explainers, "Schema de Quantification"); with
+ * dy that of y (from DGrad), dres that of h by way of the residual stream (NULL: none), the roundings taken as the identity
+ * and g = dy * weight:
+ *   dx[i][k] = rstd[i] * (g[i][k] - h[i][k] * rstd[i]^2 * mean_k(g[i] h[i])) + dres[i][k]
+ *   dw[k]    = sum_i dy[i][k] * h[i][k] * rstd[i]
+ * dx is the gradient of h, so of x and of the residual alike.  dy, h, dres [rows][cols] bf16, weight [cols] bf16, rstd
+ * [rows] fp32 -> dst_dx_bf16 [rows][cols] (fp32, rounded once; it may be dy_bf16 or dres_bf16), dst_dw [cols] fp32
+ * (NULL: not written; then no workspace is needed).  Column sums are fp32 in one fixed order over at most 512 parts of the
+ * rows and fp64 over the parts: a call's results are the same every time.  cols % 128 == 0 and cols <= 8192.
+ * workspace: jetfp8_rmsnorm_backward_workspace() bytes; calls that may run at the same time need one each;
+ * JETFP8_ERR_SHAPE if workspace_bytes is less. */
+int jetfp8_rmsnorm_backward(const void* dy_bf16, const void* h_bf16, const void* weight_bf16, const float* rstd,
+                            const void* dres_bf16, int64_t rows, int64_t cols, void* dst_dx_bf16, float* dst_dw,
+                            void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that jetfp8_rmsnorm_backward needs for dst_dw; JETFP8_ERR_SHAPE if it would refuse the sizes. */
+int64_t jetfp8_rmsnorm_backward_workspace(int64_t rows, int64_t cols);
 
 /* Fused SwiGLU -> 1x128 quantization (the activation in front of the down projection, quantized by the
  * operator that produces it; Jet-RL explainers, "Schema de Quantification"):
@@ -312,6 +343,96 @@ int jetfp8_attention(const void* q_bf16, int64_t ldq, int64_t tokens, const int3
  * less of both as two calls, each with a part of the plan's units (any part, in any order) and its own max_new. */
 int64_t jetfp8_attention_workspace(int64_t num_units, int64_t max_new, int64_t max_seq, int64_t q_heads,
                                    int64_t kv_heads, int64_t head_dim);
+
+/* ---- Samples that share a prompt, and the cache's pages between steps ------------------------------------------
+ *
+ * Reinforcement learning rolls out several samples of each prompt (Jet-RL explainers, "Enonce du Probleme": rollout is
+ * most of the time).  Their requests hold the prompt's complete blocks in common: the same ids at the head of their rows
+ * of the block table.  A request holds what the first tokens / 64 entries of its row name, and nothing else says so:
+ * blocks need no counts, and a request that is done gives up its own by having 0 tokens in its state.
+ */
+
+/* Which units of a step share blocks, from jetfp8_kv_plan's units in their order: once for a step, for all layers.
+ *   groups [requests] int32: consecutive requests with the same id, 0 or above, make a group (those with the same id
+ *                              further on another one); a negative id: no group;
+ *   prefix [num_units][4] int32: for the units of a group of which two requests or more have new tokens, and whose tables
+ *                              agree in 8 blocks or more before the earliest of the units: the first unit of the group,
+ *                              the number of its units, the blocks that they share (a multiple of 8), 0.  Other units:
+ *                              itself, 1, 0, 0; unused ones -1, 0, 0, 0.
+ * The tables are compared, so a group whose requests turn out to share less is no error. */
+int jetfp8_kv_prefix(const int32_t* units, int64_t num_units, const int32_t* block_table, int64_t requests,
+                     int64_t max_blocks, const int32_t* groups, int32_t* prefix, void* stream);
+
+/* jetfp8_attention, with the blocks that the units of a group share read once for all their rows.  prefix: of
+ * jetfp8_kv_prefix for these units and tables (others give unspecified results of the units concerned, within the buffers).
+ * The results are those of jetfp8_attention, bit for bit.  workspace: jetfp8_attention_prefix_workspace() bytes. */
+int jetfp8_attention_prefix(const void* q_bf16, int64_t ldq, int64_t tokens, const int32_t* units, int64_t num_units,
+                            const int32_t* prefix, const int32_t* block_table, int64_t requests, int64_t max_blocks,
+                            const uint8_t* codes, const float* scales, int64_t num_blocks, const void* recent_bf16,
+                            int64_t recent_blocks, int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads,
+                            int64_t head_dim, float softmax_scale, void* dst_o_bf16, uint8_t* dst_codes, float* dst_scales,
+                            void* workspace, int64_t workspace_bytes, void* stream);
+
+int64_t jetfp8_attention_prefix_workspace(int64_t num_units, int64_t max_new, int64_t max_seq, int64_t q_heads,
+                                          int64_t kv_heads, int64_t head_dim);
+
+/* Requests that go on from others: samples of one prompt, beams, resampled rollouts.  parents [requests] int32: request r
+ * becomes a copy of request parents[r] as it is now; it stays as it is if that is r or no request, or if one of the two has
+ * a recent block other than 0 or 1.  Any map will do, also one in which requests change places.  Writes, to other
+ * buffers than the inputs,
+ *   next_state [requests][2]: a copy has its parent's tokens, and the one of its own recent blocks that was not in use;
+ *   next_table [requests][max_blocks]: the parent's row (the request's own if it stays), -1 behind its complete blocks.
+ * Per layer, jetfp8_kv_fork_recent copies the unfinished blocks.  A copy's former blocks are free after the next sweep. */
+int jetfp8_kv_fork(const int32_t* state, const int32_t* block_table, int64_t max_blocks, int64_t requests,
+                   const int32_t* parents, int32_t* next_state, int32_t* next_table, void* stream);
+
+/* The recent blocks of one layer for the same parents and (former) state.  Repeating the call writes the same values. */
+int jetfp8_kv_fork_recent(const int32_t* parents, const int32_t* state, int64_t requests, int64_t kv_heads,
+                          int64_t head_dim, void* recent_bf16, int64_t recent_blocks, void* stream);
+
+/* The free list anew, from what the requests hold (entries that are no block of the cache do not count):
+ *   free_blocks [num_blocks] int32: the blocks that nobody holds, ascending, and -1 behind them, which ends the list for
+ *                              jetfp8_kv_plan; free_head [1] int32: 0;  live [1] int32: the number L of held blocks.
+ * With next_table and moves (both or neither) the cache is compacted: held blocks with ids of L and above, ascending, move
+ * to the free ids below L, ascending, and the free list begins with L:
+ *   next_table [requests][max_blocks] int32 (not block_table): the tables with the new ids, -1 behind the complete blocks;
+ *   moves [max(1, num_blocks / 2)][2] int32: from, to; unused ones -1, -1.  Per layer, jetfp8_kv_move carries them out.
+ * num_blocks <= 2^18.  workspace: jetfp8_kv_sweep_workspace() bytes (0: none). */
+int jetfp8_kv_sweep(const int32_t* state, const int32_t* block_table, int64_t max_blocks, int64_t requests,
+                    int64_t num_blocks, int32_t* free_blocks, int32_t* free_head, int32_t* live, int32_t* next_table,
+                    int32_t* moves, void* workspace, int64_t workspace_bytes, void* stream);
+
+int64_t jetfp8_kv_sweep_workspace(int64_t requests, int64_t max_blocks, int64_t num_blocks);
+
+/* Copies of blocks in one layer's cache, codes and scales: moves [num_moves][2] int32, from and to.  No block may be the
+ * target of two moves or both a source and a target (jetfp8_kv_sweep's are in order); moves with an id outside 0 ..
+ * num_blocks - 1 are left out. */
+int jetfp8_kv_move(const int32_t* moves, int64_t num_moves, int64_t kv_heads, int64_t head_dim, uint8_t* codes,
+                   float* scales, int64_t num_blocks, void* stream);
+
+/* ---- Rotary positions ---------------------------------------------------------------------------------------- */
+
+typedef enum {                  /* the channels of pair i of a head's first 2 pairs channels */
+    JETFP8_ROTARY_HALVES = 0,       /* i and pairs + i */
+    JETFP8_ROTARY_INTERLEAVED = 1   /* 2 i and 2 i + 1 */
+} jetfp8_rotary_layout;
+
+/* Queries and keys turned by their tokens' positions, between the projection and jetfp8_kv_append.  Pair (a, b) number i
+ * of row t turns by the angle f = positions[t] * freqs[i]:
+ *   a' = amplitude * (a cos f - b sin f),   b' = amplitude * (b cos f + a sin f);
+ * inverse = 1: by -f, with the same amplitude, which is the backward pass.  Channels behind the pairs stay as they are, and
+ * so do rows whose position is negative (they are not written).  The angle is formed in fp64, the rest in fp32, rounded
+ * once.  x: bf16, row t at x + t * ldx elements, [heads][head_dim] contiguous within a row (queries and keys of a fused
+ * projection are one call); dst likewise at ldd.  dst may be x (ldd = ldx then).  head_dim % 16 == 0, at most 512;
+ * pairs % 8 == 0, 2 * pairs <= head_dim; ldx, ldd >= heads * head_dim and multiples of 8.  freqs [pairs] fp64, radians for
+ * each position.  0 < amplitude <= FLT_MAX (JETFP8_ERR_VALUE otherwise); an unknown layout is JETFP8_ERR_MODE. */
+int jetfp8_rotary(const void* x_bf16, int64_t ldx, int64_t tokens, int64_t heads, int64_t head_dim,
+                  const int32_t* positions, const double* freqs, int64_t pairs, int layout, float amplitude, int inverse,
+                  void* dst_bf16, int64_t ldd, void* stream);
+
+/* The positions of a step's rows from jetfp8_kv_plan's units in their order: positions [tokens] int32, -1 for rows of no
+ * unit.  tokens <= 2^19. */
+int jetfp8_kv_positions(const int32_t* units, int64_t num_units, int64_t tokens, int32_t* positions, void* stream);
 
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char* jetfp8_status_string(int status);
