@@ -668,14 +668,17 @@ def rmsnorm_add_quantize(x, residual, weight, eps: float, return_y: bool = False
     rstd [R], h [R, C]) of h = bf16(x + residual) and, with return_y, the normalized activation as well.  out: where h
     goes (x or residual for an update in place)."""
     torch = _torch_mod()
-    _need(x, x.shape, torch.bfloat16, "x")
     R, C = x.shape
     with _memory_of(stream, x.device):
         new = x.new_empty
         q, s, r = new((R, C), dtype=torch.uint8), new((C // 128, R), dtype=torch.float32), new((R,), dtype=torch.float32)
         h = new((R, C)) if out is None else out
         y = new((R, C)) if return_y else None
-    jetfp8_rmsnorm_add_quantize(x, residual, weight, R, C, eps, h, q, s, r, y, stream)
+    bf, dev = torch.bfloat16, x.get_device()
+    _call("jetfp8_rmsnorm_add_quantize", dev, stream, _use(x, (R, C), bf, "x"), _use(residual, (R, C), bf, "residual", dev),
+          _use(weight, (C,), bf, "weight", dev), R, C, float(eps),
+          h.data_ptr() if out is None else _use(out, (R, C), bf, "out", dev), q.data_ptr(), s.data_ptr(), r.data_ptr(),
+          y.data_ptr() if return_y else None)
     return (q, s, r, h, y) if return_y else (q, s, r, h)
 
 
@@ -734,11 +737,18 @@ def rotary(x, positions, freqs, interleaved: bool = False, amplitude: float = 1.
     [T], freqs fp64 [pairs] (rotary_frequencies) -> bf16 [T, heads, D], or `out` (x itself for an update in place; rows
     with a negative position are not written).  inverse: the backward pass."""
     T, H, D = x.shape
+    dev = x.get_device()
+    src = _rows(x, (T, H, D), "x", dev)
     if out is None:
         with _memory_of(stream, x.device):
             out = x.new_empty((T, H, D))
-    jetfp8_rotary(x, T, H, D, positions, freqs, ROTARY_INTERLEAVED if interleaved else ROTARY_HALVES, amplitude,
-                  1 if inverse else 0, out, stream)
+        dst = out.data_ptr(), H * D
+    else:
+        dst = _rows(out, (T, H, D), "out", dev)
+    P = freqs.shape[0]
+    _call("jetfp8_rotary", dev, stream, *src, T, H, D, _use(positions, (T,), _torch.int32, "positions", dev),
+          _use(freqs, (P,), _torch.float64, "freqs", dev), P, ROTARY_INTERLEAVED if interleaved else ROTARY_HALVES,
+          float(amplitude), 1 if inverse else 0, *dst)
     return out
 
 

@@ -48,7 +48,7 @@ bool attention_dims_ok(int64_t num_units, int64_t max_new, int64_t max_seq, int6
                        int64_t head_dim, bool prefix) {
     return dim_ok(num_units) && dim_ok(max_new) && dim_ok(max_seq) && dim_ok(q_heads) && dim_ok(kv_heads) &&
            q_heads % kv_heads == 0 && q_heads <= 65536 && (head_dim == 64 || head_dim == 128) &&
-           jetfp8::attention_fits(num_units, max_new, max_seq, q_heads, kv_heads, prefix);
+           jetfp8::attention_fits(num_units, max_new, max_seq, q_heads, kv_heads, head_dim, prefix);
 }
 
 bool table_ok(int64_t requests, int64_t max_blocks) {

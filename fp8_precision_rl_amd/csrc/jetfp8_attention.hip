@@ -205,7 +205,7 @@ template <int D>
 struct Raw {
     uint4 w[D / 16];
 };
-template <int R, bool VALUES, int D>
+template <int R, bool VALUES, bool KEEP, int D>
 __device__ __forceinline__ void load_raw(Raw<D>& r, const uint8_t* block, int lane) {
     typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
     constexpr int steps = VALUES ? 1 : D / 64, shares = R / 16;
@@ -213,7 +213,7 @@ __device__ __forceinline__ void load_raw(Raw<D>& r, const uint8_t* block, int la
     for (int i = 0; i < D / 16; ++i) {
         const int at = operand_at<R>(i / (steps * shares), i % (steps * shares), steps, lane);
         const u32x4* p = reinterpret_cast<const u32x4*>(block) + at;
-        const u32x4 x = R == 16 ? __builtin_nontemporal_load(p) : *p;
+        const u32x4 x = KEEP ? *p : __builtin_nontemporal_load(p);
         r.w[i] = make_uint4(x.x, x.y, x.z, x.w);
     }
 }
@@ -502,8 +502,9 @@ __device__ __forceinline__ const uint4* recent_block(const AttnArgs& a, int rece
 }
 
 // Takes cache blocks first .. last - 1 of a request, at most a span and at least one, into the rows' state, which is empty
-// before the first (whatever the registers hold).
-template <int D, int R>
+// before the first (whatever the registers hold).  The next block's codes are loaded while this one's are used; KEEP: they
+// are to be kept in the caches, since others read them too.
+template <int D, int R, bool KEEP>
 __device__ __forceinline__ void walk_span(State<D, R>& st, const typename State<D, R>::Queries& q, const AttnArgs& a,
                                           int request, int head, int first, int last, int lane) {
     typedef State<D, R> S;
@@ -513,8 +514,8 @@ __device__ __forceinline__ void walk_span(State<D, R>& st, const typename State<
     if (!(run.use & 1)) st.clear();
     Raw<D> kr, vr;
     const uint8_t* here = codes + __builtin_amdgcn_readlane(run.at, 0) * block_bytes;
-    load_raw<R, false>(kr, here, lane);
-    load_raw<R, true>(vr, here + kKvBlock * D, lane);
+    load_raw<R, false, KEEP>(kr, here, lane);
+    load_raw<R, true, KEEP>(vr, here + kKvBlock * D, lane);
 #pragma unroll
     for (int i = 0; i < kSpan; ++i) {
         if (first + i >= last) break;
@@ -531,7 +532,7 @@ __device__ __forceinline__ void walk_span(State<D, R>& st, const typename State<
                 s[t] = mfma(x, q[k], k ? s[t] : typename S::Acc{});
             }
         const bool more = i + 1 < kSpan && first + i + 1 < last;
-        if (more) load_raw<R, false>(kr, next, lane);
+        if (more) load_raw<R, false, KEEP>(kr, next, lane);
         if (run.use >> i & 1) {
             f16x8 p[2][S::kShares];
             const float c = lane_value(run.c, i), log_v = lane_value(run.log_v, i);
@@ -551,7 +552,7 @@ __device__ __forceinline__ void walk_span(State<D, R>& st, const typename State<
                         st.o[t] = mfma(x, p[h][g], i == 0 && h + g == 0 ? typename S::Acc{} : st.o[t]);
                     }
         }
-        if (more) load_raw<R, true>(vr, next + kKvBlock * D, lane);
+        if (more) load_raw<R, true, KEEP>(vr, next + kKvBlock * D, lane);
     }
 }
 
@@ -585,7 +586,8 @@ __global__ __launch_bounds__(kWaves * 64, R == 16 ? 3 : 2) void attention_span_k
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int head = blockIdx.x % a.kv_heads;
     const int jobs = a.parts * a.row_groups, chunks = (jobs + kWaves - 1) / kWaves;
-    const int unit = blockIdx.x / a.kv_heads / chunks, job = blockIdx.x / a.kv_heads % chunks * kWaves + wave;
+    const int unit = PREFIX ? blockIdx.x / a.kv_heads % a.num_units : blockIdx.x / a.kv_heads / chunks;
+    const int job = (PREFIX ? blockIdx.x / a.kv_heads / a.num_units : blockIdx.x / a.kv_heads % chunks) * kWaves + wave;
     if (job >= jobs) return;
     const int row0 = job % a.row_groups * R;
     const KvUnit u = a.units[unit];
@@ -601,14 +603,18 @@ __global__ __launch_bounds__(kWaves * 64, R == 16 ? 3 : 2) void attention_span_k
     float factor = 1.0f;
     if (span == own) {
         const uint4* mem = recent_block<D>(a, u.recent, head);
-        uint4 v[S::kOut][2][S::kShares];           // loaded before the scores are formed
+        // loaded before the scores are formed; the second half of the keys only if a row reaches it, as own_block has it
+        const bool both = u.offset + (row0 + R - 1) / a.group >= 32;
+        uint4 v[S::kOut][2][S::kShares];
 #pragma unroll
         for (int t = 0; t < S::kOut; ++t)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int g = 0; g < S::kShares; ++g)
-                    v[t][h][g] = mem[kKvBlock * D / 8 + operand_at<R>(t, h * S::kShares + g, 2, lane)];
+                for (int g = 0; g < S::kShares; ++g) {
+                    v[t][h][g] = make_uint4(0, 0, 0, 0);
+                    if (!h || both) v[t][h][g] = mem[kKvBlock * D / 8 + operand_at<R>(t, h * S::kShares + g, 2, lane)];
+                }
         own_block<D, R>(
             st, q, a.scale_log2, u.offset, a.group, row0, lane,
             [&](int t, int k) { return __builtin_bit_cast(bf16x8, mem[operand_at<R>(t, k, D / 32, lane)]); },
@@ -622,7 +628,7 @@ __global__ __launch_bounds__(kWaves * 64, R == 16 ? 3 : 2) void attention_span_k
             });
     } else {
         const int first = span * kSpan;
-        walk_span<D, R>(st, q, a, u.request, head, first, min(first + kSpan, u.block), lane);
+        walk_span<D, R, R == 32 || PREFIX>(st, q, a, u.request, head, first, min(first + kSpan, u.block), lane);
         factor = st.factor();
     }
     store_part<D, R>(st.top, st.sum(), st.o, factor, a, unit, head, span, row0 + lane % R, rows, lane);
@@ -630,59 +636,114 @@ __global__ __launch_bounds__(kWaves * 64, R == 16 ? 3 : 2) void attention_span_k
 
 // attention_prefix_kernel takes the blocks that the requests of a group share, in the rows of all its units at once: row g
 // of the group is row g % max_rows of its unit g / max_rows, and 32 of them are a wave's, whatever units they belong to.
-// The units' own records say which group; a thread block is that of the unit whose rows the tile of 32 begins with.
-// It takes a run of 8 spans, two of them by each wave, and joins them in order as the other kernels do, so that one
-// partial result of a run is written instead of eight: in the place of the run's last shared span.
+// A piece of work is such a tile of rows and a run of 8 spans: eight waves take a span each and join them in order as the other
+// kernels do, so that one partial result of a run is written instead of eight, in the place of the run's last shared span.
+//
+// How many pieces there are is known from the units' records only, so a fixed number of thread blocks, as many as fit the
+// chip, count them and take them in turn.  (With a thread block for every piece that the sizes allow, most of which find
+// nothing to do, the empty ones delayed the others: 16 samples of 16 prompts up to 8192 89 us instead of 59.)
+//
+// Bound by the arithmetic of 32 rows to a wave once a group has more rows than that, by HBM below (us for 8 kv heads of 128,
+// 4 query heads each, and prompts of 4096 to 8192 tokens: 16 prompts of 8 samples 41, which is 4.9 TB/s of codes; of 16
+// samples 59; of 32 samples 96; all with four waves that take two spans each, 3 to 10 % slower than eight).  What was tried
+// instead, at 16 samples: the next blocks' codes by way of LDS, so that two blocks are on the way, 59; a stage in LDS that two
+// waves share, 115; 64 rows to a wave, 108.
+constexpr int kPrefixWaves = kRun;
+struct PrefixUnit {
+    int4 group;                // its record; no shared blocks if the record does not fit
+    int first_tile, tiles, runs;
+};
+
+__device__ __forceinline__ PrefixUnit prefix_unit(const AttnArgs& a, int unit) {
+    PrefixUnit p;
+    p.group = a.prefix[unit];
+    const int rank = unit - p.group.x;
+    const bool fits = p.group.x >= 0 && rank >= 0 && rank < p.group.y && p.group.y <= a.num_units - p.group.x &&
+                      p.group.z <= a.max_blocks;
+    p.runs = fits ? max((p.group.z / kSpan + kRun - 1) / kRun, 0) : 0;
+    // tiles of the group that begin in this unit's rows
+    p.first_tile = fits ? (rank * a.max_rows + 31) / 32 : 0;
+    p.tiles = p.runs > 0 ? ((rank + 1) * a.max_rows + 31) / 32 - p.first_tile : 0;
+    return p;
+}
+
 template <int D>
-__global__ __launch_bounds__(kWaves * 64, 2) void attention_prefix_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kPrefixWaves * 64, 2) void attention_prefix_kernel(AttnArgs a) {
     typedef State<D, 32> S;
-    constexpr int kQuads = D / 4, kMine = kQuads / 2 / kWaves;       // 4 channels each: of a row, and of a lane to join
-    __shared__ v4f part_o[kWaves][kQuads][32];
-    __shared__ float2 part_ml[kWaves][32];
+    constexpr int kQuads = D / 4, kMine = kQuads / 2 / kPrefixWaves;       // 4 channels each: of a row, and of a lane to join
+    __shared__ v4f part_o[kPrefixWaves][kQuads][32];
+    __shared__ float2 part_ml[kPrefixWaves][32];
+    __shared__ int upto[kPrefixWaves * 64], found[5];                // pieces of the units up to a thread's last
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    const int head = blockIdx.x % a.kv_heads;
-    int job = blockIdx.x / a.kv_heads;
-    const int run = job % a.runs;
-    job /= a.runs;
-    const int unit = job / a.row_groups;
-    const int4 group = a.prefix[unit];
-    const int rank = unit - group.x, shared = group.z / kSpan;       // spans
-    if (group.x < 0 || rank < 0 || rank >= group.y || group.y > a.num_units - group.x || shared <= run * kRun ||
-        group.z > a.max_blocks)
-        return;
-    const int row0 = ((rank * a.max_rows + 31) / 32 + job % a.row_groups) * 32;
-    if (row0 >= (rank + 1) * a.max_rows) return;
-    const int request = a.units[group.x].request;
-    if (request < 0 || request >= a.requests) return;
-    const int spans = min(shared - run * kRun, kRun);                // of this run
-
-    // this lane's row
-    const int row = row0 + lane % 32, member = row / a.max_rows, local = row % a.max_rows;
-    const int mine = group.x + min(member, group.y - 1);
-    const KvUnit u = a.units[mine];
-    const int rows = u.rows * a.group;
-    const bool live = member < group.y && unit_fits(u, a.requests, a.tokens, a.recent_blocks, a.num_blocks) && local < rows &&
-                      rows <= a.max_rows && u.block <= a.max_blocks && u.block >= group.z;
-    typename S::Queries q;
-    const uint16_t* p = a.q + (live ? (u.row + local / a.group) * a.ldq + ((int64_t)head * a.group + local % a.group) * D : 0) +
-                        lane / 32 * 8;
-#pragma unroll
-    for (int k = 0; k < S::kSteps; ++k) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (live) x = *reinterpret_cast<const uint4*>(p + k * 16);
-        q[k] = __builtin_bit_cast(bf16x8, x);
+    const int each = (a.num_units + kPrefixWaves * 64 - 1) / (kPrefixWaves * 64), from = threadIdx.x * each;
+    int pieces = 0;
+    for (int i = from; i < min(from + each, a.num_units); ++i) {
+        const PrefixUnit p = prefix_unit(a, i);
+        pieces += p.tiles * p.runs;
     }
-
-    float M = -INFINITY, L = 0.0f;
-    v4f o[kMine];
+    int sum = pieces;
 #pragma unroll
-    for (int i = 0; i < kMine; ++i) o[i] = v4f{};
-    for (int s0 = 0; s0 < spans; s0 += kWaves) {
-        if (s0) __syncthreads();
-        if (s0 + wave < spans) {
+    for (int d = 1; d < 64; d *= 2) {
+        const int y = __shfl_up(sum, d);
+        if (lane >= d) sum += y;
+    }
+    upto[threadIdx.x] = sum;
+    __syncthreads();
+    int base = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < kPrefixWaves; ++w) {
+        if (w < wave) base += upto[w * 64 + 63];
+        total += upto[w * 64 + 63];
+    }
+    const int64_t all = (int64_t)total * a.kv_heads;
+    for (int64_t job = blockIdx.x; job < all; job += gridDim.x) {
+        const int head = job % a.kv_heads;
+        int left = (int)(job / a.kv_heads) - (base + sum - pieces);
+        __syncthreads();
+        // the thread whose units have the piece tells the others
+        if (left >= 0 && left < pieces) {
+            for (int i = from;; ++i) {
+                const PrefixUnit p = prefix_unit(a, i);
+                if (left < p.tiles * p.runs) {
+                    found[0] = p.group.x;
+                    found[1] = p.group.y;
+                    found[2] = p.group.z;
+                    found[3] = p.first_tile + left / p.runs;
+                    found[4] = left % p.runs;
+                    break;
+                }
+                left -= p.tiles * p.runs;
+            }
+        }
+        __syncthreads();
+        const int first_unit = __builtin_amdgcn_readfirstlane(found[0]), units = __builtin_amdgcn_readfirstlane(found[1]);
+        const int shared = __builtin_amdgcn_readfirstlane(found[2]);
+        const int tile = __builtin_amdgcn_readfirstlane(found[3]), run = __builtin_amdgcn_readfirstlane(found[4]);
+        const int request = a.units[first_unit].request;
+        if (request < 0 || request >= a.requests) continue;
+        const int spans = min(shared / kSpan - run * kRun, kRun);        // of this run
+
+        // this lane's row
+        const int row = tile * 32 + lane % 32, member = row / a.max_rows, local = row % a.max_rows;
+        const int mine = first_unit + min(member, units - 1);
+        const KvUnit u = a.units[mine];
+        const int rows = u.rows * a.group;
+        const bool live = member < units && unit_fits(u, a.requests, a.tokens, a.recent_blocks, a.num_blocks) &&
+                          local < rows && rows <= a.max_rows && u.block <= a.max_blocks && u.block >= shared;
+        typename S::Queries q;
+        const uint16_t* p =
+            a.q + (live ? (u.row + local / a.group) * a.ldq + ((int64_t)head * a.group + local % a.group) * D : 0) + lane / 32 * 8;
+#pragma unroll
+        for (int k = 0; k < S::kSteps; ++k) {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (live) x = *reinterpret_cast<const uint4*>(p + k * 16);
+            q[k] = __builtin_bit_cast(bf16x8, x);
+        }
+
+        if (wave < spans) {
             S st;
-            const int first = (run * kRun + s0 + wave) * kSpan;
-            walk_span<D, 32>(st, q, a, request, head, first, first + kSpan, lane);
+            const int first = (run * kRun + wave) * kSpan;
+            walk_span<D, 32, true>(st, q, a, request, head, first, first + kSpan, lane);
             const float factor = st.factor(), l = st.sum();
 #pragma unroll
             for (int t = 0; t < S::kOut; ++t)
@@ -693,8 +754,11 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attention_prefix_kernel(AttnAr
             if (lane < 32) part_ml[wave][lane] = make_float2(st.top, l);
         }
         __syncthreads();
-        const int n = min(spans - s0, kWaves);
-        for (int s = 0; s < n; ++s) {
+        float M = -INFINITY, L = 0.0f;
+        v4f o[kMine];
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) o[i] = v4f{};
+        for (int s = 0; s < spans; ++s) {
             const float2 ml = part_ml[s][lane % 32];
             float x, y;
             join_factors(M, ml.x, x, y);
@@ -706,13 +770,14 @@ __global__ __launch_bounds__(kWaves * 64, 2) void attention_prefix_kernel(AttnAr
                 for (int c = 0; c < 4; ++c) o[i][c] = fmaf(o[i][c], x, v[c] * y);
             }
         }
-    }
-    if (!live) return;
-    const int64_t at = (((int64_t)mine * a.kv_heads + head) * a.parts + run * kRun + spans - 1) * a.max_rows + local;
+        if (live) {
+            const int64_t at = (((int64_t)mine * a.kv_heads + head) * a.parts + run * kRun + spans - 1) * a.max_rows + local;
 #pragma unroll
-    for (int i = 0; i < kMine; ++i)
-        *reinterpret_cast<v4f*>(a.part_o + at * D + (wave * kMine + i) * 8 + lane / 32 * 4) = o[i];
-    if (wave == 0 && lane < 32) a.part_ml[at] = make_float2(M, L);
+            for (int i = 0; i < kMine; ++i)
+                *reinterpret_cast<v4f*>(a.part_o + at * D + (wave * kMine + i) * 8 + lane / 32 * 4) = o[i];
+            if (wave == 0 && lane < 32) a.part_ml[at] = make_float2(M, L);
+        }
+    }
 }
 
 // The pair of units that stands at place x if all are ordered by the blocks that precede them, most first (64 classes;
@@ -1127,7 +1192,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
 struct AttnShape {
     int64_t max_rows, row_groups, runs, parts, max_blocks;
     int rows;                       // of a wave
-    bool split;
+    bool split, prefix;
 };
 
 // Waves of 32 rows.
@@ -1135,7 +1200,8 @@ double attn_waves(const AttnShape& s, int64_t num_units, int64_t kv_heads) {
     return (double)num_units * kv_heads * ((s.max_rows + 31) / 32);
 }
 
-AttnShape attn_shape(int64_t num_units, int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads, bool prefix) {
+AttnShape attn_shape(int64_t num_units, int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads, int64_t D,
+                     bool prefix) {
     AttnShape s;
     s.max_rows = (max_new < kKvBlock ? max_new : kKvBlock) * (q_heads / kv_heads);
     s.max_blocks = (max_seq - 1) / kKvBlock;
@@ -1145,7 +1211,15 @@ AttnShape attn_shape(int64_t num_units, int64_t max_new, int64_t max_seq, int64_
     // the tile kernel if that has enough waves (32 rows each) for the chip's 1024 SIMDs: below, spans in parallel win (256
     // tokens at 4096, 320 waves: 54 against 106 us), at 1072 and 1472 waves the two are within 5 %, above the
     // partial results cost more than they bring (16 times 64 tokens at 4096, 3008 waves: 157 against 109 us).
-    s.split = spans > 0 && (prefix || s.max_rows <= 16 || attn_waves(s, num_units, kv_heads) < 1024);
+    // Shared blocks are taken apart where the call may read more than the last level of cache holds, 256 MB; below, it finds
+    // them there, and waiting for one kernel after the other costs more than it saves (8 kv heads of 128, us apart against
+    // not: 8 samples at 2300 25 / 12, 32 samples at 8700 36 / 58, 32 requests at 4600 34 / 26, 64 requests at 2500 34 / 39, 256
+    // requests at 9200 146 / 421).  And where a unit's rows do not fill the 32 of a wave several times by themselves (8
+    // query heads each, 128 requests at 8700: 2 tokens 128 / 240, 4 tokens 256 / 386; 2 prompts of 16 samples, 16 tokens 132 / 156,
+    // with partial results of twice the size).
+    s.prefix = prefix && s.max_rows <= 32 &&
+               (double)num_units * kv_heads * s.max_blocks * (2 * kKvBlock) * D >= (double)(1 << 28);
+    s.split = spans > 0 && (s.prefix || s.max_rows <= 16 || attn_waves(s, num_units, kv_heads) < 1024);
     s.rows = s.split && s.max_rows <= 16 ? 16 : 32;
     s.row_groups = (s.max_rows + s.rows - 1) / s.rows;
     s.parts = s.split ? spans + 1 : s.runs > 1 ? s.runs + 1 : 0;
@@ -1166,9 +1240,7 @@ double attn_blocks(const AttnShape& s, int64_t num_units, int64_t kv_heads) {
 template <int D, bool PREFIX>
 hipError_t launch(const AttnArgs& a, const AttnShape& s, unsigned grid, hipStream_t st) {
     if (PREFIX) {
-        // (no more thread blocks than the grid that attention_fits looks at)
-        const int64_t blocks = (int64_t)a.num_units * a.kv_heads * s.runs * s.row_groups;
-        attention_prefix_kernel<D><<<(unsigned)blocks, kWaves * 64, 0, st>>>(a);
+        attention_prefix_kernel<D><<<(unsigned)device_cu_count(), kPrefixWaves * 64, 0, st>>>(a);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
@@ -1191,12 +1263,13 @@ hipError_t launch(const AttnArgs& a, const AttnShape& s, unsigned grid, hipStrea
 
 int64_t attention_workspace(int64_t num_units, int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads,
                             int64_t D, bool prefix) {
-    return partial_rows(attn_shape(num_units, max_new, max_seq, q_heads, kv_heads, prefix), num_units, kv_heads) * (D + 2) *
+    return partial_rows(attn_shape(num_units, max_new, max_seq, q_heads, kv_heads, D, prefix), num_units, kv_heads) * (D + 2) *
            (int64_t)sizeof(float);
 }
 
-bool attention_fits(int64_t num_units, int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads, bool prefix) {
-    const AttnShape s = attn_shape(num_units, max_new, max_seq, q_heads, kv_heads, prefix);
+bool attention_fits(int64_t num_units, int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads, int64_t D,
+                    bool prefix) {
+    const AttnShape s = attn_shape(num_units, max_new, max_seq, q_heads, kv_heads, D, prefix);
     const double join = s.parts ? (double)num_units * kv_heads * s.max_rows / 4 : 0.0;      // its thread blocks, nearly
     return attn_blocks(s, num_units, kv_heads) < kKvMaxGrid && join < kKvMaxGrid - 1 &&
            (double)num_units * kv_heads * s.max_rows <= INT32_MAX;
@@ -1208,7 +1281,7 @@ hipError_t launch_attention(const uint16_t* q, int64_t ldq, int64_t tokens, cons
                             int64_t recent_blocks, int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads,
                             int64_t D, float softmax_scale, uint16_t* o, uint8_t* oq, float* os, float* workspace,
                             hipStream_t st) {
-    const AttnShape s = attn_shape(num_units, max_new, max_seq, q_heads, kv_heads, prefix != nullptr);
+    const AttnShape s = attn_shape(num_units, max_new, max_seq, q_heads, kv_heads, D, prefix != nullptr);
     AttnArgs a;
     a.q = q;
     a.units = reinterpret_cast<const KvUnit*>(units);
@@ -1243,7 +1316,7 @@ hipError_t launch_attention(const uint16_t* q, int64_t ldq, int64_t tokens, cons
     // at 17344 344 -> 360, at 31840 405 -> 428.
     a.ordered = requests > 1 && s.max_blocks > 0 && num_units <= 2 * 256 * kOrder && attn_waves(s, num_units, kv_heads) < 12288;
     const unsigned grid = (unsigned)attn_blocks(s, num_units, kv_heads);
-    if (prefix && s.split) return D == 64 ? launch<64, true>(a, s, grid, st) : launch<128, true>(a, s, grid, st);
+    if (s.prefix) return D == 64 ? launch<64, true>(a, s, grid, st) : launch<128, true>(a, s, grid, st);
     return D == 64 ? launch<64, false>(a, s, grid, st) : launch<128, false>(a, s, grid, st);
 }
 

@@ -72,7 +72,8 @@ hipError_t launch_kv_append(const uint16_t* k, int64_t ldk, const uint16_t* v, i
 // Bytes of workspace, and whether the launch grids hold the call.  prefix: with records of the blocks that units share.
 int64_t attention_workspace(int64_t num_units, int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads,
                             int64_t D, bool prefix);
-bool attention_fits(int64_t num_units, int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads, bool prefix);
+bool attention_fits(int64_t num_units, int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads, int64_t D,
+                    bool prefix);
 hipError_t launch_attention(const uint16_t* q, int64_t ldq, int64_t tokens, const int32_t* units, int64_t num_units,
                             const int32_t* prefix, const int32_t* table, int64_t requests, int64_t width,
                             const uint8_t* codes, const float* scales, int64_t num_blocks, const uint16_t* recent,

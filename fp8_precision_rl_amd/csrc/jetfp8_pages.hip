@@ -334,10 +334,11 @@ __global__ __launch_bounds__(kThreads) void kv_move_kernel(const int2* __restric
     if (threadIdx.x < 2) scales[2 * t + threadIdx.x] = scales[2 * s + threadIdx.x];
 }
 
-// Copies of the marks: one for about every 4096 table entries.  With one, every thread block of the second kernel marks
-// the tables for itself and there is no first.
+// Copies of the marks: one for as many table entries as a thread block has on the way at once.  With one, every thread block
+// of the second kernel marks the tables for itself and there is no first.
 int64_t sweep_copies(int64_t requests, int64_t width) {
-    const int64_t n = (requests * width + 4095) / 4096;
+    constexpr int64_t share = kMarkBatch * kSweepThreads;
+    const int64_t n = (requests * width + share - 1) / share;
     return n < 64 ? n : 64;
 }
 
