@@ -94,7 +94,7 @@ __global__ __launch_bounds__(WPR * TEAMS * 64) void rmsnorm_backward_kernel(Norm
 #pragma unroll
             for (int p = 1; p < WPR; ++p) sum += sums[buf][team][p];
         }
-        const float c = r * r * (sum * inv_cols);
+        const float c = r * (r * (sum * inv_cols));       // (r * r may underflow)
 #pragma unroll
         for (int k = 0; k < HCH; ++k) {
             const uint32_t y[4] = {dy[k].x, dy[k].y, dy[k].z, dy[k].w}, x[4] = {h[k].x, h[k].y, h[k].z, h[k].w},

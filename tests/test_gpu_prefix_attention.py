@@ -1,0 +1,298 @@
+"""The attention of samples that share a prompt: bit for bit that of jetfp8_attention on the same step, which other tests hold
+to the oracle, and here against the oracle too.  A call takes the shared blocks apart only where it may read 256 MB or more;
+max_seq only bounds the lengths, so small caches take that path with a large one."""
+import numpy as np
+import pytest
+
+from kv_case import check_rows
+from oracle import kvcache as kc
+from oracle import rollout as ro
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def jf():
+    import torch
+    import fp8_precision_rl_amd as m
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    m.load_library()
+    return m
+
+
+def up(a):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+class Case:
+    """Groups of requests over a random cache: (prompt tokens, samples) each, samples with up to `grown` tokens of their own
+    and `new` new ones, some of them idle."""
+
+    def __init__(self, groups, grown, new, Hq, H, D, idle=0.0, seed=0):
+        import torch
+        rng = np.random.default_rng(seed)
+        self.rng, self.new, self.Hq, self.H, self.D = rng, new, Hq, H, D
+        ctx, ids = [], []
+        for g, (prompt, n) in enumerate(groups):
+            ctx += [prompt + int(rng.integers(0, grown + 1)) for _ in range(n)]
+            ids += [g] * n
+        R = len(ctx)
+        lens = np.where(rng.random(R) < idle, 0, rng.integers(1, new + 1, R)).astype(np.int32)
+        lens[0] = max(lens[0], 1)
+        state = np.stack([ctx, rng.integers(0, 2, R)], 1).astype(np.int32)
+        held, ends = state[:, 0] // 64, (state[:, 0] + lens) // 64
+        width = int(ends.max()) + 2
+        table = np.full((R, width), -1, np.int32)
+        blocks = int(ends.sum()) + 5
+        order = rng.permutation(blocks).astype(np.int32)
+        at, r = 0, 0
+        for prompt, n in groups:
+            common = prompt // 64
+            table[r:r + n, :common] = order[at:at + common]
+            at += common
+            for q in range(r, r + n):
+                k = held[q] - common
+                table[q, common:held[q]] = order[at:at + k]
+                at += k
+            r += n
+        self.pad = 3
+        self.T = int(lens.sum()) + self.pad
+        self.plan = kc.plan(state, lens, order[at:], 0, table, self.T, new)
+        assert not self.plan["status"].any()
+        self.groups = np.array(ids, np.int32)
+        self.R = R
+        n = (H, 2, 64 * D)
+        codes = rng.integers(0, 254, (blocks,) + n).astype(np.uint8)
+        self.codes = np.where(codes >= 127, codes + 1, codes).astype(np.uint8)                   # without 0x7F and 0xFF
+        self.scales = np.exp2(rng.uniform(-9, -5, (blocks,) + n[:2])).astype(np.float32)
+        g = torch.Generator(device="cuda")
+        g.manual_seed(seed)
+        self.recent = torch.randn((2 * R + self.T // 64,) + n, device="cuda", generator=g).to(torch.bfloat16)
+        self.q = torch.randn((self.T, (Hq + 2) * D), device="cuda", generator=g).to(torch.bfloat16)[:, D:(Hq + 1) * D]
+        self.q = self.q.unflatten(1, (Hq, D))
+        self.units, self.table = up(self.plan["units"]), up(self.plan["table"])
+        self.dcodes, self.dscales = up(self.codes), up(self.scales)
+        self.max_seq = int(self.plan["next_state"][:, 0].max())
+
+    def far(self):
+        """A max_seq with which the call may read 256 MB."""
+        return max(self.max_seq, 64 * (-(-(1 << 28) // (len(self.units) * self.H * 128 * self.D))) + 1)
+
+    def args(self):
+        return self.units, self.table, self.dcodes, self.dscales, self.recent
+
+    def prefix(self, jf):
+        got = jf.kv_prefix(self.units, self.table, up(self.groups))
+        assert np.array_equal(got.cpu().numpy(), ro.prefix(self.plan["units"], self.plan["table"], self.groups))
+        return got
+
+    def run(self, jf, prefix, max_seq, quantize=False):
+        """Output bits with rows of no unit 7, over a workspace of NaN."""
+        import torch
+        u, t, c, s, r = self.args()
+        o = torch.full((self.T, self.Hq, self.D), 7.0, dtype=torch.bfloat16, device="cuda")
+        need = jf.attention_workspace(len(u), self.new, max_seq, self.Hq, self.H, self.D, prefix is not None)
+        ws = torch.full((max(need, 16) + 256,), 255, dtype=torch.uint8, device="cuda")
+        codes = scales = None
+        if quantize:
+            codes = torch.full((self.T, self.Hq * 128), 9, dtype=torch.uint8, device="cuda")
+            scales = torch.full((self.Hq, self.T), 9.0, device="cuda")
+        rest = (t, c, s, r, self.T, self.new, max_seq, self.Hq, self.H, self.D, self.D ** -0.5, o, codes, scales)
+        if prefix is None:
+            jf.jetfp8_attention(self.q, u, *rest, workspace=ws[:max(need, 16)])
+        else:
+            jf.jetfp8_attention_prefix(self.q, u, prefix, *rest, workspace=ws[:max(need, 16)])
+        assert (ws[max(need, 16):] == 255).all()
+        return (o, codes, scales) if quantize else o
+
+
+def same(a, b):
+    import torch
+    d = (a.view(torch.int16) != b.view(torch.int16)).flatten(1).any(1)
+    assert not d.any(), f"rows {d.nonzero().flatten()[:8].tolist()} differ"
+
+
+GROUPS = {
+    "none long enough": [(300, 3), (511, 2)],
+    "one span": [(512, 2), (575, 5)],
+    "two and a bit": [(1024, 9), (1100, 33)],
+    "one run": [(4096, 4)],
+    "run and span": [(4608, 17), (600, 1), (4650, 2)],
+    "several runs": [(9000, 6), (64, 2), (8192, 12)],
+}
+
+
+@pytest.mark.parametrize("Hq,H,D", [(4, 1, 128), (8, 8, 64), (10, 2, 128), (16, 1, 64), (24, 8, 128), (32, 1, 64)])
+@pytest.mark.parametrize("groups", GROUPS)
+def test_bits_of_the_plain_attention(jf, groups, Hq, H, D):
+    """Single tokens."""
+    import torch
+    c = Case(GROUPS[groups], 200, 1, Hq, H, D, seed=Hq + D)
+    pre = c.prefix(jf)
+    assert (groups == "none long enough") == (int(pre[:, 2].max()) == 0)
+    plain = c.run(jf, None, c.max_seq)
+    assert torch.isfinite(plain).all()
+    for max_seq in (c.max_seq, c.far()):
+        same(c.run(jf, pre, max_seq), plain)
+    assert (plain[c.T - c.pad:] == 7.0).all()
+
+
+@pytest.mark.parametrize("Hq,H,D,new", [(4, 1, 128, 3), (8, 2, 64, 8), (5, 1, 128, 6), (14, 2, 64, 70), (32, 4, 128, 4), (8, 1, 128, 5)])
+def test_several_tokens_and_idle_requests(jf, Hq, H, D, new):
+    """Chunks that cross blocks, units of one request one after the other, requests without new tokens, rows that do and do
+    not divide the 32 of a wave, and more rows than are taken apart."""
+    c = Case([(700, 5), (1200, 20), (4200, 9), (520, 2)], 300, new, Hq, H, D, idle=0.3, seed=new)
+    pre = c.prefix(jf)
+    plain = c.run(jf, None, c.max_seq)
+    for max_seq in (c.max_seq, c.far()):
+        same(c.run(jf, pre, max_seq), plain)
+
+
+@pytest.mark.parametrize("Hq,H,D", [(4, 2, 64), (6, 2, 128)])
+def test_against_the_oracle(jf, Hq, H, D):
+    import torch
+    c = Case([(600, 3), (1050, 4)], 90, 2, Hq, H, D, idle=0.2, seed=4)
+    o = c.run(jf, c.prefix(jf), c.far())
+    bits = lambda t: t.contiguous().view(torch.int16).cpu().numpy().view(np.uint16)
+    want, bound = kc.attention(kc.bf16(bits(c.q)), c.plan["units"], c.plan["table"], c.codes, c.scales, bits(c.recent),
+                               np.float64(np.float32(D ** -0.5)))
+    check_rows(kc.bf16(bits(o)), want, bound)
+
+
+def test_codes(jf):
+    """The fused codes are those of the plain call."""
+    import torch
+    c = Case([(1300, 20), (5000, 3)], 100, 2, 8, 2, 128, seed=9)
+    plain, got = c.run(jf, None, c.max_seq, True), c.run(jf, c.prefix(jf), c.far(), True)
+    for a, b in zip(plain, got):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+def test_ids_of_no_block_and_zero_scales(jf):
+    """Ids out of range in the shared part read as blocks without keys, and values of scale 0 as zeros, as in the plain call;
+    also where a whole span, or all that is shared, has no keys."""
+    c = Case([(1100, 6), (1200, 5), (5200, 4)], 60, 1, 4, 2, 128, seed=3)
+    t = c.plan["table"].copy()
+    t[0:6, 2] = -1
+    t[0:6, 8:16] = 1 << 30
+    t[6:11, :18] = -7
+    t[11:, 0] = 2 ** 31 - 1
+    t[11:, 64:72] = -1
+    c.plan["table"], c.table = t, up(t)
+    c.dscales[::3, :, 1] = 0
+    c.dscales[1::3, :, 0] = 0
+    pre = c.prefix(jf)
+    plain = c.run(jf, None, c.max_seq)
+    same(c.run(jf, pre, c.far()), plain)
+
+
+def test_values_of_every_size(jf):
+    """Scales over 2^+-30 and infinities and NaN in the unfinished blocks, in places that no row may see and in some that do."""
+    c = Case([(1100, 6), (700, 9)], 60, 1, 4, 2, 128, seed=5)
+    c.dscales[:, :, 1] = up(np.exp2(c.rng.uniform(-30, 30, c.scales.shape[:2])).astype(np.float32))
+    pre = c.prefix(jf)
+    same(c.run(jf, pre, c.far()), c.run(jf, None, c.max_seq))
+    r = c.recent.view(c.recent.shape[0], -1)
+    r[::2, ::97] = float("nan")
+    r[1::2, 5::89] = float("inf")
+    import torch
+    plain, got = c.run(jf, None, c.max_seq), c.run(jf, pre, c.far())
+    assert torch.equal(plain.isnan(), got.isnan())
+    same(torch.nan_to_num(got), torch.nan_to_num(plain))
+
+
+def test_records_of_other_units(jf):
+    """Records that do not belong to the units stay within the buffers: rows of no unit and the bytes behind the workspace keep
+    their values (checked by run), and rows whose units have sound records keep their results."""
+    import torch
+    c = Case([(1100, 8), (4200, 9)], 100, 1, 4, 2, 128, seed=7)
+    pre = c.prefix(jf)
+    plain = c.run(jf, None, c.max_seq)
+    rng = np.random.default_rng(1)
+    for kind in range(6):
+        bad = pre.cpu().numpy().copy()
+        if kind == 0:
+            bad = np.roll(bad, 3, 0)
+        elif kind == 1:
+            bad[:8, 0] += 5
+        elif kind == 2:
+            bad[:8, 2] = 1 << 30
+        elif kind == 3:
+            bad[:8, 1] = 2 ** 31 - 1
+        elif kind == 4:
+            bad[:8] = rng.integers(-2 ** 31, 2 ** 31, (8, 4))
+        else:
+            bad[:8, 2] = -64
+        got = c.run(jf, up(bad.astype(np.int32)), c.far())
+        assert (got[c.T - c.pad:] == 7.0).all()
+        if kind in (2, 4):                       # the second group's records are as they were
+            same(got[8:], plain[8:])
+
+
+def test_streams_and_graphs(jf):
+    """Two calls at once with workspaces of their own, and a captured step: records and attention replayed for other lengths."""
+    import torch
+    c = Case([(1100, 8), (4200, 9), (600, 3)], 100, 1, 4, 2, 128, seed=8)
+    d = Case([(600, 9), (1500, 5), (4700, 6)], 100, 1, 4, 2, 128, seed=8)
+    assert c.T == d.T and len(c.units) == len(d.units)
+    width, blocks = max(c.table.shape[1], d.table.shape[1]), max(len(c.codes), len(d.codes))
+    far = max(c.far(), d.far())
+    pad = lambda x, n, v=0: torch.cat([x, x.new_full((n - x.shape[0],) + x.shape[1:], v)])
+    wide = lambda t: torch.cat([t, t.new_full((t.shape[0], width - t.shape[1]), -1)], 1)
+    both = [dict(units=x.units, table=wide(x.table), codes=pad(x.dcodes, blocks), scales=pad(x.dscales, blocks),
+                 recent=x.recent, q=x.q.contiguous(), groups=up(x.groups), plain=x.run(jf, None, x.max_seq)) for x in (c, d)]
+    s = {k: v.clone() for k, v in both[0].items()}
+    size = jf.attention_workspace(len(c.units), 1, far, 4, 2, 128, True)
+
+    def call(ws, stream=None):
+        pre = jf.kv_prefix(s["units"], s["table"], s["groups"], stream=stream)
+        return jf.attention(s["q"], s["units"], s["table"], s["codes"], s["scales"], s["recent"], 1, far, prefix=pre,
+                            workspace=ws, stream=stream)
+
+    rows = c.T - c.pad
+    streams, space = [torch.cuda.Stream() for _ in range(2)], [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    torch.cuda.synchronize()
+    outs = [call(space[i], streams[i]) for i in range(2)]
+    torch.cuda.synchronize()
+    for o in outs:
+        same(o[:rows], both[0]["plain"][:rows])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o = call(space[2])
+    for n in (1, 0, 1):
+        for k, v in both[n].items():
+            s[k].copy_(v)
+        space[2].fill_(255)
+        graph.replay()
+        torch.cuda.synchronize()
+        same(o[:rows], both[n]["plain"][:rows])
+
+
+def test_a_part_of_the_units(jf):
+    """Records go with all of a plan's units; records of single units make the plain call of any part of them."""
+    import torch
+    c = Case([(1100, 8), (600, 3)], 100, 1, 4, 2, 128, seed=2)
+    plain = c.run(jf, None, c.max_seq)
+    u = c.units[3:9].contiguous()
+    alone = torch.tensor([[i, 1, 0, 0] for i in range(6)], dtype=torch.int32, device="cuda")
+    o = torch.full_like(plain, 7.0)
+    far = 64 * ((1 << 28) // (6 * 2 * 128 * 128)) + 65
+    ws = torch.empty(jf.attention_workspace(6, 1, far, 4, 2, 128, True), dtype=torch.uint8, device="cuda")
+    jf.jetfp8_attention_prefix(c.q, u, alone, c.table, c.dcodes, c.dscales, c.recent, c.T, 1, far, 4, 2, 128, 128 ** -0.5, o,
+                               workspace=ws)
+    same(o[3:9], plain[3:9])
+    assert (o[:3] == 7.0).all() and (o[9:] == 7.0).all()
+
+
+def test_binding_refusals(jf):
+    import torch
+    c = Case([(600, 3)], 10, 1, 4, 2, 128)
+    pre = c.prefix(jf)
+    for bad in (pre[:1], pre.view(-1), pre.long()):
+        with pytest.raises((ValueError, TypeError)):
+            jf.attention(c.q, *c.args(), max_new=1, max_seq=c.max_seq, prefix=bad)
+    with pytest.raises(jf.JetFP8Error):
+        jf.attention(c.q, *c.args(), max_new=1, max_seq=c.far(), prefix=pre, workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        jf.jetfp8_attention_prefix(c.q, c.units, None, c.table, c.dcodes, c.dscales, c.recent, c.T, 1, c.max_seq, 4, 2, 128, 0.1)

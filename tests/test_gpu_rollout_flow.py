@@ -1,0 +1,195 @@
+"""A rollout of several samples of each prompt through a stack of FP8 decoder blocks that runs on the library's kernels alone:
+residual norms, rotary positions, the key/value cache with forks, sweeps and compactions between steps, and the attention that
+reads a prompt's blocks once for its samples (Jet-RL explainers, "Architecture Centrale": the rollout graph is a subgraph of
+the training forward graph).  Every hidden state is bitwise that of the same tokens fed to a request of its own as one
+prompt, without any sharing.  And a training step of such a block: its input's gradient against differences of the same block
+in float64.  Weights are random and seeded; no trained model is involved."""
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+DM, HQ, HKV, HD, F, LAYERS = 512, 8, 2, 128, 1024, 2
+QKV = (HQ + 2 * HKV) * HD
+EPS = 1e-5
+
+
+@pytest.fixture(scope="module")
+def stack():
+    import torch
+    import fp8_precision_rl_amd as jf
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    jf.load_library()
+    g = torch.Generator(device="cuda")
+    g.manual_seed(12)
+
+    def lin(n, k):
+        return jf.quantize_blocks((torch.randn((n, k), device="cuda", generator=g) * k ** -0.5).to(torch.bfloat16), False)
+
+    norm = lambda: (1.0 + 0.1 * torch.randn((DM,), device="cuda", generator=g)).to(torch.bfloat16)
+    layers = [dict(qkv=lin(QKV, DM), o=lin(DM, HQ * HD), gu=lin(2 * F, DM), dn=lin(DM, F), n1=norm(), n2=norm())
+              for _ in range(LAYERS)]
+    return jf, layers, jf.rotary_frequencies(64, scaling="bands", factor=4, original=512)
+
+
+class Rollout:
+    def __init__(self, jf, layers, freqs, R, blocks, width, tokens):
+        import torch
+        self.jf, self.layers, self.freqs, self.R, self.blocks = jf, layers, freqs, R, blocks
+        self.caches = [jf.kv_cache(blocks, R, tokens, HKV, HD) for _ in layers]
+        self.state = torch.zeros((R, 2), dtype=torch.int32, device="cuda")
+        self.table = torch.full((R, width), -1, dtype=torch.int32, device="cuda")
+        self.sweep(False)
+
+    def sweep(self, compact):
+        p = self.jf.kv_sweep(self.state, self.table, self.blocks, compact=compact)
+        if compact:
+            for codes, scales, _ in self.caches:
+                self.jf.kv_move(p.moves, codes, scales)
+                codes[int(p.live):] = 0x7F                              # what is free holds nothing any more
+            self.table = p.next_table
+        self.free, self.head = p.free_blocks, p.free_head
+
+    def fork(self, parents):
+        import torch
+        parents = torch.tensor(parents, dtype=torch.int32, device="cuda")
+        f = self.jf.kv_fork(self.state, self.table, parents)
+        for _, _, recent in self.caches:
+            self.jf.kv_fork_recent(parents, self.state, recent)
+        self.state, self.table = f.next_state, f.next_table
+
+    def end(self, r):
+        self.state[r, 0] = 0
+
+    def step(self, x, lens, groups=None, max_seq=None):
+        """x: the step's rows, request by request; returns the hidden states behind the last block."""
+        import torch
+        jf, T = self.jf, len(x)
+        n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        p = jf.kv_plan(self.state, n, self.free, self.head, self.table, T, max(lens), cache=self.caches[0])
+        positions = jf.kv_positions(p.units, T)
+        prefix = None
+        if groups is not None:
+            prefix = jf.kv_prefix(p.units, self.table, torch.tensor(groups, dtype=torch.int32, device="cuda"))
+        max_seq = max_seq or 64 * self.table.shape[1]
+        h, y = x, None
+        for L, cache in zip(self.layers, self.caches):
+            if y is None:
+                xq, xs, _ = jf.rmsnorm_quantize(h, L["n1"], EPS)
+            else:
+                xq, xs, _, h = jf.rmsnorm_add_quantize(y, h, L["n1"], EPS)
+            qkv = jf.gemm_fwd(xq, xs, *L["qkv"]).view(T, HQ + 2 * HKV, HD)
+            turned = qkv[:, :HQ + HKV]
+            jf.rotary(turned, positions, self.freqs, out=turned)
+            jf.kv_append(turned[:, HQ:], qkv[:, HQ + HKV:], p.units, *cache)
+            aq, as_ = jf.attention(turned[:, :HQ], p.units, self.table, *cache, max_new=max(lens), max_seq=max_seq, quantize=True,
+                                   return_o=False, prefix=prefix)
+            hq, hs, _, h = jf.rmsnorm_add_quantize(jf.gemm_fwd(aq, as_, *L["o"]), h, L["n2"], EPS)
+            sq, ss = jf.swiglu_quantize(jf.gemm_fwd(hq, hs, *L["gu"]))
+            y = jf.gemm_fwd(sq, ss, *L["dn"])
+        self.state, self.head = p.next_state, p.next_free
+        assert not p.status.any()
+        return (h.float() + y.float()).to(torch.bfloat16), prefix
+
+
+def test_samples_equal_their_own_sequences(stack):
+    """Two prompts, three samples of each with tokens of their own; ended, forked from one another, swept and compacted."""
+    import torch
+    jf, layers, freqs = stack
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    rows = lambda n: torch.randn((n, DM), device="cuda", generator=g).to(torch.bfloat16)
+    R, n, lens = 6, 3, (600, 1153)
+    far = 64 * ((1 << 28) // (R * HKV * 128 * HD)) + 65                 # bounds with which prompts are taken apart
+    run = Rollout(jf, layers, freqs, R, 130, far // 64 + 1, sum(lens))
+    prompts = [rows(k) for k in lens]
+    seqs = [None] * R                                                   # tokens of each request, and what came out for them
+    zero = [0] * R
+    out, _ = run.step(torch.cat(prompts), [lens[0], 0, 0, lens[1], 0, 0])
+    seqs[0], seqs[3] = [prompts[0], out[:lens[0]]], [prompts[1], out[lens[0]:]]
+    run.fork([-1, 0, 0, -1, 3, 3])
+    for r in (1, 2, 4, 5):
+        seqs[r] = list(seqs[r // n * n])
+    run.sweep(False)
+    took = 0
+    for step in range(75):
+        lens_now = [1 if seqs[r] is not None and not (step % 7 == 3 and r == 4) else 0 for r in range(R)]
+        x = rows(sum(lens_now))
+        out, prefix = run.step(x, lens_now, [0, 0, 0, 1, 1, 1], far)
+        took += int((prefix[:, 2] > 0).any())
+        at = 0
+        for r in range(R):
+            if lens_now[r]:
+                seqs[r] = [torch.cat([seqs[r][0], x[at:at + 1]]), torch.cat([seqs[r][1], out[at:at + 1]])]
+                at += 1
+        if step == 20:                                                  # request 1 ends; 2 is rolled out twice
+            run.end(1)
+            run.sweep(True)
+            run.fork([-1, 2, -1, -1, -1, -1])
+            seqs[1] = list(seqs[2])
+        if step == 40:                                                  # samples change places, one of them is dropped
+            run.fork([2, -1, 0, 5, -1, -1])
+            seqs = [seqs[2], seqs[1], seqs[0], seqs[5], seqs[4], seqs[5]]
+            run.sweep(step % 2 == 0)
+        if step == 55:
+            run.end(4)
+            seqs[4] = None
+            run.sweep(True)
+    assert took > 60
+    for r in range(R):
+        if seqs[r] is None:
+            continue
+        x, want = seqs[r]
+        alone = Rollout(jf, layers, freqs, 1, 30, 30, len(x))
+        got, _ = alone.step(x, [len(x)])
+        diff = (got.view(torch.int16) != want.view(torch.int16)).any(1).nonzero().flatten()
+        assert len(diff) == 0, f"request {r}: tokens {diff[:8].tolist()} of {len(x)} differ"
+
+
+def test_training_step(stack):
+    """y = rotary(W norm(x + residual)), sum(y dy): the gradient through rotary, DGrad and the norm against central differences
+    in float64 of the same function with the quantized weights, along random directions: off by the FP8 roundings of the
+    gradient (2^-4 of each of DGrad's terms) and of its output."""
+    import torch
+    jf, layers, freqs = stack
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    T, heads = 128, 2
+    rnd = lambda *s: torch.randn(s, device="cuda", generator=g).to(torch.bfloat16)
+    x, res, w, W = rnd(T, DM), rnd(T, DM), (1 + 0.1 * rnd(DM)).to(torch.bfloat16), (rnd(heads * HD, DM) * DM ** -0.5).to(torch.bfloat16)
+    wq, ws, wqT = jf.quantize_blocks(W)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda") * 3
+    q, s, rstd, h = jf.rmsnorm_add_quantize(x, res, w, EPS)
+    y = jf.rotary(jf.gemm_fwd(q, s, wq, ws).view(T, heads, HD), pos, freqs)
+    dy, dres = rnd(*y.shape), rnd(T, DM)
+    dz = jf.rotary(dy, pos, freqs, inverse=True).view(T, -1)
+    dn = jf.gemm_dgrad(*jf.quantize_rows(dz), wqT, ws)
+    dx, dw = jf.rmsnorm_backward(dn, h, w, rstd, dres)
+
+    deq = wq.view(torch.float8_e4m3fn).double() * ws.double().repeat_interleave(128, 0).repeat_interleave(128, 1)
+    angle = pos.double()[:, None] * freqs
+    c, sn = angle.cos()[:, None], angle.sin()[:, None]
+    P = len(freqs)
+
+    def loss(h, w):
+        n = h * (h.square().mean(1, keepdim=True) + EPS).rsqrt() * w
+        z = (n @ deq.t()).view(T, heads, HD)
+        a, b = z[..., :P], z[..., P:2 * P]
+        z = torch.cat([a * c - b * sn, b * c + a * sn, z[..., 2 * P:]], -1)
+        return (z * dy.double()).sum() + (h * dres.double()).sum()
+
+    h0, w0 = h.double(), w.double()
+    # the error's size: DGrad's terms, each off by 2^-4 at most, through the norm's linear map
+    size = (dz.double().abs() @ deq.abs()) * 2.0 ** -4 + dn.double().abs() * 2.0 ** -8
+    r = rstd.double()[:, None]
+    for _ in range(6):
+        v, u = (torch.randn(t.shape, device="cuda", generator=g, dtype=torch.float64) for t in (h0, w0))
+        e = 1e-4
+        diff = (loss(h0 + e * v, w0) - loss(h0 - e * v, w0)) / (2 * e)
+        got = (dx.double() * v).sum()
+        back = r * w0 * (v - h0 * r * r * (h0 * v).mean(1, keepdim=True))
+        most = (size * back.abs()).sum() + 2.0 ** -8 * (dx.double().abs() * v.abs()).sum()
+        assert (got - diff).abs() <= most
+        diff = (loss(h0, w0 + e * u) - loss(h0, w0 - e * u)) / (2 * e)
+        got = (dw.double() * u).sum()
+        assert (got - diff).abs() <= (size * (h0 * r * u).abs()).sum()

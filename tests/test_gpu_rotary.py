@@ -1,0 +1,160 @@
+"""Rotary positions on the GPU against float64 (the bound of fp32 products is derived in oracle/rollout.py), in both layouts
+and directions, on parts of heads and columns of wider matrices."""
+import numpy as np
+import pytest
+
+from conftest import bits_to_dev, dev_to_bits, f32_to_bits
+from oracle import rollout as ro
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def jf():
+    import torch
+    import fp8_precision_rl_amd as m
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    m.load_library()
+    return m
+
+
+def value(bits):
+    return (np.asarray(bits).astype(np.uint32) << 16).view(np.float32).astype(np.float64)
+
+
+def check(got_bits, x, positions, freqs, interleaved, amplitude, inverse):
+    want, bound = ro.rotary(x, positions, freqs, interleaved, amplitude, inverse)
+    got = value(got_bits)
+    live = positions >= 0
+    err = np.abs(got - want)[live]
+    most = (bound + (np.abs(want) + bound) * 2.0 ** -8 + 2.0 ** -133)[live]
+    assert (err <= most).all(), f"worst error / bound {(err / most).max():.3f}"
+    P = len(freqs)
+    assert np.array_equal(got[live][..., 2 * P:], x[live][..., 2 * P:])
+
+
+@pytest.mark.parametrize("inverse", [False, True])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("T,H,D,P,far", [(1, 1, 16, 8, 10), (1, 48, 128, 64, 1 << 20), (32, 40, 128, 64, 4096), (3, 5, 64, 8, 1 << 20),
+                                         (100, 3, 80, 32, 9999), (7, 20, 512, 256, 1 << 21), (9, 2, 144, 40, 100), (1001, 32, 64, 16, 1 << 20),
+                                         (8200, 2, 128, 64, 8200), (16500, 1, 64, 32, 1 << 24), (2, 300, 32, 16, 50)])
+def test_against_float64(jf, T, H, D, P, far, interleaved, inverse):
+    """Rows of a wider matrix, in a new tensor and in place; the columns around them keep their values."""
+    import torch
+    rng = np.random.default_rng(T + D)
+    wide = f32_to_bits(rng.standard_normal((T, H * D + 24)))
+    wide[:, 8] = f32_to_bits(np.full(T, 1e30))
+    x = value(wide[:, 8:8 + H * D]).reshape(T, H, D)
+    pos = rng.integers(0, far, T).astype(np.int32)
+    pos[0] = far - 1
+    freqs = 10000.0 ** (-np.arange(P) / P)
+    amp = 1.25 if inverse else 1.0
+    dev = bits_to_dev(wide)
+    xs = dev[:, 8:8 + H * D].unflatten(1, (H, D))
+    p, f = torch.from_numpy(pos).cuda(), torch.from_numpy(freqs).cuda()
+    y = jf.rotary(xs, p, f, interleaved=interleaved, amplitude=amp, inverse=inverse)
+    check(dev_to_bits(y), x, pos, freqs, interleaved, float(np.float32(amp)), inverse)
+    assert np.array_equal(dev_to_bits(dev), wide)
+    z = jf.rotary(xs, p, f, interleaved=interleaved, amplitude=amp, inverse=inverse, out=xs)
+    assert z is xs and torch.equal(xs, y)
+    after = dev_to_bits(dev)
+    assert np.array_equal(after[:, :8], wide[:, :8]) and np.array_equal(after[:, 8 + H * D:], wide[:, 8 + H * D:])
+
+
+@pytest.mark.parametrize("T", [6, 5000])
+def test_rows_without_a_position_are_left(jf, T):
+    import torch
+    rng = np.random.default_rng(2)
+    x = f32_to_bits(rng.standard_normal((T, 3, 64)))
+    pos = rng.integers(-3, 50, T).astype(np.int32)
+    pos[:2] = -1, 0
+    f = 10.0 ** -np.arange(8.0)
+    out = torch.full((T, 3, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    got = jf.rotary(bits_to_dev(x), torch.from_numpy(pos).cuda(), torch.from_numpy(f).cuda(), out=out)
+    assert (got[torch.from_numpy(pos < 0).cuda()] == 7.0).all()
+    check(dev_to_bits(got), value(x), pos, f, False, 1.0, False)
+
+
+def test_a_row_does_not_depend_on_the_call(jf):
+    """Bitwise the same alone, among few and among many rows, and for the heads of a call together or apart."""
+    import torch
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    x = torch.randn((20000, 12, 128), device="cuda", generator=g).to(torch.bfloat16)
+    pos = torch.randint(0, 1 << 20, (20000,), device="cuda", generator=g, dtype=torch.int32)
+    f = jf.rotary_frequencies(128)
+    whole = jf.rotary(x, pos, f)
+    for n in (1, 33, 4100):
+        assert torch.equal(jf.rotary(x[:n], pos[:n].contiguous(), f), whole[:n])
+    assert torch.equal(jf.rotary(x[:64, 5:7], pos[:64].contiguous(), f), whole[:64, 5:7])
+    back = jf.rotary(whole, pos, f, inverse=True).float() - x.float()
+    assert back.norm() / x.float().norm() <= 2.0 ** -7      # two roundings to bf16, each by 2^-8 at most
+
+
+def test_special_values(jf):
+    """Infinities and NaN stay in their pair; subnormals and signed zeros are kept at position 0."""
+    import torch
+    x = torch.randn((4, 2, 64), device="cuda").to(torch.bfloat16)
+    x[1, 0, 3], x[2, 1, 9] = float("nan"), float("inf")
+    x[0, 0, :4] = torch.tensor([1e-40, -1e-40, -0.0, 0.0], device="cuda").to(torch.bfloat16)
+    pos = torch.tensor([0, 5, 6, 7], dtype=torch.int32, device="cuda")
+    f = jf.rotary_frequencies(32)
+    y = jf.rotary(x, pos, f)
+    assert torch.equal(y[0], x[0])
+    bad = ~torch.isfinite(y)
+    where = {tuple(i) for i in bad.nonzero().tolist()}
+    assert where == {(1, 0, 3), (1, 0, 19), (2, 1, 9), (2, 1, 25)}
+
+
+def test_long_rows_and_large_offsets(jf):
+    """Rows further apart than 2^31 elements in all."""
+    import torch
+    T, ld = 140, 1 << 24
+    wide = torch.zeros((T, ld), dtype=torch.bfloat16, device="cuda")
+    x = wide[:, 64:192].unflatten(1, (2, 64))
+    src = torch.randn((T, 2, 64), device="cuda").to(torch.bfloat16)
+    x.copy_(src)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda") * 7919
+    f = jf.rotary_frequencies(64)
+    want = jf.rotary(src, pos, f)
+    jf.rotary(x, pos, f, out=x)
+    assert torch.equal(x, want)
+    assert not wide[:, :64].any() and not wide[-3:, 192:].any()
+
+
+def test_streams_and_graphs(jf):
+    import torch
+    x = torch.randn((500, 6, 128), device="cuda").to(torch.bfloat16)
+    pos = torch.arange(500, dtype=torch.int32, device="cuda")
+    f = jf.rotary_frequencies(128)
+    want = jf.rotary(x, pos, f)
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = jf.rotary(x, pos, f, stream=stream)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = jf.rotary(x, pos, f, interleaved=True)
+    for n in range(3):
+        pos.add_(1000 * n)
+        x.mul_(1.5)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, jf.rotary(x, pos, f, interleaved=True))
+
+
+def test_binding_refusals(jf):
+    import torch
+    x = torch.zeros((4, 2, 64), dtype=torch.bfloat16, device="cuda")
+    pos, f = torch.zeros(4, dtype=torch.int32, device="cuda"), jf.rotary_frequencies(64)
+    ok = dict(x=x, positions=pos, freqs=f)
+    for bad in (dict(positions=pos[:3]), dict(out=x[:2]), dict(x=x.transpose(0, 1)), dict(freqs=f.cpu())):
+        with pytest.raises(ValueError):
+            jf.rotary(**(ok | bad))
+    for bad in (dict(positions=pos.long()), dict(freqs=f.float()), dict(x=x.half())):
+        with pytest.raises(TypeError):
+            jf.rotary(**(ok | bad))
+    for bad in (dict(freqs=jf.rotary_frequencies(72)), dict(amplitude=0.0), dict(freqs=jf.rotary_frequencies(128))):
+        with pytest.raises(jf.JetFP8Error):
+            jf.rotary(**(ok | bad))
