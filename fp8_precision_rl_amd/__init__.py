@@ -932,7 +932,9 @@ def kv_fork(state, block_table, parents, stream=None) -> KVFork:
     R, W = block_table.shape
     with _memory_of(stream, state.device):
         f = KVFork(state.new_empty(R, 2), state.new_empty(R, W))
-    jetfp8_kv_fork(state, block_table, W, R, parents, f.next_state, f.next_table, stream)
+    i32, dev = _torch.int32, state.get_device()
+    _call("jetfp8_kv_fork", dev, stream, _use(state, (R, 2), i32, "state"), _use(block_table, (R, W), i32, "block_table", dev),
+          W, R, _use(parents, (R,), i32, "parents", dev), f.next_state.data_ptr(), f.next_table.data_ptr())
     return f
 
 
@@ -963,7 +965,10 @@ def kv_sweep(state, block_table, num_blocks: int, compact: bool = False, workspa
         p = KVSweep(new(n), new(1), new(1), new(R, W) if compact else None, new(max(1, n // 2), 2) if compact else None)
         if size and workspace is None:
             workspace = new(size, dtype=_torch.uint8)
-    jetfp8_kv_sweep(state, block_table, W, R, n, p.free_blocks, p.free_head, p.live, p.next_table, p.moves, workspace, stream)
+    i32, dev = _torch.int32, state.get_device()
+    _call("jetfp8_kv_sweep", dev, stream, _use(state, (R, 2), i32, "state"), _use(block_table, (R, W), i32, "block_table", dev),
+          W, R, n, p.free_blocks.data_ptr(), p.free_head.data_ptr(), p.live.data_ptr(),
+          p.next_table.data_ptr() if compact else None, p.moves.data_ptr() if compact else None, *_space(workspace, dev))
     return p
 
 

@@ -578,24 +578,32 @@ __device__ __forceinline__ void walk_span(State<D, R>& st, const typename State<
 // are used; there is no LDS.  With R = 16 all rows are one wave's and nobody else reads its codes: the loads are marked
 // as not to be kept, which leaves the caches to the partial results (256 requests up to 8192 tokens: 477 -> 422 us).
 //
-// PREFIX: the spans that the unit's group shares are attention_prefix_kernel's, and the others are taken from the last on,
-// so that the thread blocks without work are whole.
+// PREFIX: the spans that the unit's group shares are attention_prefix_kernel's, and how many are left is known on the device
+// only.  So they are taken from the last on (the own block), all units' last ones first: the thread blocks without work come
+// at the end.  Two waves to a thread block, since what is left is seldom even (256 requests of 16 prompts with up to 1024
+// tokens of their own, us: 4 waves and a unit's spans next to one another 78, 2 waves 71, 1 wave 71; 64 prompts of 8 samples 95, 92
+// and 91); four with 64 channels, where starting them takes its share (12.7 against 15.6 and 16.6).
+template <int D>
+constexpr int kTailWaves = D == 64 ? 4 : 2;
+
 template <int D, int R, bool PREFIX>
-__global__ __launch_bounds__(kWaves * 64, R == 16 ? 3 : 2) void attention_span_kernel(AttnArgs a) {
+__global__ __launch_bounds__((PREFIX ? kTailWaves<D> : kWaves) * 64, R == 16 ? 3 : 2) void attention_span_kernel(AttnArgs a) {
     typedef State<D, R> S;
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int head = blockIdx.x % a.kv_heads;
     const int jobs = a.parts * a.row_groups, chunks = (jobs + kWaves - 1) / kWaves;
     const int unit = PREFIX ? blockIdx.x / a.kv_heads % a.num_units : blockIdx.x / a.kv_heads / chunks;
-    const int job = (PREFIX ? blockIdx.x / a.kv_heads / a.num_units : blockIdx.x / a.kv_heads % chunks) * kWaves + wave;
+    const int job = PREFIX ? blockIdx.x / a.kv_heads / a.num_units * kTailWaves<D> + wave
+                           : blockIdx.x / a.kv_heads % chunks * kWaves + wave;
     if (job >= jobs) return;
     const int row0 = job % a.row_groups * R;
     const KvUnit u = a.units[unit];
     if (!unit_fits(u, a.requests, a.tokens, a.recent_blocks, a.num_blocks)) return;
     const int rows = u.rows * a.group, own = (u.block + kSpan - 1) / kSpan;
-    const int span = PREFIX ? own - job / a.row_groups : job / a.row_groups;
     if (row0 >= rows || rows > a.max_rows || u.block > a.max_blocks) return;
-    if (PREFIX ? span < a.prefix[unit].z / kSpan || span < 0 : span > own) return;
+    const int from = PREFIX ? max(a.prefix[unit].z / kSpan, 0) : 0;
+    const int span = PREFIX ? own - job / a.row_groups : job / a.row_groups;
+    if (span < from || span > own) return;
 
     typename S::Queries q;
     load_queries<D, R>(q, a, u, head, row0, rows, lane);
@@ -1126,7 +1134,16 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
             join_parts<W>(load_ml(s0, n), po + s0 * step, step, n, lane, M, L, o);
         }
     } else {
-        for (int r0 = 0; r0 < runs; r0 += kRun) {
+        int first_run = 0;
+        if (PREFIX) {                    // the runs that are one partial result each
+            first_run = shared / kRun < 2 ? 0 : min(shared / kRun, runs);
+            for (int r0 = 0; r0 < first_run; r0 += kJoin) {
+                const int n = min(kJoin, first_run - r0), s0 = r0 * kRun + kRun - 1;
+                const float2 ml = lane < n ? pml[(int64_t)(s0 + lane * kRun) * a.max_rows] : make_float2(-INFINITY, 0.0f);
+                join_parts<W>(ml, po + s0 * step, kRun * step, n, lane, M, L, o);
+            }
+        }
+        for (int r0 = first_run; r0 < runs; r0 += kRun) {
             const int n = min(kRun, runs - r0);
             for (int r = wave % WAVES; r < n; r += WAVES) {
                 const int s0 = run_begin((r0 + r) * kRun), m = min((r0 + r + 1) * kRun, parts) - s0;
@@ -1244,9 +1261,14 @@ hipError_t launch(const AttnArgs& a, const AttnShape& s, unsigned grid, hipStrea
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
+    const unsigned threads = (PREFIX ? kTailWaves<D> : kWaves) * 64;
+    if (PREFIX) {       // no more threads than with four waves to a thread block, which attention_fits looks at
+        const int64_t jobs = s.parts * s.row_groups, chunks = (jobs + kTailWaves<D> - 1) / kTailWaves<D>;
+        grid = (unsigned)((int64_t)a.num_units * a.kv_heads * chunks);
+    }
     if (!s.split) attention_tile_kernel<D><<<grid, kWaves * 64, 0, st>>>(a);
-    else if (s.rows == 16) attention_span_kernel<D, 16, PREFIX><<<grid, kWaves * 64, 0, st>>>(a);
-    else attention_span_kernel<D, 32, PREFIX><<<grid, kWaves * 64, 0, st>>>(a);
+    else if (s.rows == 16) attention_span_kernel<D, 16, PREFIX><<<grid, threads, 0, st>>>(a);
+    else attention_span_kernel<D, 32, PREFIX><<<grid, threads, 0, st>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || s.parts == 0) return e;
     const int64_t rows = (int64_t)a.num_units * a.kv_heads * a.max_rows;
