@@ -226,6 +226,70 @@ __global__ __launch_bounds__(RN_WAVES * 64) void rmsnorm_quant_kernel(
     }
 }
 
+// The same for few rows: a thread block takes one row, a wave one chunk of 512 columns, so that a row's chunks are normalized
+// and encoded side by side instead of one after the other.  Every wave forms the row's sum of squares for itself, from LDS
+// and in the order of rmsnorm_quant_kernel (HALF chunks in line per lane, the halves' totals added), so a row has the same bits
+// in both.  HALF: chunks per half, those of <NCH, WPR> above; 0: the row has no halves.
+template <int HALF, int NCH, bool ADD>
+__global__ __launch_bounds__(NCH * 64) void rmsnorm_row_kernel(
+    const uint16_t* x, const uint16_t* residual, const uint16_t* __restrict__ w, int64_t R, int64_t C, float eps,
+    uint16_t* h, uint8_t* __restrict__ q, float* __restrict__ s, float* __restrict__ rstd, uint16_t* __restrict__ y) {
+    __shared__ uint4 all[NCH][64];
+    const int lane = threadIdx.x & 63, chunk = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t row = blockIdx.x, col = (int64_t)chunk * 512 + lane * 8, at = row * C + col;
+    const bool ok = col < C;
+    uint4 v = make_uint4(0, 0, 0, 0), wv = v;
+    if (ok) {
+        v = ld16(x + at);
+        wv = ld16(w + col);
+        if (ADD) {
+            const uint4 b = ld16(residual + at);
+            uint32_t sum[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                sum[i] = bf16x2_rne(elem_of(v, 2 * i) + elem_of(b, 2 * i), elem_of(v, 2 * i + 1) + elem_of(b, 2 * i + 1));
+            v = make_uint4(sum[0], sum[1], sum[2], sum[3]);
+            *reinterpret_cast<uint4*>(h + at) = v;
+        }
+    }
+    all[chunk][lane] = v;
+    __syncthreads();
+    constexpr int PARTS = HALF ? 2 : 1, PER = HALF ? HALF : NCH;
+    double pa[PARTS][8];
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) pa[p][i] = 0;
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+        const uint4 a = all[k][lane];                            // zeros behind the row's end: they add nothing
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const double f = (double)elem_of(a, i);
+            pa[k / PER][i] = fma(f, f, pa[k / PER][i]);
+        }
+    }
+    double ss[PARTS];
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p)
+        ss[p] = wave_sum(((pa[p][0] + pa[p][1]) + (pa[p][2] + pa[p][3])) + ((pa[p][4] + pa[p][5]) + (pa[p][6] + pa[p][7])));
+    const double total = PARTS > 1 ? ss[0] + ss[PARTS - 1] : ss[0];
+    const float r = (float)(1.0 / sqrt(total / (double)C + (double)eps));
+    if (rstd && threadIdx.x == 0) rstd[row] = r;
+    uint32_t hw[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        hw[k] = bf16x2_rne((elem_of(v, 2 * k) * r) * elem_of(wv, 2 * k), (elem_of(v, 2 * k + 1) * r) * elem_of(wv, 2 * k + 1));
+    const uint4 yv = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+    float scale;
+    const uint2 codes = quantize_lane8(yv, scale);
+    if (ok) {
+        *reinterpret_cast<uint2*>(q + at) = codes;
+        if (y) *reinterpret_cast<uint4*>(y + at) = yv;
+        if ((lane & 15) == 0) s[(int64_t)(chunk * 4 + (lane >> 4)) * R + row] = scale;
+    }
+}
+
 // ---------------------------------------------------------------------------------------------------------
 // SwiGLU -> 1x128.  gate_up [R][2F] -> codes [R][F], scales [F/128][R], optional h [R][F].  A block of 8 waves
 // owns 32 rows x 512 output columns (4 groups per row); lane l of a wave covers output columns
@@ -326,6 +390,18 @@ hipError_t launch_norm(const uint16_t* x, const uint16_t* res, const uint16_t* w
     const dim3 block(RN_WAVES * 64);
     const dim3 grid1((unsigned)((R + RN_WAVES - 1) / RN_WAVES)), grid2((unsigned)((R + RN_WAVES / 2 - 1) / (RN_WAVES / 2)));
     const int nch = (int)((C + 511) / 512);
+    // (us with the addition, a thread block a row against the other: 32 rows of 5120 5.0 / 8.2, 256 rows 5.9 / 8.7, 512 8.9 / 9.2, 1024
+    // 14.7 / 11.3; of 2048 3.4 / 6.7, 512 rows 4.4 / 7.3, 2048 rows 8.9 / 9.0)
+    if (R <= 512) {
+        const unsigned grid = (unsigned)R;
+        if (nch <= 2) rmsnorm_row_kernel<0, 2, ADD><<<grid, 2 * 64, 0, st>>>(x, res, w, R, C, eps, h, q, s, rstd, y);
+        else if (nch <= 4) rmsnorm_row_kernel<0, 4, ADD><<<grid, 4 * 64, 0, st>>>(x, res, w, R, C, eps, h, q, s, rstd, y);
+        else if (nch <= 8) rmsnorm_row_kernel<4, 8, ADD><<<grid, 8 * 64, 0, st>>>(x, res, w, R, C, eps, h, q, s, rstd, y);
+        else if (nch <= 10) rmsnorm_row_kernel<5, 10, ADD><<<grid, 10 * 64, 0, st>>>(x, res, w, R, C, eps, h, q, s, rstd, y);
+        else if (nch <= 12) rmsnorm_row_kernel<6, 12, ADD><<<grid, 12 * 64, 0, st>>>(x, res, w, R, C, eps, h, q, s, rstd, y);
+        else rmsnorm_row_kernel<8, 16, ADD><<<grid, 16 * 64, 0, st>>>(x, res, w, R, C, eps, h, q, s, rstd, y);
+        return hipGetLastError();
+    }
     if (nch <= 2) rmsnorm_quant_kernel<2, 1, ADD><<<grid1, block, 0, st>>>(x, res, w, R, C, eps, h, q, s, rstd, y);
     else if (nch <= 4) rmsnorm_quant_kernel<4, 1, ADD><<<grid1, block, 0, st>>>(x, res, w, R, C, eps, h, q, s, rstd, y);
     else if (nch <= 8) rmsnorm_quant_kernel<8, 2, ADD><<<grid2, block, 0, st>>>(x, res, w, R, C, eps, h, q, s, rstd, y);

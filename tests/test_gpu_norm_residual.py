@@ -68,6 +68,27 @@ def test_forward(jf, prod, R, C):
     assert np.array_equal(s.cpu().numpy()[:, pick].view(np.uint32), os_.view(np.uint32))
 
 
+@pytest.mark.parametrize("C", [128, 896, 1152, 2048, 2176, 4096, 4224, 5120, 5248, 6144, 6272, 8192])
+def test_a_row_does_not_depend_on_the_call(jf, C):
+    """The same bits alone, among a few rows and among many, with magnitudes so far apart that the order of the sum of squares
+    matters to it."""
+    import torch
+    g = torch.Generator(device="cuda")
+    g.manual_seed(C)
+    R = 700
+    rnd = lambda: torch.randn((R, C), device="cuda", generator=g)
+    x, res = (rnd() * torch.exp2(20 * torch.rand((R, C), device="cuda", generator=g) - 10)).to(torch.bfloat16), rnd().to(torch.bfloat16)
+    w = (1 + 0.1 * torch.randn((C,), device="cuda", generator=g)).to(torch.bfloat16)
+    whole, plain = jf.rmsnorm_add_quantize(x, res, w, 1e-5, return_y=True), jf.rmsnorm_quantize(x, w, 1e-5, return_y=True)
+    for a, b in ((0, 1), (1, 40), (188, 700)):
+        part = jf.rmsnorm_add_quantize(x[a:b].contiguous(), res[a:b].contiguous(), w, 1e-5, return_y=True)
+        for have, want in zip(part, (whole[0][a:b], whole[1][:, a:b], whole[2][a:b], whole[3][a:b], whole[4][a:b])):
+            assert torch.equal(have, want)
+        part = jf.rmsnorm_quantize(x[a:b].contiguous(), w, 1e-5, return_y=True)
+        for have, want in zip(part, (plain[0][a:b], plain[1][:, a:b], plain[2][a:b], plain[3][a:b])):
+            assert torch.equal(have, want)
+
+
 @pytest.mark.parametrize("where", ["x", "residual"])
 @pytest.mark.parametrize("R,C", [(5, 128), (70, 5120)])
 def test_forward_in_place(jf, R, C, where):
