@@ -645,7 +645,8 @@ __global__ __launch_bounds__((PREFIX ? kTailWaves<D> : kWaves) * 64, R == 16 ? 3
 // attention_prefix_kernel takes the blocks that the requests of a group share, in the rows of all its units at once: row g
 // of the group is row g % max_rows of its unit g / max_rows, and 32 of them are a wave's, whatever units they belong to.
 // A piece of work is such a tile of rows and a run of 8 spans: eight waves take a span each and join them in order as the other
-// kernels do, so that one partial result of a run is written instead of eight, in the place of the run's last shared span.
+// kernels do, so that one partial result of a run is written instead of eight, in the place of the run's last shared span.  Of
+// the last run, where only s spans are shared, a piece is as many tiles as eight waves hold, 8 / s.
 //
 // How many pieces there are is known from the units' records only, so a fixed number of thread blocks, as many as fit the
 // chip, count them and take them in turn.  (With a thread block for every piece that the sizes allow, most of which find
@@ -658,8 +659,11 @@ __global__ __launch_bounds__((PREFIX ? kTailWaves<D> : kWaves) * 64, R == 16 ? 3
 // waves share, 115; 64 rows to a wave, 108.
 constexpr int kPrefixWaves = kRun;
 struct PrefixUnit {
-    int4 group;                // its record; no shared blocks if the record does not fit
-    int first_tile, tiles, runs;
+    int4 group;                // its record
+    int full, rest, pack;      // runs that are shared whole, spans of the one behind them, tiles in a piece of that
+    int tile, tiles;           // pieces of a whole run that begin in this unit's rows: the first, and how many
+    int part, parts;           // the same for those of the last run
+    __device__ __forceinline__ int pieces() const { return full * tiles + parts; }
 };
 
 __device__ __forceinline__ PrefixUnit prefix_unit(const AttnArgs& a, int unit) {
@@ -667,11 +671,16 @@ __device__ __forceinline__ PrefixUnit prefix_unit(const AttnArgs& a, int unit) {
     p.group = a.prefix[unit];
     const int rank = unit - p.group.x;
     const bool fits = p.group.x >= 0 && rank >= 0 && rank < p.group.y && p.group.y <= a.num_units - p.group.x &&
-                      p.group.z <= a.max_blocks;
-    p.runs = fits ? max((p.group.z / kSpan + kRun - 1) / kRun, 0) : 0;
-    // tiles of the group that begin in this unit's rows
-    p.first_tile = fits ? (rank * a.max_rows + 31) / 32 : 0;
-    p.tiles = p.runs > 0 ? ((rank + 1) * a.max_rows + 31) / 32 - p.first_tile : 0;
+                      p.group.z > 0 && p.group.z <= a.max_blocks;
+    const int spans = fits ? p.group.z / kSpan : 0;
+    p.full = spans / kRun;
+    p.rest = spans % kRun;
+    p.pack = p.rest ? kPrefixWaves / p.rest : 1;
+    const int begin = fits ? rank * a.max_rows : 0, end = fits ? begin + a.max_rows : 0;
+    p.tile = (begin + 31) / 32;
+    p.tiles = p.full ? (end + 31) / 32 - p.tile : 0;
+    p.part = (begin + 32 * p.pack - 1) / (32 * p.pack);
+    p.parts = p.rest ? (end + 32 * p.pack - 1) / (32 * p.pack) - p.part : 0;
     return p;
 }
 
@@ -681,14 +690,12 @@ __global__ __launch_bounds__(kPrefixWaves * 64, 2) void attention_prefix_kernel(
     constexpr int kQuads = D / 4, kMine = kQuads / 2 / kPrefixWaves;       // 4 channels each: of a row, and of a lane to join
     __shared__ v4f part_o[kPrefixWaves][kQuads][32];
     __shared__ float2 part_ml[kPrefixWaves][32];
-    __shared__ int upto[kPrefixWaves * 64], found[5];                // pieces of the units up to a thread's last
+    __shared__ int64_t place[kPrefixWaves][32];                      // of the rows' partial results; -1: none
+    __shared__ int upto[kPrefixWaves * 64], found[6];                // pieces of the units up to a thread's last
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int each = (a.num_units + kPrefixWaves * 64 - 1) / (kPrefixWaves * 64), from = threadIdx.x * each;
     int pieces = 0;
-    for (int i = from; i < min(from + each, a.num_units); ++i) {
-        const PrefixUnit p = prefix_unit(a, i);
-        pieces += p.tiles * p.runs;
-    }
+    for (int i = from; i < min(from + each, a.num_units); ++i) pieces += prefix_unit(a, i).pieces();
     int sum = pieces;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
@@ -712,32 +719,39 @@ __global__ __launch_bounds__(kPrefixWaves * 64, 2) void attention_prefix_kernel(
         if (left >= 0 && left < pieces) {
             for (int i = from;; ++i) {
                 const PrefixUnit p = prefix_unit(a, i);
-                if (left < p.tiles * p.runs) {
+                if (left < p.pieces()) {
+                    const bool last = left >= p.full * p.tiles;
                     found[0] = p.group.x;
                     found[1] = p.group.y;
                     found[2] = p.group.z;
-                    found[3] = p.first_tile + left / p.runs;
-                    found[4] = left % p.runs;
+                    found[3] = last ? (p.part + left - p.full * p.tiles) * p.pack : p.tile + left / p.full;
+                    found[4] = last ? p.full : left % p.full;
+                    found[5] = last ? p.rest : kRun;
                     break;
                 }
-                left -= p.tiles * p.runs;
+                left -= p.pieces();
             }
         }
         __syncthreads();
         const int first_unit = __builtin_amdgcn_readfirstlane(found[0]), units = __builtin_amdgcn_readfirstlane(found[1]);
         const int shared = __builtin_amdgcn_readfirstlane(found[2]);
-        const int tile = __builtin_amdgcn_readfirstlane(found[3]), run = __builtin_amdgcn_readfirstlane(found[4]);
+        const int first_tile = __builtin_amdgcn_readfirstlane(found[3]), run = __builtin_amdgcn_readfirstlane(found[4]);
+        const int spans = __builtin_amdgcn_readfirstlane(found[5]), pack = kPrefixWaves / spans;
         const int request = a.units[first_unit].request;
         if (request < 0 || request >= a.requests) continue;
-        const int spans = min(shared / kSpan - run * kRun, kRun);        // of this run
+        const int tile = wave / spans, span = wave % spans;              // of this wave; tiles from pack on: none
 
-        // this lane's row
-        const int row = tile * 32 + lane % 32, member = row / a.max_rows, local = row % a.max_rows;
+        // this lane's row, and where its result goes
+        const int row = (first_tile + tile) * 32 + lane % 32, member = row / a.max_rows, local = row % a.max_rows;
         const int mine = first_unit + min(member, units - 1);
         const KvUnit u = a.units[mine];
         const int rows = u.rows * a.group;
-        const bool live = member < units && unit_fits(u, a.requests, a.tokens, a.recent_blocks, a.num_blocks) &&
-                          local < rows && rows <= a.max_rows && u.block <= a.max_blocks && u.block >= shared;
+        const bool live = tile < pack && member < units &&
+                          unit_fits(u, a.requests, a.tokens, a.recent_blocks, a.num_blocks) && local < rows &&
+                          rows <= a.max_rows && u.block <= a.max_blocks && u.block >= shared;
+        if (span == 0 && lane < 32)
+            place[tile][lane] =
+                live ? (((int64_t)mine * a.kv_heads + head) * a.parts + run * kRun + spans - 1) * a.max_rows + local : -1;
         typename S::Queries q;
         const uint16_t* p =
             a.q + (live ? (u.row + local / a.group) * a.ldq + ((int64_t)head * a.group + local % a.group) * D : 0) + lane / 32 * 8;
@@ -748,9 +762,9 @@ __global__ __launch_bounds__(kPrefixWaves * 64, 2) void attention_prefix_kernel(
             q[k] = __builtin_bit_cast(bf16x8, x);
         }
 
-        if (wave < spans) {
+        if (tile < pack && __any(live)) {
             S st;
-            const int first = (run * kRun + wave) * kSpan;
+            const int first = (run * kRun + span) * kSpan;
             walk_span<D, 32, true>(st, q, a, request, head, first, first + kSpan, lane);
             const float factor = st.factor(), l = st.sum();
 #pragma unroll
@@ -762,24 +776,25 @@ __global__ __launch_bounds__(kPrefixWaves * 64, 2) void attention_prefix_kernel(
             if (lane < 32) part_ml[wave][lane] = make_float2(st.top, l);
         }
         __syncthreads();
-        float M = -INFINITY, L = 0.0f;
-        v4f o[kMine];
+        for (int t = 0; t < pack; ++t) {
+            const int64_t at = place[t][lane % 32];
+            if (at < 0) continue;
+            float M = -INFINITY, L = 0.0f;
+            v4f o[kMine];
 #pragma unroll
-        for (int i = 0; i < kMine; ++i) o[i] = v4f{};
-        for (int s = 0; s < spans; ++s) {
-            const float2 ml = part_ml[s][lane % 32];
-            float x, y;
-            join_factors(M, ml.x, x, y);
-            L = fmaf(L, x, ml.y * y);
+            for (int i = 0; i < kMine; ++i) o[i] = v4f{};
+            for (int s = t * spans; s < (t + 1) * spans; ++s) {
+                const float2 ml = part_ml[s][lane % 32];
+                float x, y;
+                join_factors(M, ml.x, x, y);
+                L = fmaf(L, x, ml.y * y);
 #pragma unroll
-            for (int i = 0; i < kMine; ++i) {
-                const v4f v = part_o[s][(wave * kMine + i) * 2 + lane / 32][lane % 32];
+                for (int i = 0; i < kMine; ++i) {
+                    const v4f v = part_o[s][(wave * kMine + i) * 2 + lane / 32][lane % 32];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) o[i][c] = fmaf(o[i][c], x, v[c] * y);
+                    for (int c = 0; c < 4; ++c) o[i][c] = fmaf(o[i][c], x, v[c] * y);
+                }
             }
-        }
-        if (live) {
-            const int64_t at = (((int64_t)mine * a.kv_heads + head) * a.parts + run * kRun + spans - 1) * a.max_rows + local;
 #pragma unroll
             for (int i = 0; i < kMine; ++i)
                 *reinterpret_cast<v4f*>(a.part_o + at * D + (wave * kMine + i) * 8 + lane / 32 * 4) = o[i];

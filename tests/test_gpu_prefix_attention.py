@@ -117,6 +117,7 @@ GROUPS = {
     "none long enough": [(300, 3), (511, 2)],
     "one span": [(512, 2), (575, 5)],
     "two and a bit": [(1024, 9), (1100, 33)],
+    "three to seven": [(1600, 40), (2100, 9), (2700, 12), (3300, 70), (3700, 3), (512, 290)],
     "one run": [(4096, 4)],
     "run and span": [(4608, 17), (600, 1), (4650, 2)],
     "several runs": [(9000, 6), (64, 2), (8192, 12)],
