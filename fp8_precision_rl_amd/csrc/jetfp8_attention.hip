@@ -694,8 +694,9 @@ __global__ __launch_bounds__(kPrefixWaves * 64, 2) void attention_prefix_kernel(
     __shared__ int upto[kPrefixWaves * 64], found[6];                // pieces of the units up to a thread's last
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int each = (a.num_units + kPrefixWaves * 64 - 1) / (kPrefixWaves * 64), from = threadIdx.x * each;
+    const int end = min(from + each, a.num_units);
     int pieces = 0;
-    for (int i = from; i < min(from + each, a.num_units); ++i) pieces += prefix_unit(a, i).pieces();
+    for (int i = from; i < end; ++i) pieces += prefix_unit(a, i).pieces();
     int sum = pieces;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
@@ -717,7 +718,8 @@ __global__ __launch_bounds__(kPrefixWaves * 64, 2) void attention_prefix_kernel(
         __syncthreads();
         // the thread whose units have the piece tells the others
         if (left >= 0 && left < pieces) {
-            for (int i = from;; ++i) {
+            found[5] = 0;
+            for (int i = from; i < end; ++i) {
                 const PrefixUnit p = prefix_unit(a, i);
                 if (left < p.pieces()) {
                     const bool last = left >= p.full * p.tiles;
@@ -736,8 +738,9 @@ __global__ __launch_bounds__(kPrefixWaves * 64, 2) void attention_prefix_kernel(
         const int first_unit = __builtin_amdgcn_readfirstlane(found[0]), units = __builtin_amdgcn_readfirstlane(found[1]);
         const int shared = __builtin_amdgcn_readfirstlane(found[2]);
         const int first_tile = __builtin_amdgcn_readfirstlane(found[3]), run = __builtin_amdgcn_readfirstlane(found[4]);
-        const int spans = __builtin_amdgcn_readfirstlane(found[5]), pack = kPrefixWaves / spans;
-        const int request = a.units[first_unit].request;
+        const int spans = __builtin_amdgcn_readfirstlane(found[5]);
+        if (spans == 0) continue;                        // the records have changed since they were counted
+        const int request = a.units[first_unit].request, pack = kPrefixWaves / spans;
         if (request < 0 || request >= a.requests) continue;
         const int tile = wave / spans, span = wave % spans;              // of this wave; tiles from pack on: none
 
