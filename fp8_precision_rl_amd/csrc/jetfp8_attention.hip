@@ -636,7 +636,11 @@ __global__ __launch_bounds__((PREFIX ? kTailWaves<D> : kWaves) * 64, R == 16 ? 3
             });
     } else {
         const int first = span * kSpan;
-        walk_span<D, R, R == 32 || PREFIX>(st, q, a, u.request, head, first, min(first + kSpan, u.block), lane);
+        // 16 rows: marked as not to be kept, but with 64 channels and shared prompts, where the blocks of a prompt that do not
+        // fill a span are much of what is read (us, kept against not: 256 requests of 16 prompts 141 / 128, 128 channels; 124 of 3
+        // prompts 37 / 40, 64 channels)
+        constexpr bool keep = R == 32 || (PREFIX && D == 64);
+        walk_span<D, R, keep>(st, q, a, u.request, head, first, min(first + kSpan, u.block), lane);
         factor = st.factor();
     }
     store_part<D, R>(st.top, st.sum(), st.o, factor, a, unit, head, span, row0 + lane % R, rows, lane);
