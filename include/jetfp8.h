@@ -350,6 +350,8 @@ int64_t jetfp8_attention_workspace(int64_t num_units, int64_t max_new, int64_t m
  * most of the time).  Their requests hold the prompt's complete blocks in common: the same ids at the head of their rows
  * of the block table.  A request holds what the first tokens / 64 entries of its row name, and nothing else says so:
  * blocks need no counts, and a request that is done gives up its own by having 0 tokens in its state.
+ * The calls that take a state stand between two steps and take that after the last one (jetfp8_kv_plan's next_state): by the
+ * state before a step, the blocks that the step filled would count as free.
  */
 
 /* Which units of a step share blocks, from jetfp8_kv_plan's units in their order: once for a step, for all layers.
