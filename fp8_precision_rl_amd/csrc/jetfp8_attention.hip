@@ -23,7 +23,7 @@ constexpr int kWaves = 4;          // waves of a thread block; they share nothin
 // 4 % slower where the cache is long (256 requests up to 8192 tokens 421 against 405 us: twice the partial results)
 // and 6 % in the tile kernel (twice the joining), and 4 % faster for 32 requests up to 4096 tokens.
 constexpr int kSpan = kKvSpan;
-constexpr int kRun = 8;
+constexpr int kRun = kKvRun;
 constexpr int kRunBlocks = kRun * kSpan;
 // The cache's probabilities enter the second product as fp16, in which the values' codes are exact, each times its block's
 // scale and relative to a reference of its own, near the row's largest such product in the span: what a block adds to the
@@ -599,9 +599,9 @@ __global__ __launch_bounds__((PREFIX ? kTailWaves<D> : kWaves) * 64, R == 16 ? 3
     const int row0 = job % a.row_groups * R;
     const KvUnit u = a.units[unit];
     if (!unit_fits(u, a.requests, a.tokens, a.recent_blocks, a.num_blocks)) return;
-    const int rows = u.rows * a.group, own = (u.block + kSpan - 1) / kSpan;
+    const int rows = u.rows * a.group, own = join_spans(u.block);
     if (row0 >= rows || rows > a.max_rows || u.block > a.max_blocks) return;
-    const int from = PREFIX ? max(a.prefix[unit].z / kSpan, 0) : 0;
+    const int from = PREFIX ? join_shared(u.block, a.prefix[unit].z) : 0;
     const int span = PREFIX ? own - job / a.row_groups : job / a.row_groups;
     if (span < from || span > own) return;
 
@@ -1135,7 +1135,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
     if (!unit_fits(u, a.requests, a.tokens, a.recent_blocks, a.num_blocks)) return;
     const int rows = u.rows * a.group;
     if (row >= rows || rows > a.max_rows || u.block > a.max_blocks) return;
-    const int runs = (u.block + kRunBlocks - 1) / kRunBlocks, parts = SPANS ? (u.block + kSpan - 1) / kSpan : runs;
+    const int runs = join_runs(u.block), parts = SPANS ? join_spans(u.block) : runs;
     const int64_t base = ((int64_t)unit * a.kv_heads + head) * a.parts * a.max_rows + row;
     const int64_t step = (int64_t)a.max_rows * D;
     const float* po = a.part_o + base * D + lane * W;
@@ -1143,9 +1143,9 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
     auto load_ml = [&](int first, int n) {
         return lane < n ? pml[(int64_t)(first + lane) * a.max_rows] : make_float2(-INFINITY, 0.0f);
     };
-    const int shared = PREFIX ? a.prefix[unit].z / kSpan : 0;
+    const int shared = PREFIX ? join_shared(u.block, a.prefix[unit].z) : 0;
     // First partial result of the run that begins at span s.
-    auto run_begin = [&](int s) { return PREFIX && shared > s ? min(shared, s + kRun) - 1 : s; };
+    auto run_begin = [&](int s) { return PREFIX ? join_run_begin(s, shared) : s; };
     float M = -INFINITY, L = 0.0f, o[W];
 #pragma unroll
     for (int i = 0; i < W; ++i) o[i] = 0.0f;
@@ -1207,7 +1207,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
     } else {
         int first_run = 0;
         if (PREFIX) {                    // the runs that are one partial result each
-            first_run = shared / kRun < 2 ? 0 : min(shared / kRun, runs);
+            first_run = join_whole_runs(shared);
             for (int r0 = 0; r0 < first_run; r0 += kJoin) {
                 const int n = min(kJoin, first_run - r0), s0 = r0 * kRun + kRun - 1;
                 const float2 ml = lane < n ? pml[(int64_t)(s0 + lane * kRun) * a.max_rows] : make_float2(-INFINITY, 0.0f);

@@ -15,10 +15,11 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "jetfp8_join.h"
+
 namespace jetfp8 {
 
 constexpr int kKvBlock = 64;       // tokens of a block
-constexpr int kKvSpan = 8;         // blocks of a span, the attention's unit of summation
 constexpr int kUnitWords = 8;      // int32 words of a work unit's record
 
 // One work unit: the new tokens of one request that fall into one block.

@@ -231,6 +231,25 @@ def test_records_of_other_units(jf):
             same(got[8:], plain[8:])
 
 
+@pytest.mark.parametrize("Hq,H", [(8, 8), (64, 8)])
+def test_records_of_other_units_far(jf, Hq, H):
+    """The same beyond 32768 tokens, where a row has 9 runs and more, with a workspace that ends with the last row's partial
+    results: shared blocks that the unit does not have are bounded by those it has."""
+    c = Case([(600, 4), (34000, 2), (33100, 2)], 0, 1, Hq, H, 128, seed=6)
+    c.plan["units"], c.units = c.plan["units"][:8], c.units[:8].contiguous()       # no unused ones behind them
+    assert len(c.units) * H * ((c.max_seq - 1) // 64) * 128 * 128 >= 1 << 28       # taken apart with a tight max_seq
+    pre, plain = c.prefix(jf), c.run(jf, None, c.max_seq)
+    same(c.run(jf, pre, c.max_seq), plain)
+    own = c.plan["units"][-1, 1]
+    assert own > 512
+    for shared in (own + 8, own + 64, 4096, 1 << 30, 2 ** 31 - 1, -8, -2 ** 31):
+        bad = pre.cpu().numpy().copy()
+        bad[6:, 2] = shared
+        got = c.run(jf, up(bad), c.max_seq)
+        same(got[:6], plain[:6])
+        assert (got[c.T - c.pad:] == 7.0).all()
+
+
 def test_streams_and_graphs(jf):
     """Two calls at once with workspaces of their own, and a captured step: records and attention replayed for other lengths."""
     import torch
