@@ -150,6 +150,43 @@ def test_several_tokens_and_idle_requests(jf, Hq, H, D, new):
         same(c.run(jf, pre, max_seq), plain)
 
 
+def many_parts(c, pre):
+    """Rows of several runs with more partial results than are joined at once: how many, and how many of them with runs that
+    are shared whole."""
+    n = whole = 0
+    for u, rec in zip(c.plan["units"], pre.cpu().numpy()):
+        spans, shared = -(-int(u[1]) // 8), int(rec[2]) // 8
+        if u[0] >= 0 and spans > 8:
+            parts = sum(s >= shared or s % 8 == 7 or s == shared - 1 for s in range(spans))
+            n += parts > 8
+            whole += parts > 8 and shared >= 16
+    return n, whole
+
+
+# (prompt, samples), own tokens, whether runs are shared whole
+MANY = {
+    "long prompts": ([(34000, 5), (40000, 6)], 300, True),
+    "long samples": ([(4608, 6), (8192, 5)], 9000, True),
+    "alone": ([(9000, 1), (1100, 4), (9500, 1), (4096, 5)], 5500, False),
+}
+
+
+@pytest.mark.parametrize("Hq,H,D,new,times", [(4, 2, 128, 1, 1), (16, 1, 64, 2, 1), (32, 1, 64, 1, 7), (16, 1, 128, 2, 7)])
+@pytest.mark.parametrize("kind", MANY)
+def test_rows_of_many_parts(jf, kind, Hq, H, D, new, times):
+    """Rows whose join goes run by run: behind runs that are shared whole, within a run that is shared in part, and of requests
+    that share nothing beside such that do; by four waves a row, and by one (2048 rows and more)."""
+    groups, grown, shares = MANY[kind]
+    c = Case([(n, k * times if k > 1 else k) for n, k in groups], grown, new, Hq, H, D, seed=Hq + new)
+    assert (len(c.units) * Hq * new >= 2048) == (times > 1)
+    pre = c.prefix(jf)
+    n, whole = many_parts(c, pre)
+    assert n >= 2 and (whole >= 2 or not shares)
+    plain = c.run(jf, None, c.max_seq)
+    for max_seq in (c.max_seq, c.far()):
+        same(c.run(jf, pre, max_seq), plain)
+
+
 @pytest.mark.parametrize("Hq,H,D", [(4, 2, 64), (6, 2, 128)])
 def test_against_the_oracle(jf, Hq, H, D):
     import torch
