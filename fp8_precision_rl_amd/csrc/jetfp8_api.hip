@@ -51,6 +51,12 @@ bool attention_dims_ok(int64_t num_units, int64_t max_new, int64_t max_seq, int6
            jetfp8::attention_fits(num_units, max_new, max_seq, q_heads, kv_heads, head_dim, prefix);
 }
 
+// Whether two buffers of the same size share bytes.
+bool overlap(const void* a, const void* b, int64_t bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return (x < y ? y - x : x - y) < static_cast<uintptr_t>(bytes);
+}
+
 bool table_ok(int64_t requests, int64_t max_blocks) {
     return requests >= 1 && requests <= jetfp8::kKvMaxRequests && dim_ok(max_blocks) &&
            dim_ok(JETFP8_KV_BLOCK * max_blocks) && dim_ok(requests * max_blocks);
@@ -373,6 +379,10 @@ int jetfp8_kv_fork(const int32_t* state, const int32_t* block_table, int64_t max
     if (!aligned16(state) || !aligned16(block_table) || !aligned16(parents) || !aligned16(next_state) ||
         !aligned16(next_table))
         return JETFP8_ERR_ALIGN;
+    // in place, a copy could find its parent overwritten
+    if (overlap(state, next_state, requests * 2 * (int64_t)sizeof(int32_t)) ||
+        overlap(block_table, next_table, requests * max_blocks * (int64_t)sizeof(int32_t)))
+        return JETFP8_ERR_SHAPE;
     return hip_status(jetfp8::launch_kv_fork(state, block_table, max_blocks, requests, parents, next_state, next_table,
                                              static_cast<hipStream_t>(stream)));
 }
@@ -404,6 +414,9 @@ int jetfp8_kv_sweep(const int32_t* state, const int32_t* block_table, int64_t ma
     if (!aligned16(state) || !aligned16(block_table) || !aligned16(free_blocks) || !aligned16(free_head) ||
         !aligned16(live) || !aligned16(next_table) || !aligned16(moves) || !aligned16(workspace))
         return JETFP8_ERR_ALIGN;
+    // in place, thread blocks would mark ids that others have written already
+    if (next_table && overlap(block_table, next_table, requests * max_blocks * (int64_t)sizeof(int32_t)))
+        return JETFP8_ERR_SHAPE;
     return hip_status(jetfp8::launch_kv_sweep(state, block_table, max_blocks, requests, num_blocks, free_blocks, free_head,
                                               live, next_table, moves, static_cast<uint64_t*>(workspace),
                                               static_cast<hipStream_t>(stream)));

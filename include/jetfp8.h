@@ -381,7 +381,7 @@ int64_t jetfp8_attention_prefix_workspace(int64_t num_units, int64_t max_new, in
 /* Requests that go on from others: samples of one prompt, beams, resampled rollouts.  parents [requests] int32: request r
  * becomes a copy of request parents[r] as it is now; it stays as it is if that is r or no request, or if one of the two has
  * a recent block other than 0 or 1.  Any map will do, also one in which requests change places.  Writes, to other
- * buffers than the inputs,
+ * buffers than the inputs (JETFP8_ERR_SHAPE if next_state overlaps state, or next_table block_table),
  *   next_state [requests][2]: a copy has its parent's tokens, and the one of its own recent blocks that was not in use;
  *   next_table [requests][max_blocks]: the parent's row (the request's own if it stays), -1 behind its complete blocks.
  * Per layer, jetfp8_kv_fork_recent copies the unfinished blocks.  A copy's former blocks are free after the next sweep. */
@@ -397,7 +397,8 @@ int jetfp8_kv_fork_recent(const int32_t* parents, const int32_t* state, int64_t 
  *                              jetfp8_kv_plan; free_head [1] int32: 0;  live [1] int32: the number L of held blocks.
  * With next_table and moves (both or neither) the cache is compacted: held blocks with ids of L and above, ascending, move
  * to the free ids below L, ascending, and the free list begins with L:
- *   next_table [requests][max_blocks] int32 (not block_table): the tables with the new ids, -1 behind the complete blocks;
+ *   next_table [requests][max_blocks] int32: the tables with the new ids, -1 behind the complete blocks; JETFP8_ERR_SHAPE
+ *                              if it overlaps block_table;
  *   moves [max(1, num_blocks / 2)][2] int32: from, to; unused ones -1, -1.  Per layer, jetfp8_kv_move carries them out.
  * num_blocks <= 2^18.  workspace: jetfp8_kv_sweep_workspace() bytes (0: none). */
 int jetfp8_kv_sweep(const int32_t* state, const int32_t* block_table, int64_t max_blocks, int64_t requests,

@@ -273,3 +273,29 @@ def test_binding_refusals(jf):
         jf.kv_sweep(i(2, 2), i(2, 8), (1 << 18) + 1)
     with pytest.raises(jf.JetFP8Error):
         jf.kv_fork_recent(i(4), i(4, 2), torch.zeros((7, 1, 2, 64 * 64), dtype=torch.bfloat16, device="cuda"))
+
+
+@pytest.mark.parametrize("R,W", [(8, 16), (70, 128)])
+def test_tables_side_by_side(jf, R, W):
+    """The tables before and after may be neighbours in one buffer; in place they are refused and nothing is written."""
+    import torch
+    rng = np.random.default_rng(4)
+    state = np.stack([rng.integers(0, 64 * W, R), rng.integers(0, 2, R)], 1).astype(np.int32)
+    table = rng.integers(0, 300, (R, W)).astype(np.int32)
+    parents = rng.integers(-1, R, R).astype(np.int32)
+    both, states = torch.zeros((2, R, W), dtype=torch.int32, device="cuda"), torch.zeros((2, R, 2), dtype=torch.int32, device="cuda")
+    both[0], states[0] = up(table), up(state)
+    new = lambda *s: torch.empty(s, dtype=torch.int32, device="cuda")
+    free, head, live, moves = new(300), new(1), new(1), new(150, 2)
+    ws = torch.empty(max(16, jf.kv_sweep_workspace(R, W, 300)), dtype=torch.uint8, device="cuda")
+    jf.jetfp8_kv_fork(states[0], both[0], W, R, up(parents), states[1], both[1])
+    s, t = ro.fork(state, table, parents)
+    assert np.array_equal(states[1].cpu().numpy(), s) and np.array_equal(both[1].cpu().numpy(), t)
+    jf.jetfp8_kv_sweep(states[0], both[0], W, R, 300, free, head, live, both[1], moves, ws)
+    assert np.array_equal(both[1].cpu().numpy(), ro.sweep(state, table, 300, True)["next_table"])
+    for f in (lambda: jf.jetfp8_kv_fork(states[0], both[0], W, R, up(parents), states[0], both[1]),
+              lambda: jf.jetfp8_kv_fork(states[0], both[0], W, R, up(parents), states[1], both[0]),
+              lambda: jf.jetfp8_kv_sweep(states[0], both[0], W, R, 300, free, head, live, both[0], moves, ws)):
+        with pytest.raises(jf.JetFP8Error):
+            f()
+    assert np.array_equal(both[0].cpu().numpy(), table) and np.array_equal(states[0].cpu().numpy(), state)

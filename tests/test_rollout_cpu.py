@@ -146,6 +146,20 @@ def test_sweep_and_move_refusals(lib):
         assert move(**kw) == SHAPE, kw
 
 
+def test_fork_and_sweep_in_place_are_refused(lib):
+    """Both read tables that other thread blocks would be overwriting."""
+    Q = 4 * P                                                # far from the buffers at P: 4 requests of 8 blocks, 128 bytes
+    fork = lambda ns, nt: lib.jetfp8_kv_fork(2 * P, P, 8, 4, 3 * P, ns, nt, None)
+    for at in (-16, 0, 16):
+        assert fork(2 * P + at, Q) == SHAPE
+    for at in (-112, 0, 16, 112):
+        assert fork(Q, P + at) == SHAPE
+        assert lib.jetfp8_kv_sweep(2 * P, P, 8, 4, 100, Q, Q + 512, Q + 528, P + at, Q + 1024, None, 0, None) == SHAPE
+    # tables of more than 2^31 bytes
+    assert lib.jetfp8_kv_fork(P, 2 * P, 1 << 20, 1024, P, 1 << 40, 2 * P + (1 << 32) - 16, None) == SHAPE
+    assert lib.jetfp8_kv_sweep(P, 2 * P, 1 << 20, 1024, 100, P, P, P, 2 * P + (1 << 32) - 16, P, P, 1 << 40, None) == SHAPE
+
+
 def test_binding_refuses_host_tensors():
     import torch
     import fp8_precision_rl_amd as jf
