@@ -37,7 +37,8 @@ struct NormBackArgs {
 // A team of WPR waves takes a row, TEAMS of them in a thread block take rows in turn.  A wave's k-th chunk covers 512
 // columns, lane l columns 8 l .. + 7 of it, as in the forward kernel; what a lane holds of dy, h and dres is loaded once,
 // the row's sum meets in LDS (two buffers, so one barrier a row), and each lane keeps the column sums of its columns in
-// registers over all rows of its thread block.
+// registers over all rows of its thread block.  h enters as h r alone, whose size is that of 1: g h overflows fp32 and r^2
+// underflows for rows that bf16 and the forward pass still hold.
 template <int HCH, int WPR, int TEAMS>
 __global__ __launch_bounds__(WPR * TEAMS * 64) void rmsnorm_backward_kernel(NormBackArgs a) {
     __shared__ float sums[2][TEAMS][WPR];
@@ -82,8 +83,8 @@ __global__ __launch_bounds__(WPR * TEAMS * 64) void rmsnorm_backward_kernel(Norm
                            g[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                sum = fmaf(lo_of(y[i]) * lo_of(g[i]), lo_of(x[i]), sum);
-                sum = fmaf(hi_of(y[i]) * hi_of(g[i]), hi_of(x[i]), sum);
+                sum = fmaf(lo_of(y[i]) * lo_of(g[i]), lo_of(x[i]) * r, sum);
+                sum = fmaf(hi_of(y[i]) * hi_of(g[i]), hi_of(x[i]) * r, sum);
             }
         }
         sum = wave_sum(sum);
@@ -94,7 +95,7 @@ __global__ __launch_bounds__(WPR * TEAMS * 64) void rmsnorm_backward_kernel(Norm
 #pragma unroll
             for (int p = 1; p < WPR; ++p) sum += sums[buf][team][p];
         }
-        const float c = r * (r * (sum * inv_cols));       // (r * r may underflow)
+        const float mean = sum * inv_cols;
 #pragma unroll
         for (int k = 0; k < HCH; ++k) {
             const uint32_t y[4] = {dy[k].x, dy[k].y, dy[k].z, dy[k].w}, x[4] = {h[k].x, h[k].y, h[k].z, h[k].w},
@@ -102,12 +103,13 @@ __global__ __launch_bounds__(WPR * TEAMS * 64) void rmsnorm_backward_kernel(Norm
             uint32_t out[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float a0 = fmaf(r, fmaf(-lo_of(x[i]), c, lo_of(y[i]) * lo_of(g[i])), lo_of(d[i]));
-                const float a1 = fmaf(r, fmaf(-hi_of(x[i]), c, hi_of(y[i]) * hi_of(g[i])), hi_of(d[i]));
+                const float n0 = lo_of(x[i]) * r, n1 = hi_of(x[i]) * r;
+                const float a0 = fmaf(r, fmaf(-n0, mean, lo_of(y[i]) * lo_of(g[i])), lo_of(d[i]));
+                const float a1 = fmaf(r, fmaf(-n1, mean, hi_of(y[i]) * hi_of(g[i])), hi_of(d[i]));
                 const bf16x2 b = {(__bf16)a0, (__bf16)a1};
                 out[i] = __builtin_bit_cast(uint32_t, b);
-                dw[k][2 * i] = fmaf(lo_of(y[i]), lo_of(x[i]) * r, dw[k][2 * i]);
-                dw[k][2 * i + 1] = fmaf(hi_of(y[i]), hi_of(x[i]) * r, dw[k][2 * i + 1]);
+                dw[k][2 * i] = fmaf(lo_of(y[i]), n0, dw[k][2 * i]);
+                dw[k][2 * i + 1] = fmaf(hi_of(y[i]), n1, dw[k][2 * i + 1]);
             }
             if (live && ok[k])
                 *reinterpret_cast<uint4*>(a.dx + row * a.cols + col[k]) = make_uint4(out[0], out[1], out[2], out[3]);

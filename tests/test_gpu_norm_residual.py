@@ -146,6 +146,24 @@ def test_backward(jf, R, C, dres):
     assert torch.equal(place, dx)
 
 
+@pytest.mark.parametrize("R,C", [(9, 128), (6, 2176), (40, 5120), (5, 8192)])
+def test_backward_of_rows_of_every_size(jf, R, C):
+    """Rows as large and as small as bf16 and the forward pass hold, with gradients with which dy * w * h, or its sum over the
+    row, leaves fp32's range; the results do not."""
+    import torch
+    rng = np.random.default_rng(C)
+    size = np.exp2(rng.permutation(np.linspace(-120, 125, R)))[:, None]
+    hb, wb = f32_to_bits(rng.standard_normal((R, C)).clip(-4, 4) * size), f32_to_bits(1 + 0.1 * rng.standard_normal(C))
+    dyb, db = f32_to_bits(2.0 ** 20 * rng.standard_normal((R, C))), f32_to_bits(rng.standard_normal((R, C)) / size.clip(min=1))
+    h = value(hb)
+    rstd = (1 / np.sqrt((h * h).mean(1) + 1e-5)).astype(np.float32)
+    dx, dw = jf.rmsnorm_backward(bits_to_dev(dyb), bits_to_dev(hb), bits_to_dev(wb), torch.from_numpy(rstd).cuda(), bits_to_dev(db))
+    want, bound, want_w, bound_w = ro.rmsnorm_backward(value(dyb), h, value(wb), rstd.astype(np.float64), value(db))
+    err = np.abs(value(dev_to_bits(dx)) - want)
+    assert (err <= bound + (np.abs(want) + bound) * 2.0 ** -8).all()
+    assert (np.abs(dw.cpu().numpy() - want_w) <= bound_w + (np.abs(want_w) + bound_w) * 2.0 ** -24).all()
+
+
 def test_backward_against_differences(jf):
     """The gradient of sum(dy y) for y the norm of x + residual, against differences of that sum in float64: their step is
     chosen so that the third derivative's part stays below the gradient's rounding."""
