@@ -61,6 +61,23 @@ def test_against_float64(jf, T, H, D, P, far, interleaved, inverse):
     assert np.array_equal(after[:, :8], wide[:, :8]) and np.array_equal(after[:, 8 + H * D:], wide[:, 8 + H * D:])
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("H,D", [(3, 16), (2, 32)])
+@pytest.mark.parametrize("T", [65535, 65536 + 9, 131071, 131072, 131072 + 37])
+def test_narrow_heads_of_many_tokens(jf, T, H, D, interleaved):
+    """8 pairs: up to 32 tokens to a thread block, from 131072 tokens on, the last of them with fewer."""
+    import torch
+    rng = np.random.default_rng(T)
+    x = f32_to_bits(rng.standard_normal((T, H, D)))
+    pos = rng.integers(-1, 1 << 20, T).astype(np.int32)
+    freqs = 10000.0 ** (-np.arange(8) / 8)
+    dev, p, f = bits_to_dev(x), torch.from_numpy(pos).cuda(), torch.from_numpy(freqs).cuda()
+    out = torch.full((T, H, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    y = jf.rotary(dev, p, f, interleaved=interleaved, inverse=interleaved, out=out)
+    check(dev_to_bits(y), value(x), pos, freqs, interleaved, 1.0, interleaved)
+    assert (y[torch.from_numpy(pos < 0).cuda()] == 7.0).all()
+
+
 @pytest.mark.parametrize("T", [6, 5000])
 def test_rows_without_a_position_are_left(jf, T):
     import torch
