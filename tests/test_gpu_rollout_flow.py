@@ -193,3 +193,92 @@ def test_training_step(stack):
         diff = (loss(h0, w0 + e * u) - loss(h0, w0 - e * u)) / (2 * e)
         got = (dw.double() * u).sum()
         assert (got - diff).abs() <= (size * (h0 * r * u).abs()).sum()
+
+
+def test_training_step_gradients(stack):
+    """The same step element by element.  Each operator's output against float64 from what it was given, then the whole chain:
+    dx and dw from the codes of dz, off by DGrad's rounding (2^-8 of a value, and by the matrix instruction's cuts at most 7 of
+    2^-13 of each block's largest product, taken twice here: 2^-9 of the sum of the products' sizes) and the norm's own; and
+    from dy, off by those and the codes of dz (2^-4 of each), by norms: a row's map from dn to dx is no longer than rstd times
+    the largest weight, DGrad's no longer than the weights' largest singular value.  Gradients with a mistake in them leave
+    these bounds, which float64 differences show to lie around the function's gradient."""
+    import torch
+    jf, _, freqs = stack
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+    T, heads, P = 128, 2, len(freqs)
+    rnd = lambda *s: torch.randn(s, device="cuda", generator=g).to(torch.bfloat16)
+    x, res, w, W = rnd(T, DM), rnd(T, DM), (1 + 0.1 * rnd(DM)).to(torch.bfloat16), (rnd(heads * HD, DM) * DM ** -0.5).to(torch.bfloat16)
+    wq, ws, wqT = jf.quantize_blocks(W)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda") * 3
+    _, _, rstd, h = jf.rmsnorm_add_quantize(x, res, w, EPS)
+    dy, dres = rnd(T, heads, HD), rnd(T, DM)
+    dz = jf.rotary(dy, pos, freqs, inverse=True).view(T, -1)
+    dq, ds = jf.quantize_rows(dz)
+    dn = jf.gemm_dgrad(dq, ds, wqT, ws)
+    dx, dw = jf.rmsnorm_backward(dn, h, w, rstd, dres)
+
+    deq = wq.view(torch.float8_e4m3fn).double() * ws.double().repeat_interleave(128, 0).repeat_interleave(128, 1)
+    codes = dq.view(torch.float8_e4m3fn).double() * ds.double().t().repeat_interleave(128, 1)
+    angle = pos.double()[:, None] * freqs
+    c, s = angle.cos()[:, None], angle.sin()[:, None]
+    n, r, wd = h.double() * rstd.double()[:, None], rstd.double()[:, None], w.double()
+
+    def turned(v, s):
+        a, b = v[..., :P], v[..., P:2 * P]
+        return torch.cat([a * c - b * s, b * c + a * s, v[..., 2 * P:]], -1)
+
+    def norm_back(d, mean=True, stream=True):
+        t = d * wd
+        return r * (t - mean * n * (t * n).mean(1, keepdim=True)) + stream * dres.double(), (d * n).sum(0)
+
+    def norm_size(e):                   # of an error e in dn: in dx, in dw
+        return r * (e * wd.abs() + n.abs() * (e * wd.abs() * n.abs()).mean(1, keepdim=True)), (e * n.abs()).sum(0)
+
+    # each operator by itself: rotary, codes, DGrad, norm
+    z = turned(dy.double(), -s).view(T, -1)
+    assert ((dz.double() - z).abs() <= 2.0 ** -8 * z.abs() + 2.0 ** -20 * dy.double().abs().amax()).all()
+    step = torch.maximum(dz.double().abs() * (2.0 ** -4 + 2.0 ** -20), 2.0 ** -10 * ds.double().t().repeat_interleave(128, 1))
+    assert ((codes - dz.double()).abs() <= step).all()
+    exact, most = codes @ deq, (codes.abs() @ deq.abs()) * 2.0 ** -9
+    most = most + 2.0 ** -8 * (exact.abs() + most)
+    assert ((dn.double() - exact).abs() <= most).all()
+    fx, fw = norm_back(dn.double())
+    sx, sw = norm_size(dn.double().abs())
+    assert ((dx.double() - fx).abs() <= 2.0 ** -8 * fx.abs() + 2.0 ** -17 * (sx + dres.double().abs())).all()
+    assert ((dw.double() - fw).abs() <= 2.0 ** -17 * sw).all()
+
+    # from the codes of dz
+    ex, ew = norm_size(most)
+
+    def check(pair):
+        a, b = pair
+        return (bool(((dx.double() - a).abs() <= ex + 2.0 ** -7 * (a.abs() + ex)).all()),
+                bool(((dw.double() - b).abs() <= ew + 2.0 ** -16 * sw).all()))
+
+    assert check(norm_back(exact)) == (True, True)
+    assert check(norm_back(-exact)) == (False, False) and check(norm_back(0 * exact)) == (False, False)
+    assert not check(norm_back(exact, mean=False))[0] and not check(norm_back(exact, stream=False))[0]
+    assert check(norm_back(turned(dy.double(), s).view(T, -1) @ deq)) == (False, False)       # turned the wrong way
+
+    # from dy
+    gx, gw = norm_back(z @ deq)
+    off = (codes - z).norm(dim=1) * torch.linalg.matrix_norm(deq, 2) + most.norm(dim=1)       # of a row of dn
+    assert ((codes - z).norm(dim=1) <= (2.0 ** -4 + 2.0 ** -7) * z.norm(dim=1)).all()
+    limit = r[:, 0] * wd.abs().max() * off + 2.0 ** -7 * gx.norm(dim=1)
+    miss = lambda a: (dx.double() - a).norm(dim=1)
+    assert (miss(gx) <= limit).all()
+    wrong = [norm_back(-(z @ deq))[0], dres.double(), gx - dres.double()]
+    assert all((miss(a) > limit).all() for a in wrong)
+    e = 1e-4
+
+    def loss(h, w):
+        y = turned(((h * (h.square().mean(1, keepdim=True) + EPS).rsqrt() * w) @ deq.t()).view(T, heads, HD), s)
+        return (y * dy.double()).sum() + (h * dres.double()).sum()
+
+    for _ in range(4):                  # the step's square, times a third derivative of about 1, is 1e-8
+        v, u = (torch.randn(t.shape, device="cuda", generator=g, dtype=torch.float64) for t in (h, w))
+        diff = (loss(h.double() + e * v, wd) - loss(h.double() - e * v, wd)) / (2 * e)
+        assert (diff - (gx * v).sum()).abs() <= 1e-5 * (gx * v).norm()
+        diff = (loss(h.double(), wd + e * u) - loss(h.double(), wd - e * u)) / (2 * e)
+        assert (diff - (gw * u).sum()).abs() <= 1e-5 * (gw * u).norm()
