@@ -1288,6 +1288,29 @@ double attn_waves(const AttnShape& s, int64_t num_units, int64_t kv_heads) {
     return (double)num_units * kv_heads * ((s.max_rows + 31) / 32);
 }
 
+// Whether blocks that units share are taken apart, which costs about 40 us for its launches and their chains of loads, 30 with 64
+// channels, however little there is to do.  Without, a call finds shared blocks in the last level of cache, so what decides
+// is how much it may read in all.  Below, us apart against not, 8 kv heads, all but 50 to 200 tokens of the contexts shared,
+// means over groups from two requests to all.
+//   Up to 16 rows a unit, 128 channels (4 rows): 32 requests at 4060 (256 MiB) 41 / 27, at 5148 (324) 42 / 34, at 6620 (416) 45 / 47,
+// at 8860 (556) 45 / 64; 64 requests at 3228 (408) 41 / 43, at 4380 (552) 47 / 58; 256 at 9200 146 / 421.  Long rows cost more to
+// join otherwise: 2 requests at 66460 (260 MiB) 50 / 59, 4 at 42140 (330) 50 / 58, 8 at 16540 (259) 43 / 44, but 16 at 8220
+// (258) 42 / 38.  64 channels (2 rows): 16 requests at 16540 (259) 30 / 33, 64 at 4060 (256) 32 / 28, at 5148 (324) 32 / 35.
+//   Contexts of few spans have little to share: 256 requests at 988 (512 MiB) 65 / 56, at 1500 (768) 69 / 73; 512 at 668 (704) 94 / 85.
+//   17 to 32 rows fill a wave by themselves, and few units of those are read as fast without (32 rows, 32 requests at 5148 (658 MiB)
+// 67 / 54, at 20000 (2540) 153 / 159; 48 at 6000 (1140) 86 / 92).  More units would take the tile kernel, which is slower than
+// spans are here: 64 requests at 1500 59 / 61, at 2524 71 / 94, 256 at 4400 300 / 690; with 64 channels not before 3000: 256 requests
+// at 2000 142 / 105, 64 at 3100 62 / 64, at 5148 70 / 144.  Beyond 32 rows the partial results are several times as many
+// (measured once: 2 prompts of 16 samples, 16 tokens of 8 query heads 132 / 156).
+//   What is shared is known on the device only.  Where that is one span of a long context, a call loses by its records: 128
+// requests with 8000 tokens of their own 225 / 210, with 64 channels 131 / 105.
+bool takes_apart(const AttnShape& s, int64_t num_units, int64_t kv_heads, int64_t D) {
+    if (s.max_rows > 32 || s.max_blocks < 24) return false;
+    const double mib = (double)num_units * kv_heads * s.max_blocks * (2 * kKvBlock) * D / (1 << 20);
+    if (s.max_rows <= 16) return mib >= (D == 64 || s.max_blocks >= 256 ? 256 : 384);
+    return attn_waves(s, num_units, kv_heads) >= 1024 ? D == 128 || s.max_blocks >= 48 : mib >= 1024;
+}
+
 AttnShape attn_shape(int64_t num_units, int64_t max_new, int64_t max_seq, int64_t q_heads, int64_t kv_heads, int64_t D,
                      bool prefix) {
     AttnShape s;
@@ -1299,14 +1322,7 @@ AttnShape attn_shape(int64_t num_units, int64_t max_new, int64_t max_seq, int64_
     // the tile kernel if that has enough waves (32 rows each) for the chip's 1024 SIMDs: below, spans in parallel win (256
     // tokens at 4096, 320 waves: 54 against 106 us), at 1072 and 1472 waves the two are within 5 %, above the
     // partial results cost more than they bring (16 times 64 tokens at 4096, 3008 waves: 157 against 109 us).
-    // Shared blocks are taken apart where the call may read more than the last level of cache holds, 256 MB; below, it finds
-    // them there, and waiting for one kernel after the other costs more than it saves (8 kv heads of 128, us apart against
-    // not: 8 samples at 2300 25 / 12, 32 samples at 8700 36 / 58, 32 requests at 4600 34 / 26, 64 requests at 2500 34 / 39, 256
-    // requests at 9200 146 / 421).  And where a unit's rows do not fill the 32 of a wave several times by themselves (8
-    // query heads each, 128 requests at 8700: 2 tokens 128 / 240, 4 tokens 256 / 386; 2 prompts of 16 samples, 16 tokens 132 / 156,
-    // with partial results of twice the size).
-    s.prefix = prefix && s.max_rows <= 32 &&
-               (double)num_units * kv_heads * s.max_blocks * (2 * kKvBlock) * D >= (double)(1 << 28);
+    s.prefix = prefix && takes_apart(s, num_units, kv_heads, D);
     s.split = spans > 0 && (s.prefix || s.max_rows <= 16 || attn_waves(s, num_units, kv_heads) < 1024);
     s.rows = s.split && s.max_rows <= 16 ? 16 : 32;
     s.row_groups = (s.max_rows + s.rows - 1) / s.rows;
