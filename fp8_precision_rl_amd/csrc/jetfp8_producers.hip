@@ -390,9 +390,13 @@ hipError_t launch_norm(const uint16_t* x, const uint16_t* res, const uint16_t* w
     const dim3 block(RN_WAVES * 64);
     const dim3 grid1((unsigned)((R + RN_WAVES - 1) / RN_WAVES)), grid2((unsigned)((R + RN_WAVES / 2 - 1) / (RN_WAVES / 2)));
     const int nch = (int)((C + 511) / 512);
-    // (us with the addition, a thread block a row against the other: 32 rows of 5120 5.0 / 8.2, 256 rows 5.9 / 8.7, 512 8.9 / 9.2, 1024
-    // 14.7 / 11.3; of 2048 3.4 / 6.7, 512 rows 4.4 / 7.3, 2048 rows 8.9 / 9.0)
-    if (R <= 512) {
+    // A thread block a row, up to 512 rows; with 16 waves to a row up to 256, one to a CU; below 512 columns not at all, where
+    // its waves have lanes without columns.  (us against the other form, with the addition / without: 32 rows of
+    // 5120 5.2 : 8.3 / 5.4 : 7.6, 256 6.9 : 9.5 / 6.5 : 8.6, 512 10.1 : 10.4 / 9.1 : 9.1, 1024 16.0 : 13.1 / 14.5 : 10.4; of 8192 32 rows
+    // 7.3 : 11.5 / 7.3 : 10.4, 256 9.7 : 13.2 / 9.0 : 11.6, 272 13.9 : 13.2 / 12.6 : 11.6; of 512 32 rows 3.2 : 3.8 / 3.4 : 3.6; of 256 3.6 : 3.7 /
+    // 3.6 : 3.4, 512 4.2 : 4.0 / 4.1 : 3.8.  Up to 2048 columns the forms meet later: 1024 rows of 2048 7.2 : 9.1 / 6.4 : 7.7, 2048
+    // 10.3 : 11.1 / 8.7 : 8.7.)
+    if (C >= 512 && R <= (nch > 12 ? 256 : 512)) {
         const unsigned grid = (unsigned)R;
         if (nch <= 2) rmsnorm_row_kernel<0, 2, ADD><<<grid, 2 * 64, 0, st>>>(x, res, w, R, C, eps, h, q, s, rstd, y);
         else if (nch <= 4) rmsnorm_row_kernel<0, 4, ADD><<<grid, 4 * 64, 0, st>>>(x, res, w, R, C, eps, h, q, s, rstd, y);

@@ -89,6 +89,24 @@ def test_a_row_does_not_depend_on_the_call(jf, C):
             assert torch.equal(have, want)
 
 
+@pytest.mark.parametrize("C", [128, 384, 512, 6144, 6272, 8192])
+def test_rows_beside_the_forms_borders(jf, C):
+    """The same bits for 255 to 513 rows, on both sides of the row form's borders in rows and columns."""
+    import torch
+    g = torch.Generator(device="cuda")
+    g.manual_seed(C + 1)
+    x, res = (torch.randn((513, C), device="cuda", generator=g).to(torch.bfloat16) for _ in range(2))
+    w = (1 + 0.1 * torch.randn((C,), device="cuda", generator=g)).to(torch.bfloat16)
+    whole, plain = jf.rmsnorm_add_quantize(x, res, w, 1e-5, return_y=True), jf.rmsnorm_quantize(x, w, 1e-5, return_y=True)
+    for n in (255, 256, 257, 512):
+        part = jf.rmsnorm_add_quantize(x[:n].contiguous(), res[:n].contiguous(), w, 1e-5, return_y=True)
+        for have, want in zip(part, (whole[0][:n], whole[1][:, :n], whole[2][:n], whole[3][:n], whole[4][:n])):
+            assert torch.equal(have, want)
+        part = jf.rmsnorm_quantize(x[:n].contiguous(), w, 1e-5, return_y=True)
+        for have, want in zip(part, (plain[0][:n], plain[1][:, :n], plain[2][:n], plain[3][:n])):
+            assert torch.equal(have, want)
+
+
 @pytest.mark.parametrize("where", ["x", "residual"])
 @pytest.mark.parametrize("R,C", [(5, 128), (70, 5120)])
 def test_forward_in_place(jf, R, C, where):
