@@ -27,6 +27,11 @@ constexpr int join_run_begin(int span, int shared) {
     return shared <= span ? span : (shared < end ? shared : end) - 1;
 }
 
+// Partial results of a row but its own block's.
+constexpr int join_parts_of(int block, int shared) {
+    return join_spans(block) - shared + (shared + kKvRun - 1) / kKvRun;
+}
+
 // Leading runs that are taken as one partial result each, the last of their spans'; below two they are as quick one by one.
 constexpr int join_whole_runs(int shared) { return shared / kKvRun < 2 ? 0 : shared / kKvRun; }
 

@@ -27,6 +27,14 @@ static int whole_of(int shared, int runs) {
 #endif
 }
 
+static bool few_parts(int block, int shared) {
+    const int runs = join_runs(block);
+#ifdef UNBOUNDED
+    if (runs > kKvRun) return false;               // (the number of parts means nothing)
+#endif
+    return runs > 1 && join_parts_of(block, shared) < kKvRun + 1;
+}
+
 // The three ways of attention_join_kernel: few parts at once, one sequence, run by run.
 static std::vector<int> walk(int block, int recorded) {
     const int runs = join_runs(block), spans = join_spans(block), shared = shared_of(block, recorded);
@@ -34,13 +42,7 @@ static std::vector<int> walk(int block, int recorded) {
     auto take = [&](int first, int n, int step) {
         for (int s = 0; s < n; ++s) at.push_back(first + s * step);
     };
-    int few = 0;
-    if (runs > 1 && runs < kKvRun + 1) {
-        for (int r = 0; r < runs; ++r)
-            few += std::max(std::min((r + 1) * kKvRun, spans) - join_run_begin(r * kKvRun, shared), 0);
-        few = few < kKvRun + 1 && few > 0 ? few + 1 : 0;
-    }
-    if (few) {
+    if (few_parts(block, shared)) {
         for (int r = 0; r < runs; ++r) {
             const int begin = join_run_begin(r * kKvRun, shared);
             take(begin, std::min((r + 1) * kKvRun, spans) - begin, 1);
@@ -88,7 +90,8 @@ int main() {
         for (int recorded = 0; recorded <= 64 * 22; ++recorded) check(recorded);
         for (int recorded : odd) check(recorded);
         for (int recorded = 0; recorded <= block; recorded += 8)
-            if (walk(block, recorded) != written(block, recorded)) {
+            if (walk(block, recorded) != written(block, recorded) ||
+                join_parts_of(block, recorded / 8) + 1 != (int)written(block, recorded).size()) {
                 if (bad++ < 5) std::printf("%d blocks, %d shared: other parts than those written\n", block, recorded);
             }
     }
