@@ -73,7 +73,7 @@ __global__ __launch_bounds__(kThreads) void kv_positions_kernel(const KvUnit* __
 }
 
 // ------------------------------------------------------------------------------------------------ shared prompts
-constexpr int kPrefixRows = 8, kWaves = kThreads / 64;      // rows that a wave compares at once
+constexpr int kPrefixRows = 8, kFewRows = 2, kWaves = kThreads / 64;      // rows that a wave compares at once
 
 struct PrefixArgs {
     const KvUnit* units;
@@ -99,10 +99,40 @@ __device__ __forceinline__ int first_unit(const PrefixArgs& a, int r) {
     return lo;
 }
 
+// How many entries the tables of units u0 + 1 .. used - 1 have in common with `first`, of its first `limit` (and no more than
+// *common): a wave compares N rows at once.
+template <int N>
+__device__ __forceinline__ void compare_rows(const PrefixArgs& a, int u0, int used, int limit, const int* first, int* common) {
+    const int lane = threadIdx.x % 64;
+    for (int k0 = u0 + 1 + threadIdx.x / 64; k0 < used; k0 += N * kWaves) {
+        const int* row[N];
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int q = a.units[min(k0 + i * kWaves, used - 1)].request;
+            const bool fits = q >= 0 && q < a.requests;
+            bad |= !fits;
+            row[i] = fits ? a.table + (int64_t)q * a.width : first;
+        }
+        int same = bad ? 0 : limit;
+        for (int j = 0; j < same; j += 64) {
+            const int at = min(j + lane, limit - 1), id = first[at];
+            bool other = false;
+#pragma unroll
+            for (int i = 0; i < N; ++i) other |= row[i][at] != id;
+            const uint64_t differ = __ballot(j + lane < limit && other);
+            if (differ) same = j + __builtin_ctzll(differ);
+        }
+        if (lane == 0 && same < limit) atomicMin(common, same);
+    }
+}
+
 // A thread block for each request; that of a group's first request (or of one without a group) takes the group: its units,
 // the earliest of their blocks, and how many entries of their tables agree before that.  The time is that of chains of two
 // dependent loads, so a wave compares several rows at once (us, a row against eight, 128 blocks: a group of 64 requests 12.6 /
-// 6.0, of 512 80 / 29, of 4096 635 / 208; 16 groups of 16 6.7 / 5.8; 4 groups of 8 with 32 blocks 4.5 / 5.0).
+// 6.0, of 512 80 / 29, of 4096 635 / 208; 16 groups of 16 6.7 / 5.8), but two where that takes them all, up to 9 units, instead of
+// loading the last one several times (two against eight: 4 groups of 8 with 32 blocks 4.0 / 4.6, with 128 blocks 4.1 / 4.8;
+// 32 groups of 2 4.1 / 4.7).
 __global__ __launch_bounds__(kThreads) void kv_prefix_kernel(PrefixArgs a) {
     __shared__ int waves[kThreads / 64], common;
     const int r = blockIdx.x, id = a.groups[r];
@@ -128,30 +158,11 @@ __global__ __launch_bounds__(kThreads) void kv_prefix_kernel(PrefixArgs a) {
         limit = max(block_min(limit, waves), 0);
         if (threadIdx.x == 0) common = limit;
         __syncthreads();
-        const int lane = threadIdx.x % 64, lead = a.units[u0].request;
+        const int lead = a.units[u0].request;
         const bool known = lead >= 0 && lead < a.requests;
         const int* first = a.table + (int64_t)(known ? lead : 0) * a.width;
-        for (int k0 = u0 + 1 + threadIdx.x / 64; known && k0 < used; k0 += kPrefixRows * kWaves) {
-            const int* row[kPrefixRows];
-            bool bad = false;
-#pragma unroll
-            for (int i = 0; i < kPrefixRows; ++i) {
-                const int q = a.units[min(k0 + i * kWaves, used - 1)].request;
-                const bool fits = q >= 0 && q < a.requests;
-                bad |= !fits;
-                row[i] = fits ? a.table + (int64_t)q * a.width : first;
-            }
-            int same = bad ? 0 : limit;
-            for (int j = 0; j < same; j += 64) {
-                const int at = min(j + lane, limit - 1), id = first[at];
-                bool other = false;
-#pragma unroll
-                for (int i = 0; i < kPrefixRows; ++i) other |= row[i][at] != id;
-                const uint64_t differ = __ballot(j + lane < limit && other);
-                if (differ) same = j + __builtin_ctzll(differ);
-            }
-            if (lane == 0 && same < limit) atomicMin(&common, same);
-        }
+        if (known && used - u0 - 1 <= kFewRows * kWaves) compare_rows<kFewRows>(a, u0, used, limit, first, &common);
+        else if (known) compare_rows<kPrefixRows>(a, u0, used, limit, first, &common);
         if (!known && threadIdx.x == 0) common = 0;          // units of another call
         __syncthreads();
         shared = common / kKvSpan * kKvSpan;
