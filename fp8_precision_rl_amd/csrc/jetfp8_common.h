@@ -1,4 +1,4 @@
-// Device helpers shared by the gfx950 kernels of libjetfp8 (quantize and GEMM).
+// Device helpers shared by the gfx950 kernels of libjetfp8.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -12,6 +12,38 @@ __device__ __forceinline__ float bf16_to_f32(uint32_t b16) { return __uint_as_fl
 __device__ __forceinline__ uint32_t f32_to_bf16_rne(float f) {
     uint32_t u = __float_as_uint(f);
     return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
+}
+
+// Two fp32 values rounded to bf16, nearest even, packed low / high: one V_CVT_PK_BF16_F32.  It equals
+// f32_to_bf16_rne on every finite fp32 pattern (all 2^32 - 2^24 of them compared on gfx950, with the
+// library's denormal mode).
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ uint32_t bf16x2_rne(float a, float b) {
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){a, b}, bf16x2_t));
+}
+
+// Eight bf16 values as a lane loads them, and the i-th of them.
+__device__ __forceinline__ uint4 ld16(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
+    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+__device__ __forceinline__ float elem_of(const uint4& v, int i) {
+    const uint32_t w = word_of(v, i >> 1);
+    return bf16_to_f32((i & 1) ? (w >> 16) : (w & 0xFFFFu));
+}
+
+// Eight fp32 values rounded to bf16.
+__device__ __forceinline__ uint4 bf16x8_rne(const float (&f)[8]) {
+    return make_uint4(bf16x2_rne(f[0], f[1]), bf16x2_rne(f[2], f[3]), bf16x2_rne(f[4], f[5]), bf16x2_rne(f[6], f[7]));
+}
+
+// Wave-wide sum (xor butterfly over the 64 lanes; every lane ends with the total).
+template <class T>
+__device__ __forceinline__ T wave_sum(T v) {
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
+    return v;
 }
 
 // Per-group quantization constants.

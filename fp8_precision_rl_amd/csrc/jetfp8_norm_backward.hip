@@ -13,18 +13,6 @@ namespace jetfp8 {
 
 namespace {
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-
-__device__ __forceinline__ float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi_of(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-
-// Sum over the 64 lanes; every lane ends with it.
-__device__ __forceinline__ float wave_sum(float x) {
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) x += __shfl_xor(x, m, 64);
-    return x;
-}
-
 struct NormBackArgs {
     const uint16_t *dy, *h, *w;
     const float* rstd;
@@ -55,7 +43,7 @@ __global__ __launch_bounds__(WPR * TEAMS * 64) void rmsnorm_backward_kernel(Norm
         col[k] = (int64_t)(part * HCH + k) * 512 + lane * 8;
         ok[k] = col[k] < a.cols;
         w[k] = make_uint4(0, 0, 0, 0);
-        if (ok[k]) w[k] = *reinterpret_cast<const uint4*>(a.w + col[k]);
+        if (ok[k]) w[k] = ld16(a.w + col[k]);
 #pragma unroll
         for (int i = 0; i < 8; ++i) dw[k][i] = 0.0f;
     }
@@ -70,23 +58,18 @@ __global__ __launch_bounds__(WPR * TEAMS * 64) void rmsnorm_backward_kernel(Norm
             dy[k] = h[k] = dr[k] = make_uint4(0, 0, 0, 0);
             if (live && ok[k]) {
                 const int64_t at = row * a.cols + col[k];
-                dy[k] = *reinterpret_cast<const uint4*>(a.dy + at);
-                h[k] = *reinterpret_cast<const uint4*>(a.h + at);
-                if (a.dres) dr[k] = *reinterpret_cast<const uint4*>(a.dres + at);
+                dy[k] = ld16(a.dy + at);
+                h[k] = ld16(a.h + at);
+                if (a.dres) dr[k] = ld16(a.dres + at);
             }
         }
         const float r = live ? a.rstd[row] : 0.0f;
         float sum = 0.0f;
 #pragma unroll
-        for (int k = 0; k < HCH; ++k) {
-            const uint32_t y[4] = {dy[k].x, dy[k].y, dy[k].z, dy[k].w}, x[4] = {h[k].x, h[k].y, h[k].z, h[k].w},
-                           g[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+        for (int k = 0; k < HCH; ++k)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                sum = fmaf(lo_of(y[i]) * lo_of(g[i]), lo_of(x[i]) * r, sum);
-                sum = fmaf(hi_of(y[i]) * hi_of(g[i]), hi_of(x[i]) * r, sum);
-            }
-        }
+            for (int i = 0; i < 8; ++i)
+                sum = fmaf(elem_of(dy[k], i) * elem_of(w[k], i), elem_of(h[k], i) * r, sum);
         sum = wave_sum(sum);
         if (WPR > 1) {
             if (lane == 0) sums[buf][team][part] = sum;
@@ -98,21 +81,14 @@ __global__ __launch_bounds__(WPR * TEAMS * 64) void rmsnorm_backward_kernel(Norm
         const float mean = sum * inv_cols;
 #pragma unroll
         for (int k = 0; k < HCH; ++k) {
-            const uint32_t y[4] = {dy[k].x, dy[k].y, dy[k].z, dy[k].w}, x[4] = {h[k].x, h[k].y, h[k].z, h[k].w},
-                           g[4] = {w[k].x, w[k].y, w[k].z, w[k].w}, d[4] = {dr[k].x, dr[k].y, dr[k].z, dr[k].w};
-            uint32_t out[4];
+            float out[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float n0 = lo_of(x[i]) * r, n1 = hi_of(x[i]) * r;
-                const float a0 = fmaf(r, fmaf(-n0, mean, lo_of(y[i]) * lo_of(g[i])), lo_of(d[i]));
-                const float a1 = fmaf(r, fmaf(-n1, mean, hi_of(y[i]) * hi_of(g[i])), hi_of(d[i]));
-                const bf16x2 b = {(__bf16)a0, (__bf16)a1};
-                out[i] = __builtin_bit_cast(uint32_t, b);
-                dw[k][2 * i] = fmaf(lo_of(y[i]), n0, dw[k][2 * i]);
-                dw[k][2 * i + 1] = fmaf(hi_of(y[i]), n1, dw[k][2 * i + 1]);
+            for (int i = 0; i < 8; ++i) {
+                const float y = elem_of(dy[k], i), n = elem_of(h[k], i) * r;
+                out[i] = fmaf(r, fmaf(-n, mean, y * elem_of(w[k], i)), elem_of(dr[k], i));
+                dw[k][i] = fmaf(y, n, dw[k][i]);
             }
-            if (live && ok[k])
-                *reinterpret_cast<uint4*>(a.dx + row * a.cols + col[k]) = make_uint4(out[0], out[1], out[2], out[3]);
+            if (live && ok[k]) *reinterpret_cast<uint4*>(a.dx + row * a.cols + col[k]) = bf16x8_rne(out);
         }
     }
     if (!a.part) return;

@@ -22,16 +22,6 @@ namespace jetfp8 {
 
 namespace {
 
-__device__ __forceinline__ uint4 ld16(const uint16_t* p) { return *reinterpret_cast<const uint4*>(p); }
-
-__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
-    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
-}
-__device__ __forceinline__ float elem_of(const uint4& v, int i) {
-    const uint32_t w = word_of(v, i >> 1);
-    return bf16_to_f32((i & 1) ? (w >> 16) : (w & 0xFFFFu));
-}
-
 // Codes of the 8 bf16 values held by a lane (bit patterns in hv), as the 1x128 quantizer forms them: the
 // group's amax from the 16 lanes of the DPP row, then the scale and the codes of the lane's 8 values.
 __device__ __forceinline__ uint2 quantize_lane8(const uint4& hv, float& scale) {
@@ -41,13 +31,6 @@ __device__ __forceinline__ uint2 quantize_lane8(const uint4& hv, float& scale) {
     const GroupScale gs = make_group_scale(bf16_to_f32(row16_max_u32(amax8_bits(hv))));
     scale = gs.s;
     return encode8(f, gs);
-}
-
-// Wave-wide sum of a double (xor butterfly over the 64 lanes; every lane ends with the total).
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-    for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
-    return v;
 }
 
 // fp32 bit pattern of v rounded to odd: the nearest fp32 toward zero, with its last bit set when that is
@@ -63,15 +46,6 @@ __device__ __forceinline__ uint32_t f64_to_f32_odd_bits(double v) {
 }
 
 __device__ __forceinline__ uint32_t f32_bits_to_bf16_rne(uint32_t u) { return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16; }
-
-// Two fp32 values rounded to bf16, nearest even, packed low / high: one V_CVT_PK_BF16_F32.  It equals
-// f32_bits_to_bf16_rne on every finite fp32 pattern (all 2^32 - 2^24 of them compared on gfx950, with the
-// library's denormal mode).
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-typedef float f32x2_t __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ uint32_t bf16x2_rne(float a, float b) {
-    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t){a, b}, bf16x2_t));
-}
 
 // exp(-g) for the SwiGLU fast path: 2^t with t = -g log2(e) split as t_hi + t_lo, where t_hi is the fp32
 // product and t_lo its rounding error (exact by fma) plus the low part of log2(e); then

@@ -11,8 +11,6 @@ namespace jetfp8 {
 
 namespace {
 
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-
 constexpr int kRotaryThreads = 256;
 
 struct RotaryArgs {
@@ -27,21 +25,6 @@ struct RotaryArgs {
     int per_split;                       // heads of one of them
     bool inverse, copy;                  // copy: out is not x, so the other channels are written too
 };
-
-__device__ __forceinline__ float half_of(const uint4& v, int i) {
-    const uint32_t w = i / 2 == 0 ? v.x : i / 2 == 1 ? v.y : i / 2 == 2 ? v.z : v.w;
-    return i % 2 ? __uint_as_float(w & 0xFFFF0000u) : bf16_to_f32(w & 0xFFFFu);
-}
-
-__device__ __forceinline__ uint4 pack(const float (&f)[8]) {
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const bf16x2 b = {(__bf16)f[2 * i], (__bf16)f[2 * i + 1]};
-        w[i] = __builtin_bit_cast(uint32_t, b);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
 
 // A thread block takes a few tokens: first the cosines and sines of their angles into LDS, each formed once for all
 // heads, then the heads in pieces of 16 channels, two 16-byte loads each.  The angle is reduced to a part of a turn in
@@ -77,15 +60,15 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(RotaryArgs a) {
             const int64_t at = (int64_t)(h0 + head) * a.items * 16;
             const uint16_t* from = a.x + (t0 + t) * a.ldx + at;
             uint16_t* to = a.out + (t0 + t) * a.ldo + at;
-            uint4 u = *reinterpret_cast<const uint4*>(from + first), v = *reinterpret_cast<const uint4*>(from + second);
+            uint4 u = ld16(from + first), v = ld16(from + second);
             if (turned) {
                 float p[8], q[8];
                 const float2* cs = turn + t * a.pairs + piece * 8;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float2 z = cs[i];
-                    const float f = INTERLEAVED ? half_of(i < 4 ? u : v, 2 * i % 8) : half_of(u, i);
-                    const float g = INTERLEAVED ? half_of(i < 4 ? u : v, 2 * i % 8 + 1) : half_of(v, i);
+                    const float f = INTERLEAVED ? elem_of(i < 4 ? u : v, 2 * i % 8) : elem_of(u, i);
+                    const float g = INTERLEAVED ? elem_of(i < 4 ? u : v, 2 * i % 8 + 1) : elem_of(v, i);
                     const float l = fmaf(f, z.x, -(g * z.y)), r = fmaf(g, z.x, f * z.y);
                     if (INTERLEAVED) {
                         (i < 4 ? p : q)[2 * i % 8] = l;
@@ -95,8 +78,8 @@ __global__ __launch_bounds__(kRotaryThreads) void rotary_kernel(RotaryArgs a) {
                         q[i] = r;
                     }
                 }
-                u = pack(p);
-                v = pack(q);
+                u = bf16x8_rne(p);
+                v = bf16x8_rne(q);
             }
             *reinterpret_cast<uint4*>(to + first) = u;
             *reinterpret_cast<uint4*>(to + second) = v;
