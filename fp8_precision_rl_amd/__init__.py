@@ -734,8 +734,9 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: Optional
 def rotary(x, positions, freqs, interleaved: bool = False, amplitude: float = 1.0, inverse: bool = False, out=None,
            stream=None):
     """Rotary positions of queries and keys: x bf16 [T, heads, D] (rows may be columns of a wider matrix), positions int32
-    [T], freqs fp64 [pairs] (rotary_frequencies) -> bf16 [T, heads, D], or `out` (x itself for an update in place; rows
-    with a negative position are not written).  inverse: the backward pass."""
+    [T], freqs fp64 [pairs] (rotary_frequencies) -> bf16 [T, heads, D], or `out` (x itself for an update in place).  Rows
+    with a negative position, as kv_positions has them for rows of no unit, are not written: out keeps what it holds, and
+    in a new tensor they are arbitrary.  inverse: the backward pass."""
     T, H, D = x.shape
     dev = x.get_device()
     src = _rows(x, (T, H, D), "x", dev)
@@ -982,8 +983,9 @@ def attention(q, units, block_table, codes, scales, recent, max_new: int, max_se
               quantize: bool = False, return_o: bool = True, workspace=None, stream=None, prefix=None):
     """Causal attention of a step's new tokens, after kv_append: q bf16 [T, Hq, D] -> bf16 [T, Hq, D]; with quantize
     (D = 128) -> (codes [T, Hq * D], scales [Hq, T]) and, with return_o, the bf16 matrix as well.  softmax_scale:
-    1 / sqrt(D) unless given.  Rows that belong to no unit are left unwritten.  prefix: kv_prefix's records; blocks that
-    requests share are then read once for all of them (the same results)."""
+    1 / sqrt(D) unless given.  Rows that belong to no unit are left unwritten (arbitrary in a new tensor).  prefix:
+    kv_prefix's records; blocks that requests share are then read once for all of them where the call is large enough (the
+    same results)."""
     T, Hq, D = q.shape
     H = codes.shape[1]
     dev, name, inputs = _attention_inputs(q, units, block_table, codes, scales, recent, T, Hq, H, D, max_new, max_seq,

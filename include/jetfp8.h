@@ -367,7 +367,11 @@ int jetfp8_kv_prefix(const int32_t* units, int64_t num_units, const int32_t* blo
 
 /* jetfp8_attention, with the blocks that the units of a group share read once for all their rows.  prefix: of
  * jetfp8_kv_prefix for these units and tables (others give unspecified results of the units concerned, within the buffers).
- * The results are those of jetfp8_attention, bit for bit.  workspace: jetfp8_attention_prefix_workspace() bytes. */
+ * The results are those of jetfp8_attention, bit for bit.  Calls that may read little (by num_units and max_seq), and those
+ * with more than 32 rows (new tokens times query heads of a kv head) a unit, are made as jetfp8_attention makes them; where
+ * one span of long contexts is all that is shared, a call without records is faster.  workspace:
+ * jetfp8_attention_prefix_workspace() bytes: as jetfp8_attention, but for 17 to 32 rows a unit a partial result of each 8
+ * blocks, where jetfp8_attention keeps one of each 64 or none. */
 int jetfp8_attention_prefix(const void* q_bf16, int64_t ldq, int64_t tokens, const int32_t* units, int64_t num_units,
                             const int32_t* prefix, const int32_t* block_table, int64_t requests, int64_t max_blocks,
                             const uint8_t* codes, const float* scales, int64_t num_blocks, const void* recent_bf16,
