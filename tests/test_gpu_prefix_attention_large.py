@@ -63,3 +63,12 @@ def test_a_part_of_the_units(jf):
                                workspace=ws)
     same(o[3:9], plain[3:9])
     assert (o[:3] == 7.0).all() and (o[9:] == 7.0).all()
+
+
+@pytest.mark.parametrize("Hq,H,D,new,idle", [(3, 1, 64, 1, 0.0), (16, 2, 64, 1, 0.1), (5, 1, 128, 2, 0.3)])
+def test_more_units_than_threads(jf, Hq, H, D, new, idle):
+    """1500 requests: each thread that counts pieces has several units, and groups begin and end within a thread's."""
+    c = Case([(520, 700), (1100, 499), (100, 2), (2100, 300)], 100, new, Hq, H, D, idle=idle, seed=Hq)
+    assert len(c.units) > 1024
+    pre = c.prefix(jf)
+    same(c.run(jf, pre, c.far()), c.run(jf, None, c.max_seq))
