@@ -100,7 +100,7 @@ int attention_call(const void* q_bf16, int64_t ldq, int64_t tokens, const int32_
 
 extern "C" {
 
-int jetfp8_version(void) { return 500; }
+int jetfp8_version(void) { return 501; }
 
 const char* jetfp8_status_string(int status) {
     switch (status) {
